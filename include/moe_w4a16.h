@@ -601,6 +601,136 @@ moe_status_t moe_ffn_forward_f8(const uint16_t* x, const float* router_logits, i
                                 const float* w2_s, uint16_t* y, int32_t* topk_ids_out, float* topk_w_out,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ---- Ragged products: INT8 (W8A8, per token and channel) and 16-bit expert weights ----------------
+ * [ATOM, 6.1: linears dispatched by quantization type; ATOM, 8.1: expert compute.]  These products take
+ * their groups as expert_offsets int32 [E + 1] on the device (as moe_align writes them; nothing of it is
+ * read by the host): expert e owns the rows [offsets[e], offsets[e + 1]) of R rows in all.  Offsets are
+ * ascending and within [0, R]; the kernels clamp them to that range.  Rows that no expert owns (past
+ * offsets[E]) are not written.  Experts without rows cost nothing.
+ * a_row_of, a_row_div: activation row of row r = a_row_of ? a_row_of[r] / a_row_div : r (with a_row_of the
+ * sorted_ids of moe_align and a_row_div = k, the token of the row).
+ */
+#define MOE_IN_F16 2
+#define MOE_OUT_F16 5
+#define MOE_RAGGED_MAX_DIM (1 << 20) /* largest N and K */
+#define MOE_I8_MAX_K (1 << 17)       /* sums of K products of int8 codes stay exact in int32 */
+
+/*
+ * Rows quantized to int8: s[r] = fp32(max |x[r, :]| / 127), q[r, c] = the integer nearest to x[r, c] / s[r]
+ * (the real quotient; ties to even), in [-127, 127]; value = q * s.  A row whose s is 0 gets codes 0; a row
+ * that holds an infinity or a NaN gets s = NaN and codes 0, so that everything made of it is NaN.  A weight
+ * matrix [N, K] is quantized per channel by the same call (rows = N, or E * N).
+ *   x [rows, K] of in_dtype MOE_IN_BF16, MOE_IN_F16 or MOE_IN_F32; q int8 [rows, K]; s fp32 [rows].
+ * Shapes: 0 <= rows < 2^26, K a positive multiple of 16.  Alignment: x and q 16 bytes, s 4 bytes.
+ */
+moe_status_t moe_i8_quantize(const void* x, int32_t in_dtype, int32_t rows, int32_t K, int8_t* q, float* s, void* stream);
+
+/*
+ * Dense int8 product: G[m, n] = As[m] * Ws[n] * sum_k Aq[m, k] * Wq[n, k], the sum exact in int32, the
+ * scales applied in fp32.  epilogue MOE_EPI_NONE: C = G [M, N]; MOE_EPI_SILU_MUL: C [M, N/2] as in
+ * moe_grouped_gemm_w4a16.  out_dtype MOE_OUT_BF16, MOE_OUT_F16 or (NONE) MOE_OUT_F32.
+ * Shapes: 0 <= M < 2^26, N >= 1 (even for SILU_MUL) and <= MOE_RAGGED_MAX_DIM, K a positive multiple of 16
+ * and <= MOE_I8_MAX_K.  Alignment: Aq, Wq, C 16 bytes; As, Ws 4 bytes.
+ */
+moe_status_t moe_gemm_i8(const int8_t* Aq, const float* As, const int8_t* Wq, const float* Ws, int32_t M, int32_t N,
+                         int32_t K, int32_t epilogue, void* C, int32_t out_dtype, void* stream);
+
+/* Workspace bytes of moe_linear_i8 (host-only, pure; 0 on invalid sizes). */
+size_t moe_linear_i8_workspace_bytes(int32_t T, int32_t K);
+
+/*
+ * Linear layer with int8 weights and activations quantized on the fly [ATOM, 8.2]: moe_i8_quantize of x
+ * [T, K] (in_dtype as there), then moe_gemm_i8 of it.  workspace: at least moe_linear_i8_workspace_bytes(T, K)
+ * bytes, 16-byte aligned.  Other arguments as for moe_gemm_i8.
+ */
+moe_status_t moe_linear_i8(const void* x, int32_t in_dtype, const int8_t* Wq, const float* Ws, int32_t T, int32_t N,
+                           int32_t K, int32_t epilogue, void* y, int32_t out_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Grouped int8 product: for row r of expert e, with activation row a of r,
+ *   G[r, n] = As[a] * Ws[e, n] * sum_k Aq[a, k] * Wq[e, n, k].
+ *   Aq int8 [*, K], As fp32 [*]; Wq int8 [E, N, K], Ws fp32 [E, N]; C [R, N], or [R, N/2] for SILU_MUL.
+ * Shapes: 0 <= R < 2^26, 1 <= E <= MOE_MAX_EXPERTS, N, K, out_dtype and alignment as for moe_gemm_i8.
+ */
+moe_status_t moe_grouped_gemm_i8(const int8_t* Aq, const float* As, const int32_t* a_row_of, int32_t a_row_div,
+                                 const int8_t* Wq, const float* Ws, const int32_t* expert_offsets, int32_t R, int32_t E,
+                                 int32_t N, int32_t K, int32_t epilogue, void* C, int32_t out_dtype, void* stream);
+
+/* Workspace bytes of moe_ffn_forward_i8 (host-only, pure; 0 on invalid sizes). */
+size_t moe_ffn_i8_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k);
+
+/*
+ * The whole INT8 layer [ATOM, 6.1 and 8.1]: route -> permute -> x quantized -> gate_up (SiLU*mul, h in
+ * bf16) -> h quantized -> down (fp32) -> combine, all enqueued on `stream`.
+ *   x bf16 [T, H]; router_logits fp32 [T, E]; w13_q int8 [E, 2I, H], w13_s fp32 [E, 2I], w2_q int8 [E, H, I],
+ *   w2_s fp32 [E, H]; y bf16 [T, H].  Optional routing copies as for moe_ffn_forward.
+ *   workspace: at least moe_ffn_i8_workspace_bytes(T, H, I, E, k) bytes.
+ * Shapes: as moe_ffn_forward, with H and I positive multiples of 16, <= MOE_I8_MAX_K.
+ */
+moe_status_t moe_ffn_forward_i8(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I,
+                                int32_t E, int32_t k, const int8_t* w13_q, const float* w13_s, const int8_t* w2_q,
+                                const float* w2_s, uint16_t* y, int32_t* topk_ids_out, float* topk_w_out,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Grouped product with 16-bit expert weights: for row r of expert e, with activation row a of r,
+ *   G[r, n] = sum_k A[a, k] * W[e, n, k]      (exact products, fp32 accumulation)
+ *   MOE_EPI_NONE: C = G [R, N]; MOE_EPI_SILU_MUL: C [R, N/2] as in moe_grouped_gemm_w4a16.
+ *   A [*, K] and W [E, N, K] both of dtype MOE_IN_BF16 or MOE_IN_F16; out_dtype MOE_OUT_BF16, MOE_OUT_F16 or
+ *   (NONE) MOE_OUT_F32.
+ * Shapes: 0 <= R < 2^26, 1 <= E <= MOE_MAX_EXPERTS, N >= 1 (even for SILU_MUL), K a positive multiple of 8,
+ *         N and K <= MOE_RAGGED_MAX_DIM.  Alignment: A, W, C 16 bytes; a_row_of, expert_offsets 4 bytes.
+ */
+moe_status_t moe_grouped_gemm_w16(const uint16_t* A, const int32_t* a_row_of, int32_t a_row_div, const uint16_t* W,
+                                  int32_t dtype, const int32_t* expert_offsets, int32_t R, int32_t E, int32_t N,
+                                  int32_t K, int32_t epilogue, void* C, int32_t out_dtype, void* stream);
+
+/*
+ * Gradient of moe_grouped_gemm_w16 (NONE) with respect to its rows: dA[r, k] = sum_n dC[r, n] * W[e, n, k] for row r of
+ * expert e, dC [R, N] of dtype, dA [R, K] of out_dtype.  Rows that share an activation row are added by
+ * moe_combine (fp32 dA as its O, weights 1).  N and K multiples of 8; otherwise as moe_grouped_gemm_w16.
+ */
+moe_status_t moe_grouped_gemm_w16_dx(const uint16_t* dC, const uint16_t* W, int32_t dtype, const int32_t* expert_offsets,
+                                     int32_t R, int32_t E, int32_t N, int32_t K, void* dA, int32_t out_dtype,
+                                     void* stream);
+
+/*
+ * Gradient of moe_grouped_gemm_w16 (NONE) with respect to its weights:
+ *   dW[e, n, k] = sum over the rows r of expert e of dC[r, n] * A[a(r), k],
+ * dC [R, N] and A [*, K] of dtype, dW [E, N, K] of out_dtype, every element written (zeros for an expert
+ * without rows, also when R is 0).  N and K multiples of 8; otherwise as moe_grouped_gemm_w16.
+ */
+moe_status_t moe_grouped_gemm_w16_dw(const uint16_t* dC, const uint16_t* A, const int32_t* a_row_of, int32_t a_row_div,
+                                     int32_t dtype, const int32_t* expert_offsets, int32_t R, int32_t E, int32_t N,
+                                     int32_t K, void* dW, int32_t out_dtype, void* stream);
+
+/*
+ * SiLU*mul of a stored gate_up result G [R, 2I] (columns [0, I) the gate g, [I, 2I) the up projection u), for
+ * training, where the backward pass needs G: h = silu(g) * u [R, I]; and its gradient: with s = 1 / (1 + exp(-g)),
+ *   dG = [dh * u * s * (1 + g * (1 - s)), dh * g * s]  [R, 2I].
+ * All of dtype MOE_IN_BF16 or MOE_IN_F16, arithmetic in fp32, one rounding.  An infinite g has no defined
+ * result.  dG may be G.  Shapes: 0 <= R < 2^26, I a positive multiple of 8 and <= MOE_RAGGED_MAX_DIM.
+ * Alignment: 16 bytes.
+ */
+moe_status_t moe_silu_mul(const uint16_t* G, int32_t dtype, int32_t R, int32_t I, uint16_t* h, void* stream);
+moe_status_t moe_silu_mul_grad(const uint16_t* G, const uint16_t* dh, int32_t dtype, int32_t R, int32_t I, uint16_t* dG,
+                               void* stream);
+
+/* Workspace bytes of moe_ffn_forward_w16 (host-only, pure; 0 on invalid sizes). */
+size_t moe_ffn_w16_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k);
+
+/*
+ * The whole layer with bf16 weights: route -> permute -> gate_up (SiLU*mul, h in bf16) -> down (fp32) ->
+ * combine, all enqueued on `stream`.  x bf16 [T, H]; w13 bf16 [E, 2I, H]; w2 bf16 [E, H, I]; y bf16 [T, H].
+ * workspace: at least moe_ffn_w16_workspace_bytes(T, H, I, E, k) bytes.  Shapes as moe_ffn_forward_i8.
+ */
+moe_status_t moe_ffn_forward_w16(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I,
+                                 int32_t E, int32_t k, const uint16_t* w13, const uint16_t* w2, uint16_t* y,
+                                 int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
 #ifdef __cplusplus
 }
 #endif

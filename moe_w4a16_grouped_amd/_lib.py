@@ -34,6 +34,8 @@ MOE_IN_F32 = 1
 MOE_OUT_F8 = 2
 MOE_OUT_F16E = 3
 MOE_OUT_H16 = 4
+MOE_IN_F16 = 2
+MOE_OUT_F16 = 5
 
 _lib = None
 
@@ -96,6 +98,20 @@ def load() -> ctypes.CDLL:
         "moe_ffn_block_m": ([I32, I32, I32, I32], I32),
         "moe_ffn_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
         "moe_ffn_forward": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, I32, P, P, P, P, SZ, P], I32),
+        "moe_i8_quantize": ([P, I32, I32, I32, P, P, P], I32),
+        "moe_gemm_i8": ([P, P, P, P, I32, I32, I32, I32, P, I32, P], I32),
+        "moe_linear_i8_workspace_bytes": ([I32, I32], SZ),
+        "moe_linear_i8": ([P, I32, P, P, I32, I32, I32, I32, P, I32, P, SZ, P], I32),
+        "moe_grouped_gemm_i8": ([P, P, P, I32, P, P, P, I32, I32, I32, I32, I32, P, I32, P], I32),
+        "moe_ffn_i8_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+        "moe_ffn_forward_i8": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P], I32),
+        "moe_grouped_gemm_w16": ([P, P, I32, P, I32, P, I32, I32, I32, I32, I32, P, I32, P], I32),
+        "moe_grouped_gemm_w16_dx": ([P, P, I32, P, I32, I32, I32, I32, P, I32, P], I32),
+        "moe_grouped_gemm_w16_dw": ([P, P, P, I32, I32, P, I32, I32, I32, I32, P, I32, P], I32),
+        "moe_silu_mul": ([P, I32, I32, I32, P, P], I32),
+        "moe_silu_mul_grad": ([P, P, I32, I32, I32, P, P], I32),
+        "moe_ffn_w16_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+        "moe_ffn_forward_w16": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P], I32),
         "moe_ffn_noalloc_scratch_bytes": ([], SZ),
         "moe_ffn_forward_noalloc": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, I32, P, P, P, P], I32),
     }
@@ -116,7 +132,10 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_last_error", "moe_route
             "moe_ffn_f8_block_m", "moe_ffn_f8_workspace_bytes", "moe_ffn_forward_f8", "moe_mx8_quantize",
             "moe_mx8_quantize_tiles", "moe_grouped_gemm_w4a8", "moe_ffn_w4a8_block_m", "moe_ffn_w4a8_workspace_bytes",
             "moe_ffn_forward_w4a8", "moe_ffn_noalloc_scratch_bytes", "moe_ffn_forward_noalloc", "moe_x_to_f16",
-            "moe_grouped_gemm_w4f16")
+            "moe_grouped_gemm_w4f16", "moe_i8_quantize", "moe_gemm_i8", "moe_linear_i8_workspace_bytes", "moe_linear_i8",
+            "moe_grouped_gemm_i8", "moe_ffn_i8_workspace_bytes", "moe_ffn_forward_i8", "moe_grouped_gemm_w16",
+            "moe_grouped_gemm_w16_dx", "moe_grouped_gemm_w16_dw", "moe_silu_mul", "moe_silu_mul_grad",
+            "moe_ffn_w16_workspace_bytes", "moe_ffn_forward_w16")
 
 
 def _check(status: int):
@@ -653,3 +672,277 @@ def moe_ffn_forward_f8(x, router_logits, w13_q, w13_s, w2_q, w2_s, k: int, y=Non
                                      workspace.numel() * workspace.element_size(), _stream(stream)))
     return y
 
+
+# ---- ragged products: INT8 (W8A8, per token and channel) and 16-bit expert weights ---------------------
+
+_IN = {torch.bfloat16: MOE_IN_BF16, torch.float16: MOE_IN_F16, torch.float32: MOE_IN_F32}
+_OUT = {torch.bfloat16: MOE_OUT_BF16, torch.float16: MOE_OUT_F16, torch.float32: MOE_OUT_F32}
+_OUT_DTYPE = {v: k for k, v in _OUT.items()}
+_W16 = (torch.bfloat16, torch.float16)
+_I8, _F32, _INT32, _U8 = (torch.int8,), (torch.float32,), (torch.int32,), (torch.uint8,)
+_ACT = tuple(_IN)
+
+
+def _need(t, dtypes, shape, name, dev=None):
+    """A contiguous GPU tensor of one of the dtypes and of this shape (None = any size), on dev."""
+    d = t.device
+    if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous() or (dev is not None and d != dev):
+        raise ValueError(f"{name} must be a contiguous {' or '.join(str(x) for x in dtypes)} CUDA tensor"
+                         f"{'' if dev is None else f' on {dev}'} (got {t.dtype}, {d})")
+    s = t.shape
+    if len(s) != len(shape) or any(w is not None and g != w for g, w in zip(s, shape)):
+        raise ValueError(f"{name} must have the shape {shape} (got {tuple(s)})")
+    return s
+
+
+def _call(fn, dev, stream, made, *args):
+    """Calls a C entry point on the tensors' device and stream.  Tensors made by the wrapper (outputs,
+    workspaces) belong to the current stream: their memory is kept until another given stream is done."""
+    index = dev.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        if stream.device != dev:
+            raise ValueError(f"stream is of {stream.device}, the tensors of {dev}")
+        raw = stream.cuda_stream
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != MOE_OK:
+        _check(status)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out(made, shape, out_dtype, dev, name):
+    """The caller's output, checked, or a new one of out_dtype; a call's out_dtype defaults to bf16."""
+    dt = _OUT_DTYPE.get(out_dtype)
+    if dt is None:
+        raise ValueError(f"unknown out_dtype {out_dtype}")
+    if made is None:
+        return torch.empty(shape, dtype=dt, device=dev)
+    _need(made, (dt,), shape, name, dev)
+    return made
+
+
+def _cols(N, epilogue):
+    if epilogue == MOE_EPI_SILU_MUL and N % 2:
+        raise ValueError(f"SILU_MUL needs an even N (got {N})")
+    return N // 2 if epilogue == MOE_EPI_SILU_MUL else N
+
+
+def _groups(A, R, a_row_of, a_row_div, expert_offsets, E, dev):
+    """Checks the description of the groups on the host's side (sizes; the contents stay on the device)."""
+    _need(expert_offsets, _INT32, (E + 1,), "expert_offsets", dev)
+    if a_row_of is None:
+        if A.shape[0] < R:
+            raise ValueError(f"A has {A.shape[0]} rows, the groups {R}")
+    else:
+        if a_row_of.dim() != 1 or a_row_of.shape[0] < R:
+            raise ValueError(f"a_row_of must hold {R} indexes (got {tuple(a_row_of.shape)})")
+        _need(a_row_of, _INT32, (None,), "a_row_of", dev)
+
+
+def moe_i8_quantize(x, q=None, s=None, stream=None):
+    """x bf16, fp16 or fp32 [rows, K] -> (codes int8 [rows, K], scales fp32 [rows])."""
+    rows, K = _need(x, _ACT, (None, None), "x")
+    dev = x.device
+    if q is None:
+        q = torch.empty((rows, K), dtype=torch.int8, device=dev)
+    else:
+        _need(q, _I8, (rows, K), "q", dev)
+    if s is None:
+        s = torch.empty((rows,), dtype=torch.float32, device=dev)
+    else:
+        _need(s, _F32, (rows,), "s", dev)
+    _call(load().moe_i8_quantize, dev, stream, (q, s), x.data_ptr(), _IN[x.dtype], rows, K, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def moe_gemm_i8(Aq, As, Wq, Ws, epilogue: int = MOE_EPI_NONE, out_dtype: int = MOE_OUT_BF16, C=None, stream=None):
+    """Aq int8 [M, K], As fp32 [M], Wq int8 [N, K], Ws fp32 [N] -> C [M, N] ([M, N/2] for SILU_MUL)."""
+    M, K = _need(Aq, _I8, (None, None), "Aq")
+    dev = Aq.device
+    _need(As, _F32, (M,), "As", dev)
+    N, _ = _need(Wq, _I8, (None, K), "Wq", dev)
+    _need(Ws, _F32, (N,), "Ws", dev)
+    C = _out(C, (M, _cols(N, epilogue)), out_dtype, dev, "C")
+    _call(load().moe_gemm_i8, dev, stream, (C,), Aq.data_ptr(), As.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), M, N, K,
+          epilogue, C.data_ptr(), out_dtype)
+    return C
+
+
+def moe_linear_i8_workspace_bytes(T: int, K: int) -> int:
+    return int(load().moe_linear_i8_workspace_bytes(T, K))
+
+
+def moe_linear_i8(x, Wq, Ws, epilogue: int = MOE_EPI_NONE, out_dtype: int = MOE_OUT_BF16, y=None, workspace=None,
+                  stream=None):
+    """x bf16, fp16 or fp32 [T, K], quantized on the fly, Wq int8 [N, K], Ws fp32 [N] -> y [T, N] ([T, N/2] for
+    SILU_MUL)."""
+    T, K = _need(x, _ACT, (None, None), "x")
+    dev = x.device
+    N, _ = _need(Wq, _I8, (None, K), "Wq", dev)
+    _need(Ws, _F32, (N,), "Ws", dev)
+    y = _out(y, (T, _cols(N, epilogue)), out_dtype, dev, "y")
+    if workspace is None:
+        workspace = torch.empty(max(moe_linear_i8_workspace_bytes(T, K), 256), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, _U8, (None,), "workspace", dev)
+    _call(load().moe_linear_i8, dev, stream, (y, workspace), x.data_ptr(), _IN[x.dtype], Wq.data_ptr(), Ws.data_ptr(), T, N,
+          K, epilogue, y.data_ptr(), out_dtype, workspace.data_ptr(), workspace.numel())
+    return y
+
+
+def moe_grouped_gemm_i8(Aq, As, a_row_of, a_row_div: int, Wq, Ws, expert_offsets, out_rows: int,
+                        epilogue: int = MOE_EPI_NONE, out_dtype: int = MOE_OUT_BF16, C=None, stream=None):
+    """Grouped int8 product over expert_offsets int32 [E + 1]: Aq int8 [*, K], As fp32 [*], Wq int8 [E, N, K],
+    Ws fp32 [E, N] -> C [out_rows, N] ([out_rows, N/2] for SILU_MUL)."""
+    rows, K = _need(Aq, _I8, (None, None), "Aq")
+    dev = Aq.device
+    _need(As, _F32, (rows,), "As", dev)
+    E, N, _ = _need(Wq, _I8, (None, None, K), "Wq", dev)
+    _need(Ws, _F32, (E, N), "Ws", dev)
+    _groups(Aq, out_rows, a_row_of, a_row_div, expert_offsets, E, dev)
+    C = _out(C, (out_rows, _cols(N, epilogue)), out_dtype, dev, "C")
+    _call(load().moe_grouped_gemm_i8, dev, stream, (C,), Aq.data_ptr(), As.data_ptr(), _ptr(a_row_of), a_row_div,
+          Wq.data_ptr(), Ws.data_ptr(), expert_offsets.data_ptr(), out_rows, E, N, K, epilogue, C.data_ptr(), out_dtype)
+    return C
+
+
+def moe_ffn_i8_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
+    return int(load().moe_ffn_i8_workspace_bytes(T, H, I, E, k))
+
+
+def _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace, need_bytes):
+    """Checks a layer's activations and optional buffers, makes y and the workspace where none is given."""
+    dev, T = x.device, x.shape[0]
+    _need(router_logits, _F32, (T, E), "router_logits", dev)
+    if topk_ids_out is not None:
+        _need(topk_ids_out, _INT32, (T, k), "topk_ids_out", dev)
+    if topk_w_out is not None:
+        _need(topk_w_out, _F32, (T, k), "topk_w_out", dev)
+    y = _out(y, (T, H), MOE_OUT_BF16, dev, "y")
+    if workspace is None:
+        workspace = torch.empty(max(need_bytes, 256), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, _U8, (None,), "workspace", dev)
+    return y, workspace
+
+
+def moe_ffn_forward_i8(x, router_logits, w13_q, w13_s, w2_q, w2_s, k: int, y=None, topk_ids_out=None, topk_w_out=None,
+                       workspace=None, stream=None):
+    """Whole INT8 layer: x bf16 [T, H], logits fp32 [T, E], w13_q int8 [E, 2I, H] with scales fp32 [E, 2I], w2_q
+    int8 [E, H, I] with scales fp32 [E, H] -> y bf16 [T, H]."""
+    T, H = _need(x, (torch.bfloat16,), (None, None), "x")
+    dev = x.device
+    E, N13, _ = _need(w13_q, _I8, (None, None, H), "w13_q", dev)
+    I = N13 // 2
+    _need(w13_s, _F32, (E, 2 * I), "w13_s", dev)
+    _need(w2_q, _I8, (E, H, I), "w2_q", dev)
+    _need(w2_s, _F32, (E, H), "w2_s", dev)
+    y, workspace = _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
+                             moe_ffn_i8_workspace_bytes(T, H, I, E, k))
+    _call(load().moe_ffn_forward_i8, dev, stream, (y, workspace), x.data_ptr(), router_logits.data_ptr(), T, H, I, E, k,
+          w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(), y.data_ptr(), _ptr(topk_ids_out),
+          _ptr(topk_w_out), workspace.data_ptr(), workspace.numel())
+    return y
+
+
+def moe_grouped_gemm_w16(A, a_row_of, a_row_div: int, W, expert_offsets, out_rows: int, epilogue: int = MOE_EPI_NONE,
+                         out_dtype: int = None, C=None, stream=None):
+    """Grouped product over expert_offsets int32 [E + 1]: A [*, K] and W [E, N, K], both bf16 or both fp16 -> C
+    [out_rows, N] ([out_rows, N/2] for SILU_MUL) of out_dtype (default: the operands' type)."""
+    _, K = _need(A, _W16, (None, None), "A")
+    dev, dt = A.device, A.dtype
+    E, N, _ = _need(W, (dt,), (None, None, K), "W", dev)
+    _groups(A, out_rows, a_row_of, a_row_div, expert_offsets, E, dev)
+    out_dtype = _OUT[dt] if out_dtype is None else out_dtype
+    C = _out(C, (out_rows, _cols(N, epilogue)), out_dtype, dev, "C")
+    _call(load().moe_grouped_gemm_w16, dev, stream, (C,), A.data_ptr(), _ptr(a_row_of), a_row_div, W.data_ptr(), _IN[dt],
+          expert_offsets.data_ptr(), out_rows, E, N, K, epilogue, C.data_ptr(), out_dtype)
+    return C
+
+
+def moe_grouped_gemm_w16_dx(dC, W, expert_offsets, out_dtype: int = None, dA=None, stream=None):
+    """Row gradients of moe_grouped_gemm_w16: dC [R, N] and W [E, N, K] of one type -> dA [R, K] of out_dtype
+    (default: the operands' type)."""
+    R, N = _need(dC, _W16, (None, None), "dC")
+    dev, dt = dC.device, dC.dtype
+    E, _, K = _need(W, (dt,), (None, N, None), "W", dev)
+    _need(expert_offsets, _INT32, (E + 1,), "expert_offsets", dev)
+    out_dtype = _OUT[dt] if out_dtype is None else out_dtype
+    dA = _out(dA, (R, K), out_dtype, dev, "dA")
+    _call(load().moe_grouped_gemm_w16_dx, dev, stream, (dA,), dC.data_ptr(), W.data_ptr(), _IN[dt],
+          expert_offsets.data_ptr(), R, E, N, K, dA.data_ptr(), out_dtype)
+    return dA
+
+
+def moe_grouped_gemm_w16_dw(dC, A, a_row_of, a_row_div: int, expert_offsets, out_dtype: int = None, dW=None, stream=None):
+    """Weight gradients of moe_grouped_gemm_w16: dC [R, N] and A [*, K] of one type -> dW [E, N, K] of out_dtype
+    (default: the operands' type); zeros for experts without rows."""
+    R, N = _need(dC, _W16, (None, None), "dC")
+    dev, dt = dC.device, dC.dtype
+    _, K = _need(A, (dt,), (None, None), "A", dev)
+    if expert_offsets.dim() != 1 or expert_offsets.shape[0] < 2:
+        raise ValueError(f"expert_offsets must have the shape (E + 1,) (got {tuple(expert_offsets.shape)})")
+    E = expert_offsets.shape[0] - 1
+    _groups(A, R, a_row_of, a_row_div, expert_offsets, E, dev)
+    out_dtype = _OUT[dt] if out_dtype is None else out_dtype
+    dW = _out(dW, (E, N, K), out_dtype, dev, "dW")
+    _call(load().moe_grouped_gemm_w16_dw, dev, stream, (dW,), dC.data_ptr(), A.data_ptr(), _ptr(a_row_of), a_row_div,
+          _IN[dt], expert_offsets.data_ptr(), R, E, N, K, dW.data_ptr(), out_dtype)
+    return dW
+
+
+def _silu_shape(G):
+    R, C = _need(G, _W16, (None, None), "G")
+    if C % 2:
+        raise ValueError(f"G must have an even number of columns (got {C})")
+    return R, C // 2
+
+
+def moe_silu_mul(G, h=None, stream=None):
+    """G [R, 2I] (gate, up) bf16 or fp16 -> h = silu(gate) * up [R, I] of its type."""
+    R, I = _silu_shape(G)
+    h = _out(h, (R, I), _OUT[G.dtype], G.device, "h")
+    _call(load().moe_silu_mul, G.device, stream, (h,), G.data_ptr(), _IN[G.dtype], R, I, h.data_ptr())
+    return h
+
+
+def moe_silu_mul_grad(G, dh, dG=None, stream=None):
+    """Gradient of moe_silu_mul: G [R, 2I], dh [R, I] -> dG [R, 2I]."""
+    R, I = _silu_shape(G)
+    _need(dh, (G.dtype,), (R, I), "dh", G.device)
+    dG = _out(dG, (R, 2 * I), _OUT[G.dtype], G.device, "dG")
+    _call(load().moe_silu_mul_grad, G.device, stream, (dG,), G.data_ptr(), dh.data_ptr(), _IN[G.dtype], R, I, dG.data_ptr())
+    return dG
+
+
+def moe_ffn_w16_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
+    return int(load().moe_ffn_w16_workspace_bytes(T, H, I, E, k))
+
+
+def moe_ffn_forward_w16(x, router_logits, w13, w2, k: int, y=None, topk_ids_out=None, topk_w_out=None, workspace=None,
+                        stream=None):
+    """Whole layer with bf16 weights: x bf16 [T, H], logits fp32 [T, E], w13 bf16 [E, 2I, H], w2 bf16 [E, H, I] -> y
+    bf16 [T, H]."""
+    bf16 = (torch.bfloat16,)
+    T, H = _need(x, bf16, (None, None), "x")
+    dev = x.device
+    E, N13, _ = _need(w13, bf16, (None, None, H), "w13", dev)
+    I = N13 // 2
+    _need(w2, bf16, (E, H, I), "w2", dev)
+    y, workspace = _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
+                             moe_ffn_w16_workspace_bytes(T, H, I, E, k))
+    _call(load().moe_ffn_forward_w16, dev, stream, (y, workspace), x.data_ptr(), router_logits.data_ptr(), T, H, I, E, k,
+          w13.data_ptr(), w2.data_ptr(), y.data_ptr(), _ptr(topk_ids_out), _ptr(topk_w_out), workspace.data_ptr(),
+          workspace.numel())
+    return y

@@ -475,6 +475,156 @@ bool f8_dims_ok(int32_t H, int32_t I) {
   return H >= 128 && I >= 128 && H % 128 == 0 && I % 128 == 0 && H <= kF8MaxK && I <= kF8MaxK;
 }
 
+// ---- ragged products (int8 and 16-bit weights) -----------------------------------------------------
+bool ragged_out_ok(int32_t out) { return out == MOE_OUT_BF16 || out == MOE_OUT_F16 || out == MOE_OUT_F32; }
+
+// Shape checks shared by the ragged products: rows R, experts E, weights [E, N, K] whose rows hold a
+// whole number of 16-byte chunks (K a multiple of kq elements; N a multiple of nq where rows of N elements are
+// loaded).
+moe_status_t check_ragged(int64_t R, int32_t E, int32_t N, int32_t K, int32_t nq, int32_t kq, const char* who) {
+  if (R < 0 || E < 1 || N < 1 || K < 1) return fail(MOE_ERR_INVALID_ARG, "%s: need R >= 0 and E, N, K >= 1", who);
+  if (E > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: E=%d exceeds %d", who, E, MOE_MAX_EXPERTS);
+  if (R >= kMaxRows) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: R=%lld must be < 2^26", who, (long long)R);
+  if (N % nq != 0 || K % kq != 0)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: N=%d must be a multiple of %d and K=%d of %d", who, N, nq, K, kq);
+  if (N > MOE_RAGGED_MAX_DIM || K > MOE_RAGGED_MAX_DIM)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: N=%d and K=%d must not exceed %d", who, N, K, MOE_RAGGED_MAX_DIM);
+  return MOE_OK;
+}
+
+moe_status_t check_ragged_epilogue(int32_t epilogue, int32_t out_dtype, int32_t N, const char* who) {
+  if (epilogue != MOE_EPI_NONE && epilogue != MOE_EPI_SILU_MUL) return fail(MOE_ERR_INVALID_ARG, "%s: unknown epilogue %d", who, epilogue);
+  if (!ragged_out_ok(out_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown out_dtype %d", who, out_dtype);
+  if (epilogue == MOE_EPI_SILU_MUL && (N % 2 != 0 || out_dtype == MOE_OUT_F32))
+    return fail(MOE_ERR_INVALID_ARG, "%s: SILU_MUL needs an even N and a 16-bit output", who);
+  return MOE_OK;
+}
+
+moe_status_t check_w16_dtype(int32_t dtype, const char* who) {
+  if (dtype != MOE_IN_BF16 && dtype != MOE_IN_F16) return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype %d", who, dtype);
+  return MOE_OK;
+}
+
+// Shape and pointer checks of one int8 product (offsets NULL: the dense one).
+moe_status_t check_i8_gemm(const int8_t* Aq, const float* As, const int8_t* Wq, const float* Ws, int64_t R, int32_t E,
+                           int32_t N, int32_t K, int32_t epilogue, const void* C, int32_t out_dtype, const char* who) {
+  if (moe_status_t st = check_ragged(R, E, N, K, 1, 16, who)) return st;
+  if (K > MOE_I8_MAX_K) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: K=%d exceeds %d (int32 sums)", who, K, MOE_I8_MAX_K);
+  if (moe_status_t st = check_ragged_epilogue(epilogue, out_dtype, N, who)) return st;
+  if (R == 0) return MOE_OK;
+  if (!Aq || !As || !Wq || !Ws || !C) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(Aq) || !aligned16(Wq) || !aligned16(C) || !aligned4(As) || !aligned4(Ws))
+    return fail(MOE_ERR_MISALIGNED, "%s: Aq, Wq, C need 16-byte alignment, As, Ws 4-byte", who);
+  return MOE_OK;
+}
+
+moe_status_t check_groups(const int32_t* a_row_of, int32_t a_row_div, const int32_t* offsets, const char* who) {
+  if (a_row_of && a_row_div < 1) return fail(MOE_ERR_INVALID_ARG, "%s: a_row_div must be >= 1", who);
+  if (!offsets) return fail(MOE_ERR_INVALID_ARG, "%s: NULL expert_offsets", who);
+  if (!aligned4(offsets) || (a_row_of && !aligned4(a_row_of)))
+    return fail(MOE_ERR_MISALIGNED, "%s: a_row_of and expert_offsets need 4-byte alignment", who);
+  return MOE_OK;
+}
+
+// Workspace of the layers on ragged products: the routing regions of ffn_layout, then (int8) x quantized
+// (codes [T, H], scales [T]), h in bf16 [R, I], (int8) h quantized (codes [R, I], scales [R]) and O in fp32
+// [R, H].
+struct RaggedFfnLayout {
+  FfnLayout L;
+  size_t xq, xs, h, hq, hs, o, total;
+};
+
+RaggedFfnLayout ragged_ffn_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool i8) {
+  RaggedFfnLayout M{};
+  M.L = ffn_layout(T, H, I, E, k, false);
+  const int64_t R = T * k;
+  size_t off = M.L.h;
+  auto take = [&](size_t bytes) { size_t at = off; off += up256(bytes); return at; };
+  M.xq = take(i8 ? (size_t)T * H : 0);
+  M.xs = take(i8 ? (size_t)T * 4 : 0);
+  M.h = take((size_t)R * I * 2);
+  M.hq = take(i8 ? (size_t)R * I : 0);
+  M.hs = take(i8 ? (size_t)R * 4 : 0);
+  M.o = take((size_t)R * H * 4);
+  M.total = off;
+  return M;
+}
+
+bool ragged_ffn_dims_ok(int32_t H, int32_t I) {
+  return H >= 16 && I >= 16 && H % 16 == 0 && I % 16 == 0 && H <= MOE_I8_MAX_K && I <= MOE_I8_MAX_K;
+}
+
+// The layer on int8 (w_s set) or bf16 weights: route and permute, gate_up with SiLU*mul, down, combine.
+moe_status_t run_ragged_ffn(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E,
+                            int32_t k, const void* w13, const float* w13_s, const void* w2, const float* w2_s,
+                            uint16_t* y, int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                            size_t workspace_bytes, bool i8, const char* who, hipStream_t s) {
+  if (moe_status_t st = check_routing_shape(T, E, k)) return st;
+  if (!ragged_ffn_dims_ok(H, I))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H=%d and I=%d must be positive multiples of 16, <= %d", who, H, I,
+                MOE_I8_MAX_K);
+  if (T == 0) return ok();
+  if (!x || !router_logits || !w13 || !w2 || (i8 && (!w13_s || !w2_s)) || !y || !workspace)
+    return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(y) || !aligned16(workspace) ||
+      !aligned4(w13_s) || !aligned4(w2_s) || !aligned4(router_logits) || (topk_ids_out && !aligned4(topk_ids_out)) ||
+      (topk_w_out && !aligned4(topk_w_out)))
+    return fail(MOE_ERR_MISALIGNED, "%s: x, weights, y and workspace need 16-byte alignment", who);
+  const RaggedFfnLayout M = ragged_ffn_layout(T, H, I, E, k, i8);
+  if (workspace_bytes < M.total)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu B < required %zu B", who, workspace_bytes, M.total);
+  const FfnLayout& L = M.L;
+  char* ws = static_cast<char*>(workspace);
+  int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
+  float* w = topk_w_out ? topk_w_out : reinterpret_cast<float*>(ws + L.w);
+  int32_t* counts = reinterpret_cast<int32_t*>(ws + L.counts);
+  int32_t* offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
+  int32_t* sorted = reinterpret_cast<int32_t*>(ws + L.sorted);
+  int32_t* inv = reinterpret_cast<int32_t*>(ws + L.inv);
+  int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+  int32_t* ntiles = reinterpret_cast<int32_t*>(ws + L.ntiles);
+  int8_t* xq = reinterpret_cast<int8_t*>(ws + M.xq);
+  float* xs = reinterpret_cast<float*>(ws + M.xs);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + M.h);
+  int8_t* hq = reinterpret_cast<int8_t*>(ws + M.hq);
+  float* hs = reinterpret_cast<float*>(ws + M.hs);
+  float* o = reinterpret_cast<float*>(ws + M.o);
+  const int R = T * k;
+  hipError_t e;
+  if (moe::route_align_fused_fits(T, E, k)) {
+    e = moe::launch_route_align_small(router_logits, T, E, k, L.block_m, ids, w, counts, offsets, sorted, inv,
+                                      tiles, L.max_tiles, ntiles, s);
+    if (e != hipSuccess) return hip_status(e, "route+align launch");
+  } else {
+    e = moe::launch_route_topk(router_logits, T, E, k, ids, w, s);
+    if (e != hipSuccess) return hip_status(e, "route launch");
+    e = moe::launch_align(ids, R, E, L.block_m, counts, offsets, sorted, inv, tiles, L.max_tiles, ntiles,
+                          ws + L.align_ws, s);
+    if (e != hipSuccess) return hip_status(e, "align launch");
+  }
+  moe::RaggedArgs g1{x, nullptr, sorted, k, w13, w13_s, offsets, R, E, 2 * I, H, h, MOE_OUT_BF16};
+  moe::RaggedArgs g2{h, nullptr, nullptr, 1, w2, w2_s, offsets, R, E, H, I, o, MOE_OUT_F32};
+  if (i8) {
+    e = moe::launch_i8_quant(x, MOE_IN_BF16, T, H, xq, xs, s);
+    if (e != hipSuccess) return hip_status(e, "x quantization launch");
+    g1.A = xq;
+    g1.As = xs;
+    e = moe::launch_ragged_i8(g1, MOE_EPI_SILU_MUL, s);
+    if (e != hipSuccess) return hip_status(e, "gate_up launch");
+    e = moe::launch_i8_quant(h, MOE_IN_BF16, R, I, hq, hs, s);
+    if (e != hipSuccess) return hip_status(e, "h quantization launch");
+    g2.A = hq;
+    g2.As = hs;
+    e = moe::launch_ragged_i8(g2, MOE_EPI_NONE, s);
+  } else {
+    e = moe::launch_ragged_w16(g1, 0, false, MOE_EPI_SILU_MUL, s);
+    if (e != hipSuccess) return hip_status(e, "gate_up launch");
+    e = moe::launch_ragged_w16(g2, 0, false, MOE_EPI_NONE, s);
+  }
+  if (e != hipSuccess) return hip_status(e, "down launch");
+  return hip_status(moe::launch_combine(o, nullptr, inv, w, nullptr, -1, T, k, H, y, s), "combine launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -1345,6 +1495,161 @@ moe_status_t moe_ffn_forward_f8(const uint16_t* x, const float* router_logits, i
   e = moe::launch_grouped_gemm_f8(g2, L.block_m, s);
   if (e != hipSuccess) return hip_status(e, "down launch");
   return hip_status(moe::launch_combine(o, oside, inv, w, nullptr, -1, T, k, H, y, s), "combine launch");
+}
+
+moe_status_t moe_i8_quantize(const void* x, int32_t in_dtype, int32_t rows, int32_t K, int8_t* q, float* s, void* stream) {
+  if (rows < 0 || K < 16 || K % 16 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "moe_i8_quantize: need rows >= 0 and K a positive multiple of 16");
+  if (in_dtype != MOE_IN_BF16 && in_dtype != MOE_IN_F16 && in_dtype != MOE_IN_F32)
+    return fail(MOE_ERR_INVALID_ARG, "moe_i8_quantize: unknown in_dtype %d", in_dtype);
+  if ((int64_t)rows >= kMaxRows || K > MOE_RAGGED_MAX_DIM)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "moe_i8_quantize: rows=%d must be < 2^26 and K=%d <= %d", rows, K, MOE_RAGGED_MAX_DIM);
+  if (rows == 0) return ok();
+  if (!x || !q || !s) return fail(MOE_ERR_INVALID_ARG, "moe_i8_quantize: NULL pointer");
+  if (!aligned16(x) || !aligned16(q) || !aligned4(s))
+    return fail(MOE_ERR_MISALIGNED, "moe_i8_quantize: x and q need 16-byte alignment, s 4-byte");
+  return hip_status(moe::launch_i8_quant(x, in_dtype, rows, K, q, s, (hipStream_t)stream), "moe_i8_quantize launch");
+}
+
+moe_status_t moe_gemm_i8(const int8_t* Aq, const float* As, const int8_t* Wq, const float* Ws, int32_t M, int32_t N,
+                         int32_t K, int32_t epilogue, void* C, int32_t out_dtype, void* stream) {
+  if (moe_status_t st = check_i8_gemm(Aq, As, Wq, Ws, M, 1, N, K, epilogue, C, out_dtype, "moe_gemm_i8")) return st;
+  if (M == 0) return ok();
+  moe::RaggedArgs a{Aq, As, nullptr, 1, Wq, Ws, nullptr, M, 1, N, K, C, out_dtype};
+  return hip_status(moe::launch_ragged_i8(a, epilogue, (hipStream_t)stream), "moe_gemm_i8 launch");
+}
+
+size_t moe_linear_i8_workspace_bytes(int32_t T, int32_t K) {
+  if (T < 0 || K < 16 || K % 16 != 0 || (int64_t)T >= kMaxRows || K > MOE_I8_MAX_K) return 0;
+  return up256((size_t)T * K) + up256((size_t)T * 4);
+}
+
+moe_status_t moe_linear_i8(const void* x, int32_t in_dtype, const int8_t* Wq, const float* Ws, int32_t T, int32_t N,
+                           int32_t K, int32_t epilogue, void* y, int32_t out_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const char* who = "moe_linear_i8";
+  if (in_dtype != MOE_IN_BF16 && in_dtype != MOE_IN_F16 && in_dtype != MOE_IN_F32)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown in_dtype %d", who, in_dtype);
+  if (T > 0 && !x) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  int8_t* q = static_cast<int8_t*>(workspace);
+  float* s = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256((size_t)(T < 0 ? 0 : T) * (K < 0 ? 0 : K)));
+  if (moe_status_t st = check_i8_gemm(q, workspace ? s : nullptr, Wq, Ws, T, 1, N, K, epilogue, y, out_dtype, who)) return st;
+  if (T == 0) return ok();
+  if (!aligned16(x)) return fail(MOE_ERR_MISALIGNED, "%s: x needs 16-byte alignment", who);
+  const size_t need = moe_linear_i8_workspace_bytes(T, K);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu B < required %zu B", who, workspace_bytes, need);
+  hipError_t e = moe::launch_i8_quant(x, in_dtype, T, K, q, s, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_status(e, "x quantization launch");
+  moe::RaggedArgs a{q, s, nullptr, 1, Wq, Ws, nullptr, T, 1, N, K, y, out_dtype};
+  return hip_status(moe::launch_ragged_i8(a, epilogue, (hipStream_t)stream), "moe_linear_i8 launch");
+}
+
+moe_status_t moe_grouped_gemm_i8(const int8_t* Aq, const float* As, const int32_t* a_row_of, int32_t a_row_div,
+                                 const int8_t* Wq, const float* Ws, const int32_t* expert_offsets, int32_t R, int32_t E,
+                                 int32_t N, int32_t K, int32_t epilogue, void* C, int32_t out_dtype, void* stream) {
+  const char* who = "moe_grouped_gemm_i8";
+  if (moe_status_t st = check_i8_gemm(Aq, As, Wq, Ws, R, E, N, K, epilogue, C, out_dtype, who)) return st;
+  if (R == 0) return ok();
+  if (moe_status_t st = check_groups(a_row_of, a_row_div, expert_offsets, who)) return st;
+  moe::RaggedArgs a{Aq, As, a_row_of, a_row_div, Wq, Ws, expert_offsets, R, E, N, K, C, out_dtype};
+  return hip_status(moe::launch_ragged_i8(a, epilogue, (hipStream_t)stream), "moe_grouped_gemm_i8 launch");
+}
+
+size_t moe_ffn_i8_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k) {
+  if (T < 0 || !ragged_ffn_dims_ok(H, I) || E < 1 || k < 1 || k > E || E > MOE_MAX_EXPERTS || (int64_t)T * k >= kMaxRows)
+    return 0;
+  return ragged_ffn_layout(T, H, I, E, k, true).total;
+}
+
+moe_status_t moe_ffn_forward_i8(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I,
+                                int32_t E, int32_t k, const int8_t* w13_q, const float* w13_s, const int8_t* w2_q,
+                                const float* w2_s, uint16_t* y, int32_t* topk_ids_out, float* topk_w_out,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return run_ragged_ffn(x, router_logits, T, H, I, E, k, w13_q, w13_s, w2_q, w2_s, y, topk_ids_out, topk_w_out,
+                        workspace, workspace_bytes, true, "moe_ffn_forward_i8", (hipStream_t)stream);
+}
+
+moe_status_t moe_grouped_gemm_w16(const uint16_t* A, const int32_t* a_row_of, int32_t a_row_div, const uint16_t* W,
+                                  int32_t dtype, const int32_t* expert_offsets, int32_t R, int32_t E, int32_t N,
+                                  int32_t K, int32_t epilogue, void* C, int32_t out_dtype, void* stream) {
+  const char* who = "moe_grouped_gemm_w16";
+  if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
+  if (moe_status_t st = check_ragged(R, E, N, K, 1, 8, who)) return st;
+  if (moe_status_t st = check_ragged_epilogue(epilogue, out_dtype, N, who)) return st;
+  if (R == 0) return ok();
+  if (!A || !W || !C) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(A) || !aligned16(W) || !aligned16(C)) return fail(MOE_ERR_MISALIGNED, "%s: A, W, C need 16-byte alignment", who);
+  if (moe_status_t st = check_groups(a_row_of, a_row_div, expert_offsets, who)) return st;
+  moe::RaggedArgs a{A, nullptr, a_row_of, a_row_div, W, nullptr, expert_offsets, R, E, N, K, C, out_dtype};
+  return hip_status(moe::launch_ragged_w16(a, 0, dtype == MOE_IN_F16, epilogue, (hipStream_t)stream), "moe_grouped_gemm_w16 launch");
+}
+
+moe_status_t moe_grouped_gemm_w16_dx(const uint16_t* dC, const uint16_t* W, int32_t dtype, const int32_t* expert_offsets,
+                                     int32_t R, int32_t E, int32_t N, int32_t K, void* dA, int32_t out_dtype,
+                                     void* stream) {
+  const char* who = "moe_grouped_gemm_w16_dx";
+  if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
+  if (moe_status_t st = check_ragged(R, E, N, K, 8, 8, who)) return st;
+  if (!ragged_out_ok(out_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown out_dtype %d", who, out_dtype);
+  if (R == 0) return ok();
+  if (!dC || !W || !dA) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(dC) || !aligned16(W) || !aligned16(dA)) return fail(MOE_ERR_MISALIGNED, "%s: dC, W, dA need 16-byte alignment", who);
+  if (moe_status_t st = check_groups(nullptr, 1, expert_offsets, who)) return st;
+  moe::RaggedArgs a{dC, nullptr, nullptr, 1, W, nullptr, expert_offsets, R, E, N, K, dA, out_dtype};
+  return hip_status(moe::launch_ragged_w16(a, 1, dtype == MOE_IN_F16, MOE_EPI_NONE, (hipStream_t)stream), "moe_grouped_gemm_w16_dx launch");
+}
+
+moe_status_t moe_grouped_gemm_w16_dw(const uint16_t* dC, const uint16_t* A, const int32_t* a_row_of, int32_t a_row_div,
+                                     int32_t dtype, const int32_t* expert_offsets, int32_t R, int32_t E, int32_t N,
+                                     int32_t K, void* dW, int32_t out_dtype, void* stream) {
+  const char* who = "moe_grouped_gemm_w16_dw";
+  if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
+  if (moe_status_t st = check_ragged(R, E, N, K, 8, 8, who)) return st;
+  if (!ragged_out_ok(out_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown out_dtype %d", who, out_dtype);
+  if (!dW || (R > 0 && (!dC || !A))) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(dC) || !aligned16(A) || !aligned16(dW)) return fail(MOE_ERR_MISALIGNED, "%s: dC, A, dW need 16-byte alignment", who);
+  if (moe_status_t st = check_groups(a_row_of, a_row_div, expert_offsets, who)) return st;
+  moe::RaggedArgs a{A, nullptr, a_row_of, a_row_div, dC, nullptr, expert_offsets, R, E, N, K, dW, out_dtype};
+  return hip_status(moe::launch_ragged_w16(a, 2, dtype == MOE_IN_F16, MOE_EPI_NONE, (hipStream_t)stream), "moe_grouped_gemm_w16_dw launch");
+}
+
+static moe_status_t check_silu(const void* G, const void* a, const void* b, int32_t dtype, int32_t R, int32_t I, const char* who) {
+  if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
+  if (R < 0 || I < 8 || I % 8 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: need R >= 0 and I a positive multiple of 8", who);
+  if ((int64_t)R >= kMaxRows || I > MOE_RAGGED_MAX_DIM)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: R=%d must be < 2^26 and I=%d <= %d", who, R, I, MOE_RAGGED_MAX_DIM);
+  if (R == 0) return MOE_OK;
+  if (!G || !a || !b) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(G) || !aligned16(a) || !aligned16(b)) return fail(MOE_ERR_MISALIGNED, "%s: pointers need 16-byte alignment", who);
+  return MOE_OK;
+}
+
+moe_status_t moe_silu_mul(const uint16_t* G, int32_t dtype, int32_t R, int32_t I, uint16_t* h, void* stream) {
+  if (moe_status_t st = check_silu(G, h, h, dtype, R, I, "moe_silu_mul")) return st;
+  if (R == 0) return ok();
+  return hip_status(moe::launch_silu_mul(G, dtype == MOE_IN_F16, R, I, h, (hipStream_t)stream), "moe_silu_mul launch");
+}
+
+moe_status_t moe_silu_mul_grad(const uint16_t* G, const uint16_t* dh, int32_t dtype, int32_t R, int32_t I, uint16_t* dG,
+                               void* stream) {
+  if (moe_status_t st = check_silu(G, dh, dG, dtype, R, I, "moe_silu_mul_grad")) return st;
+  if (R == 0) return ok();
+  return hip_status(moe::launch_silu_mul_grad(G, dh, dtype == MOE_IN_F16, R, I, dG, (hipStream_t)stream), "moe_silu_mul_grad launch");
+}
+
+size_t moe_ffn_w16_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k) {
+  if (T < 0 || !ragged_ffn_dims_ok(H, I) || E < 1 || k < 1 || k > E || E > MOE_MAX_EXPERTS || (int64_t)T * k >= kMaxRows)
+    return 0;
+  return ragged_ffn_layout(T, H, I, E, k, false).total;
+}
+
+moe_status_t moe_ffn_forward_w16(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I,
+                                 int32_t E, int32_t k, const uint16_t* w13, const uint16_t* w2, uint16_t* y,
+                                 int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  return run_ragged_ffn(x, router_logits, T, H, I, E, k, w13, nullptr, w2, nullptr, y, topk_ids_out, topk_w_out,
+                        workspace, workspace_bytes, false, "moe_ffn_forward_w16", (hipStream_t)stream);
 }
 
 }  // extern "C"

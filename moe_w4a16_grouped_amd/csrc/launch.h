@@ -174,6 +174,28 @@ hipError_t launch_grouped_gemm_f8(const F8GemmArgs& a, int block_m, hipStream_t 
 hipError_t launch_f8_quant(const void* x, bool in_f32, long long rows, int K, uint8_t* q, float* s,
                            hipStream_t stream);
 
+// Ragged products over expert offsets (ragged_gemm.h): 16-bit floats and 8-bit integers.
+struct RaggedArgs {
+  const void* A;            // FWD: activations [*, K]; DX: dC [R, N]; DW: activations [*, K]
+  const float* As;          // int8: activation row scales [*]
+  const int32_t* a_row_of;  // FWD, DW: row -> flat index (NULL = identity); activation row = index / a_row_div
+  int a_row_div;
+  const void* W;            // FWD, DX: weights [E, N, K]; DW: dC [R, N]
+  const float* Ws;          // int8: channel scales [E, N]
+  const int32_t* offsets;   // [E + 1]; NULL = one group of all R rows (FWD)
+  int R, E, N, K;
+  void* C;                  // FWD: [R, N] or [R, N/2]; DX: [R, K]; DW: [E, N, K]
+  int out;                  // MOE_OUT_BF16, MOE_OUT_F16 or MOE_OUT_F32
+};
+hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilogue, hipStream_t stream);
+hipError_t launch_ragged_i8(const RaggedArgs& a, int epilogue, hipStream_t stream);
+// x (MOE_IN_*) [rows, K] -> codes [rows, K] and scales [rows].
+hipError_t launch_i8_quant(const void* x, int in_dtype, int rows, int K, int8_t* q, float* s, hipStream_t stream);
+// gate_up G [R, 2I] -> h [R, I], and its gradient (16-bit types).
+hipError_t launch_silu_mul(const uint16_t* G, bool f16, long long R, int I, uint16_t* h, hipStream_t stream);
+hipError_t launch_silu_mul_grad(const uint16_t* G, const uint16_t* dh, bool f16, long long R, int I, uint16_t* dG,
+                                hipStream_t stream);
+
 hipError_t launch_prepack(const uint8_t* wq, const uint16_t* ws, int E, int N, int K, uint8_t* pq, uint16_t* ps,
                           hipStream_t stream);
 

@@ -1,0 +1,125 @@
+// Grouped products with 16-bit expert weights (bf16, fp16) and their gradients, and SiLU*mul of a stored
+// gate_up result with its gradient: the training forms of the expert FFN, and its serving form where the
+// weights are not quantized.  The products are ragged_gemm.h's kernel; the layer's order of work follows
+// the ATOM page ("AMD ATOM推理引擎：如何用分页KV缓存和分段编译实现大模型推理性能翻倍"), section "8.1 MoE 路径：
+// 路由、专家并行与 MORI 通信".
+#include "ragged_gemm.h"
+
+namespace moe {
+
+// Tile choice by the mean rows of a group (groups without rows count, as the host knows no better).
+template <class T, int EPI>
+static hipError_t launch_fwd(const RaggedArgs& a, hipStream_t s) {
+  const long long mean = a.offsets ? ((long long)a.R + a.E - 1) / a.E : a.R;
+  if (mean <= 16) return launch_ragged_cfg<T, kFwd, EPI, 16, 128, 1, 4, 128, 4>(a, s);
+  if (mean <= 32) return launch_ragged_cfg<T, kFwd, EPI, 32, 128, 1, 4, 128, 3>(a, s);
+  if (mean <= 64) return launch_ragged_cfg<T, kFwd, EPI, 64, 128, 1, 4, 128, 3>(a, s);
+  if (mean <= 256) return launch_ragged_cfg<T, kFwd, EPI, 128, 128, 2, 2, 64, 4>(a, s);
+  return launch_ragged_cfg<T, kFwd, EPI, 256, 256, 2, 4, 64, 4>(a, s);
+}
+
+template <class T>
+static hipError_t launch_dx(const RaggedArgs& a, hipStream_t s) {
+  const long long mean = ((long long)a.R + a.E - 1) / a.E;
+  if (mean <= 16) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 16, 128, 1, 4, 128, 4>(a, s);
+  if (mean <= 32) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 32, 128, 1, 4, 128, 3>(a, s);
+  if (mean <= 64) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 64, 128, 1, 4, 128, 3>(a, s);
+  if (mean <= 256) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 128, 128, 2, 2, 64, 4>(a, s);
+  return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 256, 256, 2, 4, 64, 4>(a, s);
+}
+
+template <class T>
+static hipError_t launch_dw(const RaggedArgs& a, hipStream_t s) {
+  const long long mean = ((long long)a.R + a.E - 1) / a.E;
+  if (mean <= 256) return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, 128, 128, 2, 2, 64, 3>(a, s);
+  return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, 256, 256, 2, 4, 64, 4>(a, s);
+}
+
+template <class T>
+static hipError_t launch_w16(const RaggedArgs& a, int mode, int epilogue, hipStream_t s) {
+  if (mode == kDw) return launch_dw<T>(a, s);
+  if (mode == kDx) return launch_dx<T>(a, s);
+  if (epilogue == MOE_EPI_SILU_MUL) return launch_fwd<T, MOE_EPI_SILU_MUL>(a, s);
+  return launch_fwd<T, MOE_EPI_NONE>(a, s);
+}
+
+hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilogue, hipStream_t stream) {
+  return f16 ? launch_w16<ElemF16>(a, mode, epilogue, stream) : launch_w16<ElemBF16>(a, mode, epilogue, stream);
+}
+
+// ---------------------------------------------------------------------------------------------------
+// SiLU*mul of a stored gate_up result and its gradient.  With s = 1 / (1 + exp(-g)):
+//   h = g s u,   du = dh g s,   dg = dh u s (1 + g (1 - s)).
+// Pure traffic: a thread takes 8 columns (one 16-byte load of each operand), arithmetic in fp32, one
+// rounding per output.
+template <bool F16>
+__device__ __forceinline__ void unpack8(const u32x4& w, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = F16 ? f16_bits_to_f32(w[i] & 0xFFFFu) : bf16_bits_to_f32(w[i] & 0xFFFFu);
+    v[2 * i + 1] = F16 ? f16_bits_to_f32(w[i] >> 16) : bf16_bits_to_f32(w[i] >> 16);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = F16 ? f32_to_f16_bits(v[2 * i]) : f32_to_bf16_bits(v[2 * i]);
+    const uint32_t hi = F16 ? f32_to_f16_bits(v[2 * i + 1]) : f32_to_bf16_bits(v[2 * i + 1]);
+    w[i] = lo | (hi << 16);
+  }
+  return w;
+}
+
+__device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+template <bool F16, bool GRAD>
+__global__ __launch_bounds__(256) void silu_mul_kernel(const u32x4* G, const u32x4* dh, long long n, int chunks,
+                                                       u32x4* out) {
+  const long long at = linear_block() * 256 + threadIdx.x;
+  if (at >= n) return;
+  const long long row = at / chunks;
+  const int c = (int)(at - row * chunks);
+  float g[8], u[8], v[8];
+  unpack8<F16>(G[row * 2 * chunks + c], g);
+  unpack8<F16>(G[row * 2 * chunks + chunks + c], u);
+  if constexpr (!GRAD) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid_f32(g[i]) * u[i];
+    out[at] = pack8<F16>(v);
+  } else {
+    float d[8], w[8];
+    unpack8<F16>(dh[at], d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sigmoid_f32(g[i]);
+      v[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+      w[i] = d[i] * g[i] * s;
+    }
+    out[row * 2 * chunks + c] = pack8<F16>(v);
+    out[row * 2 * chunks + chunks + c] = pack8<F16>(w);
+  }
+}
+
+template <bool GRAD>
+static hipError_t launch_silu(const uint16_t* G, const uint16_t* dh, bool f16, long long R, int I, uint16_t* out,
+                              hipStream_t s) {
+  const int chunks = I / 8;
+  const long long n = R * chunks;
+  const dim3 grid = grid2d((n + 255) / 256);
+  const u32x4 *g = reinterpret_cast<const u32x4*>(G), *d = reinterpret_cast<const u32x4*>(dh);
+  if (f16) silu_mul_kernel<true, GRAD><<<grid, 256, 0, s>>>(g, d, n, chunks, reinterpret_cast<u32x4*>(out));
+  else silu_mul_kernel<false, GRAD><<<grid, 256, 0, s>>>(g, d, n, chunks, reinterpret_cast<u32x4*>(out));
+  return hipGetLastError();
+}
+
+hipError_t launch_silu_mul(const uint16_t* G, bool f16, long long R, int I, uint16_t* h, hipStream_t stream) {
+  return launch_silu<false>(G, nullptr, f16, R, I, h, stream);
+}
+hipError_t launch_silu_mul_grad(const uint16_t* G, const uint16_t* dh, bool f16, long long R, int I, uint16_t* dG,
+                                hipStream_t stream) {
+  return launch_silu<true>(G, dh, f16, R, I, dG, stream);
+}
+
+}  // namespace moe
