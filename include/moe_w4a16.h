@@ -610,6 +610,7 @@ moe_status_t moe_ffn_forward_f8(const uint16_t* x, const float* router_logits, i
  * offsets[E]) are not written.  Experts without rows cost nothing.
  * a_row_of, a_row_div: activation row of row r = a_row_of ? a_row_of[r] / a_row_div : r (with a_row_of the
  * sorted_ids of moe_align and a_row_div = k, the token of the row).
+ * One expert's weights stay below 4 GiB.
  */
 #define MOE_IN_F16 2
 #define MOE_OUT_F16 5

@@ -480,8 +480,8 @@ bool ragged_out_ok(int32_t out) { return out == MOE_OUT_BF16 || out == MOE_OUT_F
 
 // Shape checks shared by the ragged products: rows R, experts E, weights [E, N, K] whose rows hold a
 // whole number of 16-byte chunks (K a multiple of kq elements; N a multiple of nq where rows of N elements are
-// loaded).
-moe_status_t check_ragged(int64_t R, int32_t E, int32_t N, int32_t K, int32_t nq, int32_t kq, const char* who) {
+// loaded), `bytes` an element.  The kernels address a weight row by a 32-bit offset within its expert.
+moe_status_t check_ragged(int64_t R, int32_t E, int32_t N, int32_t K, int32_t nq, int32_t kq, int32_t bytes, const char* who) {
   if (R < 0 || E < 1 || N < 1 || K < 1) return fail(MOE_ERR_INVALID_ARG, "%s: need R >= 0 and E, N, K >= 1", who);
   if (E > MOE_MAX_EXPERTS) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: E=%d exceeds %d", who, E, MOE_MAX_EXPERTS);
   if (R >= kMaxRows) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: R=%lld must be < 2^26", who, (long long)R);
@@ -489,6 +489,9 @@ moe_status_t check_ragged(int64_t R, int32_t E, int32_t N, int32_t K, int32_t nq
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: N=%d must be a multiple of %d and K=%d of %d", who, N, nq, K, kq);
   if (N > MOE_RAGGED_MAX_DIM || K > MOE_RAGGED_MAX_DIM)
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: N=%d and K=%d must not exceed %d", who, N, K, MOE_RAGGED_MAX_DIM);
+  if ((int64_t)N * K * bytes > kMaxExpertCodeBytes)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: one expert's weights (%lld bytes) must stay below 4 GiB", who,
+                (long long)N * K * bytes);
   return MOE_OK;
 }
 
@@ -508,7 +511,7 @@ moe_status_t check_w16_dtype(int32_t dtype, const char* who) {
 // Shape and pointer checks of one int8 product (offsets NULL: the dense one).
 moe_status_t check_i8_gemm(const int8_t* Aq, const float* As, const int8_t* Wq, const float* Ws, int64_t R, int32_t E,
                            int32_t N, int32_t K, int32_t epilogue, const void* C, int32_t out_dtype, const char* who) {
-  if (moe_status_t st = check_ragged(R, E, N, K, 1, 16, who)) return st;
+  if (moe_status_t st = check_ragged(R, E, N, K, 1, 16, 1, who)) return st;
   if (K > MOE_I8_MAX_K) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: K=%d exceeds %d (int32 sums)", who, K, MOE_I8_MAX_K);
   if (moe_status_t st = check_ragged_epilogue(epilogue, out_dtype, N, who)) return st;
   if (R == 0) return MOE_OK;
@@ -563,6 +566,8 @@ moe_status_t run_ragged_ffn(const uint16_t* x, const float* router_logits, int32
   if (!ragged_ffn_dims_ok(H, I))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H=%d and I=%d must be positive multiples of 16, <= %d", who, H, I,
                 MOE_I8_MAX_K);
+  if ((int64_t)2 * I * H * (i8 ? 1 : 2) > kMaxExpertCodeBytes)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: one expert's gate_up weights must stay below 4 GiB", who);
   if (T == 0) return ok();
   if (!x || !router_logits || !w13 || !w2 || (i8 && (!w13_s || !w2_s)) || !y || !workspace)
     return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -1575,7 +1580,7 @@ moe_status_t moe_grouped_gemm_w16(const uint16_t* A, const int32_t* a_row_of, in
                                   int32_t K, int32_t epilogue, void* C, int32_t out_dtype, void* stream) {
   const char* who = "moe_grouped_gemm_w16";
   if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
-  if (moe_status_t st = check_ragged(R, E, N, K, 1, 8, who)) return st;
+  if (moe_status_t st = check_ragged(R, E, N, K, 1, 8, 2, who)) return st;
   if (moe_status_t st = check_ragged_epilogue(epilogue, out_dtype, N, who)) return st;
   if (R == 0) return ok();
   if (!A || !W || !C) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -1590,7 +1595,7 @@ moe_status_t moe_grouped_gemm_w16_dx(const uint16_t* dC, const uint16_t* W, int3
                                      void* stream) {
   const char* who = "moe_grouped_gemm_w16_dx";
   if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
-  if (moe_status_t st = check_ragged(R, E, N, K, 8, 8, who)) return st;
+  if (moe_status_t st = check_ragged(R, E, N, K, 8, 8, 2, who)) return st;
   if (!ragged_out_ok(out_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown out_dtype %d", who, out_dtype);
   if (R == 0) return ok();
   if (!dC || !W || !dA) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -1605,7 +1610,7 @@ moe_status_t moe_grouped_gemm_w16_dw(const uint16_t* dC, const uint16_t* A, cons
                                      int32_t K, void* dW, int32_t out_dtype, void* stream) {
   const char* who = "moe_grouped_gemm_w16_dw";
   if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
-  if (moe_status_t st = check_ragged(R, E, N, K, 8, 8, who)) return st;
+  if (moe_status_t st = check_ragged(R, E, N, K, 8, 8, 2, who)) return st;
   if (!ragged_out_ok(out_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown out_dtype %d", who, out_dtype);
   if (!dW || (R > 0 && (!dC || !A))) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned16(dC) || !aligned16(A) || !aligned16(dW)) return fail(MOE_ERR_MISALIGNED, "%s: dC, A, dW need 16-byte alignment", who);

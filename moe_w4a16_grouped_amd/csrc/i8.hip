@@ -125,12 +125,12 @@ hipError_t launch_i8_quant(const void* x, int in_dtype, int rows, int K, int8_t*
 // Tile choice by the mean rows of a group.
 template <int EPI>
 static hipError_t launch_i8(const RaggedArgs& a, hipStream_t s) {
-  const long long mean = a.offsets ? ((long long)a.R + a.E - 1) / a.E : a.R;
-  if (mean <= 16) return launch_ragged_cfg<ElemI8, kFwd, EPI, 16, 128, 1, 4, 128, 4>(a, s);
-  if (mean <= 32) return launch_ragged_cfg<ElemI8, kFwd, EPI, 32, 128, 1, 4, 128, 3>(a, s);
-  if (mean <= 64) return launch_ragged_cfg<ElemI8, kFwd, EPI, 64, 128, 1, 4, 128, 3>(a, s);
-  if (mean <= 256) return launch_ragged_cfg<ElemI8, kFwd, EPI, 128, 128, 2, 2, 64, 4>(a, s);
-  return launch_ragged_cfg<ElemI8, kFwd, EPI, 256, 256, 2, 4, 64, 4>(a, s);
+  const long long mean = ((long long)a.R + a.E - 1) / a.E;
+  if (mean <= 16) return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<16, 128, 1, 4, 128, 4>>(a, s);
+  if (mean <= 32) return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<32, 128, 1, 4, 128, 3>>(a, s);
+  if (mean <= 64) return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<64, 128, 1, 4, 128, 3>>(a, s);
+  if (mean <= 256) return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<128, 128, 2, 2, 64, 4>>(a, s);
+  return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<256, 256, 2, 4, 128, 2>, TileShape<128, 256, 2, 4, 128, 2>>(a, s);
 }
 
 hipError_t launch_ragged_i8(const RaggedArgs& a, int epilogue, hipStream_t stream) {

@@ -8,7 +8,7 @@
 //   DW:  dW[e, n, k] = sum_{r of e} dC[r, n] * A[a(r), k]
 // A workgroup computes a BM x BN tile of the output.  The contraction runs in steps of RB bytes an
 // operand row (RB / 2 16-bit or RB integer elements); a step's two operand tiles reach LDS by direct
-// global->LDS 16-byte loads through a ring of NS stages, one barrier per step.  An operand whose
+// global->LDS 16-byte loads through a ring of stages, one barrier per step.  An operand whose
 // contraction axis is contiguous in memory ("rows") is kept as [row][RB bytes]; one whose other axis is
 // contiguous (W in DX, both in DW) as [contraction row][tile columns], and its fragments are read with
 // the transposing LDS load (ds_read_b64_tr_b16: a 16-lane group reads a 4 x 16 block and lane j gets
@@ -19,6 +19,8 @@
 // operand, so a lane's four results are four neighbouring columns of one output row and are stored
 // together.
 #pragma once
+#include <type_traits>
+
 #include "launch.h"
 #include "moe_common.h"
 
@@ -56,66 +58,141 @@ enum RaggedMode { kFwd = 0, kDx = 1, kDw = 2 };
 // What lanes past an operand's end load instead: zeros, so that they add nothing to the product.
 static __device__ const u32x4 kZeroChunk = {0u, 0u, 0u, 0u};
 
-// 16-byte chunk permutation of an operand kept as rows of RB bytes: the 16 rows of a fragment read at one
-// chunk column fall in 16 different chunks of a 256-byte bank line.
+// 16-byte chunk permutation of an operand kept as rows of RB bytes.  A 16-byte LDS read serves 16 lanes a
+// cycle, not 16 neighbours but lanes 0-3, 12-15 and 20-27 together, and the rest likewise: of a fragment
+// read, rows 0-3 and 12-15 at one chunk column with rows 4-11 at the next.  Both permutations put those 16
+// chunks into 16 different places of the 256-byte bank line (measured: plain (row / 4) % 4 for 64-byte rows
+// doubled the LDS cycles).
 template <int RB>
 __device__ __forceinline__ int row_swizzle(int row) {
-  return RB == 64 ? (row >> 2) & 3 : (row >> 1) & 7;
+  return RB == 64 ? ((row >> 3) & 1) | ((((row >> 2) ^ (row >> 3)) & 1) << 1) : (row >> 1) & 7;
 }
 // 32-byte window permutation of an operand kept as contraction rows: a transposing read covers 4 rows of
 // each 16-lane group, groups 8 rows apart; the eight rows of half a wave fall in eight different windows.
 __device__ __forceinline__ int col_swizzle(int crow) { return (crow & 3) | ((crow >> 1) & 4); }
 
-// A row tile of the ragged groups: expert, first row, rows (at most BM).
+// Direct global->LDS loads to a wave-uniform LDS byte address (lane l writes [16l, 16l+16), or [4l, 4l+4) from
+// it); the second takes a uniform base and a 32-bit offset a lane.
+__device__ __forceinline__ void g2lds16_at(const void* g, uint32_t lds) {
+  asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void g2lds16_at(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void g2lds4_at(const void* g, uint32_t lds) {
+  asm volatile("global_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+
+// A row tile of the ragged groups: expert, first row, rows (at most the tile's height), height class.
 struct RowTile {
-  int e, row0, rows;
+  int e, row0, rows, cls;
 };
 
 __device__ __forceinline__ int group_end(const int32_t* off, int i, int R) { return min(max(off[i], 0), R); }
 
-// Finds the workgroup's row tile and column block from the offsets: every wave counts the tiles of
-// E / 64 experts a lane, scans the counts over its lanes and walks the experts of the lane that holds the
-// wanted tile.  Offsets are clamped to [0, R], so no list of offsets leads out of the rows.
-template <int BM>
-__device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ off, int E, int R, int nbn, RowTile& t, int& nb) {
-  int tile;
-  if (!off) {  // one group of all rows
-    const int n = (R + BM - 1) / BM;
-    if (!mm_work(linear_block(), nbn, n, tile, nb)) return false;
-    t = RowTile{0, tile * BM, min(BM, R - tile * BM)};
-    return true;
-  }
-  const int lane = threadIdx.x & 63;
-  const int per = (E + 63) / 64;
-  const int e0 = min(lane * per, E), e1 = min(e0 + per, E);
-  int at = group_end(off, e0, R), n = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int end = group_end(off, e + 1, R);
-    n += (max(end - at, 0) + BM - 1) / BM;
-    at = end;
-  }
-  int incl = n;
+// Row tiles of one group, in up to three heights H0 = 2 H1 = 4 H2 (H1, H2 zero: not there): whole tiles of H0,
+// and the rest in the smaller heights where they hold it, so that at most H2 - 1 padding rows (with one height
+// H0 - 1) are multiplied.
+struct TileCount {
+  int n0, n1, n2;
+};
+template <int H0, int H1, int H2>
+__device__ __forceinline__ TileCount count_tiles(int rows) {
+  const int rest = rows % H0;
+  TileCount c{rows / H0, 0, 0};
+  if (H1 == 0 || rest > H1 + H2) c.n0 += rest > 0;
+  else if (H2 == 0) c.n1 = rest > 0;
+  else { c.n1 = rest > H2; c.n2 = (rest > 0 && rest <= H2) || rest > H1; }
+  return c;
+}
+
+// Work order.  Workgroup b runs on XCD b % 8, each XCD with its own L2.  The output tiles of all experts,
+// expert after expert, form one list per height, the highest first (the short ones then fill the end of the
+// launch), and the XCDs share each list in contiguous eighths.  An expert's tiles (nt row tiles x nbn column
+// blocks) are listed in bands of 8 row tiles, down a band's rows first: the 32 tiles that an XCD's CUs work on
+// together form a block about as wide as high, so that its L2 takes in few rows of either operand.
+constexpr int kBand = 8;
+__device__ __forceinline__ void band_place(long long i, int nt, int nbn, int& tile, int& nb) {
+  const long long band = (long long)kBand * nbn;
+  const int g = (int)(i / band);
+  const int r = (int)(i - g * band);
+  const int high = min(kBand, nt - g * kBand);
+  nb = r / high;
+  tile = g * kBand + (r - nb * high);
+}
+
+// Takes this workgroup's XCD's share of a list of `total` tiles from its number j on the XCD: true and the place
+// in the list, or false with the share taken off j.
+__device__ __forceinline__ bool list_place(long long total, long long& j, long long& at) {
+  const long long xcd = linear_block() & 7;
+  const long long from = (xcd * total) >> 3, to = ((xcd + 1) * total) >> 3;
+  at = from + j;
+  if (at < to) return true;
+  j -= to - from;
+  return false;
+}
+
+// Inclusive sum of v over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
+    const int u = __shfl_up(v, d);
+    if (lane >= d) v += u;
   }
-  const int total = __builtin_amdgcn_readlane(incl, 63);
-  if (!mm_work(linear_block(), nbn, total, tile, nb)) return false;
-  const uint64_t past = __ballot(incl > tile);
-  const int src = __builtin_ctzll(past);  // tile < total: some lane's sum is past it
-  int left = tile - (__builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(n, src));
+  return v;
+}
+
+// Finds the workgroup's row tile and column block from the offsets: every wave counts the tiles of E / 64
+// experts a lane, scans the counts over its lanes and walks the experts of the lane that holds the wanted
+// tile.  Offsets are clamped to [0, R], so no list of offsets leads out of the rows.
+template <int H0, int H1, int H2>
+__device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ off, int E, int R, int nbn, RowTile& t, int& nb) {
+  const int lane = threadIdx.x & 63;
+  const int per = off ? (E + 63) / 64 : 1;
+  const int e0 = min(lane * per, E), e1 = min(e0 + per, E);
+  // without offsets one group holds all rows
+  auto end_of = [&](int e) { return off ? group_end(off, e, R) : (e > 0 ? R : 0); };
+  int at = end_of(e0);
+  TileCount n{0, 0, 0};
+  for (int e = e0; e < e1; ++e) {
+    const int end = end_of(e + 1);
+    const TileCount c = count_tiles<H0, H1, H2>(max(end - at, 0));
+    n.n0 += c.n0;
+    n.n1 += c.n1;
+    n.n2 += c.n2;
+    at = end;
+  }
+  long long j = linear_block() >> 3, item;
+  int incl = wave_scan(n.n0, lane), mine = n.n0, cls = 0;
+  if (!list_place((long long)__builtin_amdgcn_readlane(incl, 63) * nbn, j, item)) {
+    if (H1 == 0) return false;
+    incl = wave_scan(n.n1, lane), mine = n.n1, cls = 1;
+    if (!list_place((long long)__builtin_amdgcn_readlane(incl, 63) * nbn, j, item)) {
+      if (H2 == 0) return false;
+      incl = wave_scan(n.n2, lane), mine = n.n2, cls = 2;
+      if (!list_place((long long)__builtin_amdgcn_readlane(incl, 63) * nbn, j, item)) return false;
+    }
+  }
+  const int place = (int)(item / nbn);  // names the expert: its tiles x nbn items follow each other
+  const int src = __builtin_ctzll(__ballot(incl > place));  // place < total: some lane's sum is past it
+  int before = __builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(mine, src);  // tiles before expert e
   int e = src * per;
-  at = group_end(off, e, R);
+  at = end_of(e);
   for (;; ++e) {
-    const int end = group_end(off, e + 1, R);
-    const int nt = (max(end - at, 0) + BM - 1) / BM;
-    if (left < nt || e == E - 1) {
-      const int r0 = at + left * BM;
-      t = RowTile{e, r0, min(BM, end - r0)};
+    const int end = end_of(e + 1);
+    const TileCount c = count_tiles<H0, H1, H2>(max(end - at, 0));
+    const int nt = cls == 0 ? c.n0 : (cls == 1 ? c.n1 : c.n2);
+    if (place < before + nt || e == E - 1) {
+      int tile;
+      band_place(item - (long long)before * nbn, nt, nbn, tile, nb);
+      const int r0 = at + (cls == 0 ? tile : c.n0) * H0 + (cls == 2 ? c.n1 * H1 : 0);
+      t = RowTile{e, r0, min(cls == 0 ? H0 : (cls == 1 ? H1 : H2), end - r0), cls};
       return true;
     }
-    left -= nt;
+    before += nt;
     at = end;
   }
 }
@@ -136,23 +213,38 @@ __device__ __forceinline__ void store1(void* C, int out, size_t at, float v) {
 }
 
 // Rows whose gathered indexes DW keeps in LDS at a time (a pass drains the ring of stages).
-template <int BM>
-constexpr int dw_ids() { return BM >= 256 ? 4096 : 1024; }
+constexpr int kDwIds = 1024;
 
-template <class T, int MODE, int EPI, int BM, int BN, int WM, int WN, int RB, int NS>
-__global__ __launch_bounds__(WM * WN * 64) void ragged_gemm_kernel(RaggedArgs p) {
+// Shape of one tile height's work: BM x BN by WM x WN waves, steps of RB bytes, NA stages of the A operand's tile
+// and NB >= NA of the B operand's.
+template <int BM_, int BN_, int WM_, int WN_, int RB_, int NA_, int NB_ = NA_>
+struct TileShape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, RB = RB_, NA = NA_, NB = NB_;
+  static constexpr int kLds = (NA * BM + NB * BN) * RB;
+};
+struct NoTile {
+  static constexpr int BM = 0, BN = 0, WM = 0, WN = 0, RB = 0, NA = 0, NB = 0, kLds = 0;
+};
+
+// One output tile: rows t (DW: weight rows from m0) by column block nb.
+template <class T, int MODE, int EPI, class S>
+__device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& t, int nb, int m0, uint8_t* smem, int32_t* sRow,
+                                            float* sScaleA, float* sScaleW) {
+  constexpr int BM = S::BM, BN = S::BN, WM = S::WM, WN = S::WN, RB = S::RB, NA = S::NA, NB = S::NB;
   constexpr int NW = WM * WN;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   constexpr bool A_T = MODE == kDw, B_T = MODE != kFwd;  // operand kept as contraction rows
-  constexpr int CR = RB / T::kBytes;                     // contraction elements per step
-  constexpr int SA = BM * RB, SB = BN * RB, STAGE = SA + SB;
-  constexpr int LA = SA / 1024, LT = STAGE / 1024;       // wave-wide loads of a step: the A tile's, all
-  constexpr int LW = (LT + NW - 1) / NW, LMIN = LT / NW;
+  constexpr bool I8 = T::kBytes == 1;
+  constexpr int CR = RB / T::kBytes;  // contraction elements per step
+  constexpr int SA = BM * RB, SB = BN * RB;
+  constexpr int LA = SA / 1024, LB = SB / 1024;                        // wave-wide loads of a step
+  constexpr int JA = (LA + NW - 1) / NW, JB = (LB + NW - 1) / NW;      // of one wave, at most
+  constexpr int LMIN = LA / NW + LB / NW;                              // and at least
+  // loads behind those of the next step when it is about to be read (see run)
+  constexpr int BEHIND = (NA - 2) * LMIN + (NB > NA ? LB / NW : 0);
   static_assert(EPI != MOE_EPI_SILU_MUL || (MODE == kFwd && NI % 2 == 0), "SiLU*mul pairs gate and up blocks");
-  static_assert(T::kBytes == 2 || MODE == kFwd, "transposing reads are of 16-bit elements");
-  static_assert(SA % 1024 == 0 && SB % 1024 == 0 && LMIN >= 1 && (NS - 2) * LMIN < 64, "loads");
-  __shared__ __attribute__((aligned(16))) uint8_t smem[NS * STAGE];
-  __shared__ int32_t sRow[MODE == kDw ? dw_ids<BM>() : BM];
+  static_assert(!I8 || MODE == kFwd, "transposing reads are of 16-bit elements");
+  static_assert(SA % 1024 == 0 && SB % 1024 == 0 && LMIN >= 1 && BEHIND < 64 && NA >= 2 && NB - NA <= 1 && NB >= NA && NW % 2 == 0, "loads");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -162,32 +254,7 @@ __global__ __launch_bounds__(WM * WN * 64) void ragged_gemm_kernel(RaggedArgs p)
   // output columns and contraction length
   const int ND = MODE == kFwd ? (EPI == MOE_EPI_SILU_MUL ? N / 2 : N) : K;
   constexpr int BC = EPI == MOE_EPI_SILU_MUL ? BN / 2 : BN;  // output columns of a tile
-  const int nbn = (ND + BC - 1) / BC;
-
-  RowTile t;
-  int nb, m0 = 0;  // column block; DW: first weight row of the tile
-  if constexpr (MODE == kDw) {
-    // every expert's tiles are shared evenly by the XCDs (an expert with many rows keeps all of them
-    // busy); fewer than 8 tiles an expert are dealt one by one
-    const int nbm = (N + BM - 1) / BM, per_e = nbm * nbn;
-    const long long b = linear_block();
-    int e, i;
-    if (per_e >= 8) {
-      const int xcd = (int)(b & 7), slots = (per_e + 7) / 8;
-      e = (int)((b >> 3) / slots);
-      i = (int)(((long long)xcd * per_e) >> 3) + (int)((b >> 3) % slots);
-      if (i >= (int)(((long long)(xcd + 1) * per_e) >> 3)) return;
-    } else {
-      e = (int)(b / per_e);
-      i = (int)(b % per_e);
-    }
-    if (e >= p.E) return;
-    m0 = (i / nbn) * BM;
-    nb = i % nbn;
-    const int r0 = group_end(p.offsets, e, p.R);
-    t = RowTile{e, r0, max(group_end(p.offsets, e + 1, p.R) - r0, 0)};
-  } else {
-    if (!find_row_tile<BM>(p.offsets, p.E, p.R, nbn, t, nb)) return;
+  if constexpr (MODE != kDw) {
     for (int i = tid; i < BM; i += NW * 64) {  // padding rows repeat the tile's first row
       const int r = t.row0 + (i < t.rows ? i : 0);
       sRow[i] = MODE == kFwd && p.a_row_of ? p.a_row_of[r] / p.a_row_div : r;
@@ -198,90 +265,133 @@ __global__ __launch_bounds__(WM * WN * 64) void ragged_gemm_kernel(RaggedArgs p)
   const uint8_t* A = static_cast<const uint8_t*>(p.A);
   const uint8_t* W = static_cast<const uint8_t*>(p.W);
   const uint8_t* zero = reinterpret_cast<const uint8_t*>(&kZeroChunk);
+  const uint32_t lds0 = lds_address(smem);
 
-  // Sources of this lane's loads (load j is the wave-wide load wave + NW * j of a step's LT).  Rows kind:
-  // src is the chunk at contraction byte 0 and pos its byte in the step.  Contraction-rows kind: src is
-  // the chunk of contraction row 0 (NULL when its columns lie past the edge) and pos its row in the step.
-  const uint8_t* src[LW];
-  int pos[LW];
-#pragma unroll
-  for (int j = 0; j < LW; ++j) {
-    const int i = wave + NW * j;
-    const bool is_a = i < LA;
-    const int byte = (is_a ? i : i - LA) * 1024 + lane * 16;
-    src[j] = nullptr;
-    pos[j] = 0;
-    if (is_a ? !A_T : !B_T) {
-      const int row = byte / RB;
-      pos[j] = 16 * (((byte % RB) >> 4) ^ row_swizzle<RB>(row));
-      if (is_a) {
-        const size_t width = (size_t)(MODE == kDx ? N : K) * T::kBytes;
-        src[j] = A + (size_t)sRow[row] * width + pos[j];
-      } else if (i < LT) {
-        int n;
-        if (EPI == MOE_EPI_SILU_MUL) {  // a wave's columns: its gate rows, then their up rows
-          constexpr int WC = BN / WN;
-          const int in = row % WC, h = nb * BC + (row / WC) * (WC / 2) + in % (WC / 2);
-          n = h < ND ? (in < WC / 2 ? h : ND + h) : 0;
-        } else {
-          n = nb * BN + row;
-          if (n >= N) n = 0;
-        }
-        src[j] = W + (w_e + (size_t)n * K) * T::kBytes + pos[j];
-      }
-    } else {
-      const int width = (is_a ? BM : BN) * 2;
-      const int crow = byte / width;
-      const int col = (is_a ? m0 : nb * BN) + 8 * (((byte % width) >> 4) ^ (2 * col_swizzle(crow)));
-      const int cols = is_a ? N : K;
-      pos[j] = crow;
-      // DX: rows of W; DW: rows of dC (A operand) and of A (B operand), whose row is added at the load
-      const uint8_t* base = MODE == kDx ? W + w_e * 2 : (is_a ? W : A);
-      if (col < cols) src[j] = base + (size_t)col * 2;
+  // weight row of tile column nt (a SiLU*mul wave's columns: its gate rows, then their up rows); columns past
+  // the edge read row 0, which only reaches results that are not stored
+  auto weight_row = [&](int nt) -> int {
+    if (EPI == MOE_EPI_SILU_MUL) {
+      constexpr int WC = BN / WN;
+      const int in = nt % WC, h = nb * BC + (nt / WC) * (WC / 2) + in % (WC / 2);
+      return h < ND ? (in < WC / 2 ? h : ND + h) : 0;
     }
+    const int n = nb * BN + nt;
+    return n < N ? n : 0;
+  };
+  if constexpr (I8) {  // the tile's scales, for the epilogue: older than every load of a stage
+    for (int i = wave; i < (BM + 63) / 64; i += NW)
+      g2lds4_at(p.As + sRow[min(i * 64 + lane, BM - 1)], lds_address(sScaleA) + i * 256);
+    for (int i = wave; i < BN / 64; i += NW)
+      g2lds4_at(p.Ws + (size_t)t.e * N + weight_row(i * 64 + lane), lds_address(sScaleW) + i * 256);
   }
 
-  // contraction of this pass: rows of the expert (DW), else the whole axis
-  const int KD = MODE == kFwd ? K : N;
-  int kd = MODE == kDw ? 0 : KD;  // elements in the present pass (DW sets it per pass)
-  int pass0 = 0;                  // DW: first row of the pass within the expert
-  auto issue = [&](int s, int stage) {
-    uint8_t* st = smem + stage * STAGE;
+  // Sources of this wave's loads; load j of an operand is its wave-wide load wave + NW * j of a step.
+  // Rows kind: lane's chunk at row (wave + NW j) * 1024 / RB + lane / (RB / 16), contraction byte pos in the step
+  // (the permutation does not depend on j).  Contraction-rows kind: chunk of contraction row
+  // (wave + NW j) * 1024 / width + lane / (width / 16); columns past the edge read the last ones, which only
+  // reach results that are not stored.  Activations may lie anywhere (64-bit addresses); dC and one expert's
+  // weights are addressed from a uniform base that advances from step to step (32-bit offsets).
+  const int rows_row = (lane * 16) / RB;
+  const int pos = 16 * ((((lane * 16) % RB) >> 4) ^ row_swizzle<RB>(wave * (1024 / RB) + rows_row));
+  auto cols_row = [&](int j, int width) { return (wave + NW * j) * (1024 / width) + lane * 16 / width; };
+  auto cols_off = [&](int j, int width, int col0, int cols) -> uint32_t {
+    const int crow = cols_row(j, width);
+    const int col = col0 + 8 * (((lane * 16 % width) >> 4) ^ (2 * col_swizzle(crow)));
+    return ((uint32_t)crow * cols + min(col, cols - 8)) * 2;
+  };
+  const bool gather = MODE == kDw && p.a_row_of;
+  const uint8_t* pa[JA];  // FWD
+  uint32_t oa[JA], ob[JB];
+  const uint8_t *base_a = nullptr, *base_b;
 #pragma unroll
-    for (int j = 0; j < LW; ++j) {
-      const int i = wave + NW * j;
-      if (LT % NW != 0 && i >= LT) break;
-      const uint8_t* from;
-      const bool is_a = i < LA;
-      if (is_a ? !A_T : !B_T) {
-        from = src[j] + (size_t)s * RB;
-        if ((s + 1) * RB > KD * T::kBytes && s * RB + pos[j] >= KD * T::kBytes) from = zero;
-      } else {
-        const int c = s * CR + pos[j];
-        from = zero;
-        if (src[j] && c < kd) {
-          if (MODE == kDx) from = src[j] + (size_t)c * K * 2;
-          else if (is_a) from = src[j] + (size_t)(t.row0 + pass0 + c) * N * 2;
-          else from = src[j] + (size_t)(p.a_row_of ? sRow[c] : t.row0 + pass0 + c) * K * 2;
-        }
-      }
-      g2lds16(from, st + i * 1024);
+  for (int j = 0; j < JA; ++j) {
+    const int row = min((wave + NW * j) * (1024 / RB) + rows_row, BM - 1);
+    if (MODE == kFwd) pa[j] = A + (size_t)sRow[row] * K * T::kBytes + pos;
+    else if (MODE == kDx) oa[j] = (uint32_t)(sRow[row] - t.row0) * N * 2 + pos;
+    else oa[j] = cols_off(j, BM * 2, m0, N);
+  }
+  if (MODE == kDx) base_a = A + (size_t)t.row0 * N * 2;
+  if (MODE == kDw) base_a = W + (size_t)t.row0 * N * 2;
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    if (MODE == kFwd) {
+      const int nt = min((wave + NW * j) * (1024 / RB) + rows_row, BN - 1);
+      ob[j] = (uint32_t)weight_row(nt) * K * T::kBytes + pos;
+    } else {
+      ob[j] = cols_off(j, BN * 2, nb * BN, K);
     }
+  }
+  if (MODE == kDw) {
+    base_b = A + (gather ? 0 : (size_t)t.row0 * K * 2);
+    if (gather) {  // only the column remains; the row comes with its index
+#pragma unroll
+      for (int j = 0; j < JB; ++j) ob[j] -= (uint32_t)cols_row(j, BN * 2) * K * 2;
+    }
+  } else {
+    base_b = W + w_e * T::kBytes;
+  }
+  const size_t step_a = MODE == kDw ? (size_t)CR * N * 2 : RB, step_b = MODE == kFwd ? RB : (size_t)CR * K * 2;
+
+  if constexpr (!I8 && MODE != kDw) __syncthreads();  // every wave has its rows: the stages may be filled
+
+  // contraction elements of this pass (DW: rows of the expert, as many at a time as sRow holds) and its full steps
+  int kd = MODE == kFwd ? K : N;
+  int full = kd / CR;
+  // Issue load j of step s's A or B tile into a stage; an operand's steps in turn.  FULL: the step is known to lie
+  // within the contraction; past it zeros are loaded.
+  auto issue_a = [&](int s, int stage, int j, auto whole) {
+    constexpr bool FULL = decltype(whole)::value;
+    const int left = FULL ? 0 : kd - s * CR;  // elements of this step
+    const int i = wave + NW * j;
+    if (LA % NW != 0 && i >= LA) return;
+    const uint32_t to = lds0 + stage * SA + i * 1024;
+    if (!FULL && s >= full) {
+      const uint8_t* from = MODE == kFwd ? pa[j] : base_a + oa[j];
+      if (A_T ? cols_row(j, BM * 2) >= left : pos >= left * T::kBytes) from = zero;
+      g2lds16_at(from, to);
+    } else if (MODE == kFwd) {
+      g2lds16_at(pa[j], to);
+    } else {
+      g2lds16_at(base_a, oa[j], to);
+    }
+    if (MODE == kFwd) pa[j] += RB;
+    else if (j == JA - 1) base_a += step_a;
+  };
+  auto issue_b = [&](int s, int stage, int j, auto whole) {
+    constexpr bool FULL = decltype(whole)::value;
+    const int left = FULL ? 0 : kd - s * CR;
+    const int i = wave + NW * j;
+    if (LB % NW != 0 && i >= LB) return;
+    const uint32_t to = lds0 + NA * SA + stage * SB + i * 1024;
+    const bool tail = !FULL && s >= full;
+    if (MODE == kDw && gather) {
+      const uint8_t* from = A + (size_t)sRow[min(s * CR + cols_row(j, BN * 2), kd - 1)] * K * 2 + ob[j];
+      if (tail && cols_row(j, BN * 2) >= left) from = zero;
+      g2lds16_at(from, to);
+    } else if (tail) {
+      const uint8_t* from = base_b + ob[j];
+      if (B_T ? cols_row(j, BN * 2) >= left : pos >= left * T::kBytes) from = zero;
+      g2lds16_at(from, to);
+    } else {
+      g2lds16_at(base_b, ob[j], to);
+    }
+    if (j == JB - 1) base_b += step_b;
   };
 
-  // this lane's fragment offsets in a stage
+  // This lane's fragments.  Rows kind: 16 bytes of row row0 + l16.  Contraction-rows kind: contraction rows
+  // 8 q + 4 h + l16 / 4 of the group, whose window permutation depends on the lane alone.
+  const int frag_r = l16 * RB, frag_x = row_swizzle<RB>(l16);
   auto frag_rows = [&](const uint8_t* tile, int row0, int kk) -> u32x4 {
-    return *reinterpret_cast<const u32x4*>(tile + (row0 + l16) * RB + 16 * ((kk * 4 + q) ^ row_swizzle<RB>(l16)));
+    return *reinterpret_cast<const u32x4*>(tile + row0 * RB + (frag_r + 16 * ((kk * 4 + q) ^ frag_x)));
   };
+  const int frag_g = (l16 >> 2) | ((q & 1) << 2), frag_c = 8 * q + (l16 >> 2);
   auto frag_cols = [&](const uint8_t* tile, int width, int col0, int kk) -> u32x4 {
     u32x2 half[2];
+    const uint8_t* at = tile + (kk * 32 * width) + (frag_c * width + (((col0 >> 4) ^ frag_g) << 5) + 8 * (l16 & 3));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int crow = kk * 32 + 8 * q + 4 * h + (l16 >> 2);
-      const int byte = crow * width + (((col0 >> 4) ^ col_swizzle(crow)) << 5) + 8 * (l16 & 3);
+    for (int h = 0; h < 2; ++h)
       half[h] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) i16x4*)(tile + byte)));
-    }
+          (__attribute__((address_space(3))) i16x4*)(at + 4 * h * width)));
     return u32x4{half[0][0], half[0][1], half[1][0], half[1][1]};
   };
 
@@ -291,62 +401,135 @@ __global__ __launch_bounds__(WM * WN * 64) void ragged_gemm_kernel(RaggedArgs p)
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = typename T::Acc{0, 0, 0, 0};
 
-  auto compute = [&](int stage) {
-    const uint8_t* ta = smem + stage * STAGE;
-    const uint8_t* tb = ta + SA;
-#pragma unroll
-    for (int kk = 0; kk < RB / 64; ++kk) {
-      u32x4 a[MI], b[NI];
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        const int c = wn * (BN / WN) + ni * 16;
-        b[ni] = B_T ? frag_cols(tb, BN * 2, c, kk) : frag_rows(tb, c, kk);
-      }
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        const int r = wm * (BM / WM) + mi * 16;
-        a[mi] = A_T ? frag_cols(ta, BM * 2, r, kk) : frag_rows(ta, r, kk);
-      }
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = T::mfma(b[ni], a[mi], acc[mi][ni]);
+  // Fragments of one 64-byte group of a stage: the tile columns, and one half of the wave's row blocks.
+  constexpr int KK = RB / 64;  // 64-byte groups of a step
+  constexpr int HALVES = MI >= 2 ? 2 : 1, MH = MI / HALVES;
+  constexpr int PH = KK * HALVES;  // phases of a step
+  u32x4 fa[2][MH], fb[2][NI];
+  // Read r of a phase's fragments: its NI column blocks first where it starts a group, then its MH row blocks.
+  auto read_one = [&](int stage_a, int stage_b, int kk, int half, int abuf, int bbuf, int r) {
+    if (half == 0 && r < NI) {
+      const uint8_t* tb = smem + NA * SA + stage_b * SB;
+      const int c = wn * (BN / WN) + r * 16;
+      fb[bbuf][r] = B_T ? frag_cols(tb, BN * 2, c, kk) : frag_rows(tb, c, kk);
+    } else {
+      const uint8_t* ta = smem + stage_a * SA;
+      const int i = half == 0 ? r - NI : r;
+      const int c = wm * (BM / WM) + (half * MH + i) * 16;
+      fa[abuf][i] = A_T ? frag_cols(ta, BM * 2, c, kk) : frag_rows(ta, c, kk);
     }
   };
 
-  // Step s lives in stage s % NS.  A stage is read after this wave's loads for it have landed (those of
-  // the steps behind it may still be in flight) and after the barrier that publishes everyone's; the
-  // same barrier says that the stage of step s - 1, which the next loads overwrite, is no longer read.
+  // Step s lives in stages s % NA and s % NB.  A step is PH phases (64-byte group, half of the row blocks); the
+  // reads of the next phase's fragments are spread between the matrix instructions of a phase.  Before the last
+  // phase of a step every wave has read all of its stages: there the wave waits for its own loads of the next step
+  // (BEHIND later ones may still be in flight), the barrier publishes everyone's, and the stages just read are
+  // refilled with steps s + NA and s + NB, these loads too between the matrix instructions: issued together they
+  // stood in front of the next reads (int8, 4096 x 28672 x 4096: 535 us, spread 500 us).
   auto run = [&](int steps) {
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s)
-      if (s < steps) issue(s, s);
-    for (int s = 0; s < steps; ++s) {
-      const int behind = min(NS - 2, steps - 1 - s);
-      if (behind == NS - 2) wait_vmcnt<(NS - 2) * LMIN>();
-      else if (NS > 3 && behind == NS - 3) wait_vmcnt<(NS > 3 ? NS - 3 : 0) * LMIN>();
+    for (int s = 0; s < NB; ++s) {
+      if (s >= steps) continue;
+      if (s < NA) {
+#pragma unroll
+        for (int j = 0; j < JA; ++j) issue_a(s, s, j, std::false_type{});
+      }
+#pragma unroll
+      for (int j = 0; j < JB; ++j) issue_b(s, s, j, std::false_type{});
+    }
+    // step s is about to be read; near the end the loads behind it are fewer
+    auto arrive = [&](int s) {
+      const int behind = steps - 1 - s;
+      if (behind >= NB - 2) wait_vmcnt<BEHIND>();
+      else if (NA == NB && NA > 3 && behind == NA - 3) wait_vmcnt<(NA > 3 ? NA - 3 : 0) * LMIN>();
       else wait_vmcnt<0>();
       __syncthreads();
-      if (s + NS - 1 < steps) issue(s + NS - 1, (s + NS - 1) % NS);
-      compute(s % NS);
+    };
+    if (steps >= NB) wait_vmcnt<BEHIND + LMIN>();
+    else wait_vmcnt<0>();
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < NI + MH; ++r) read_one(0, 0, 0, 0, 0, 0, r);
+    int ca = 0, cb = 0;  // stages of the present step
+    // MID: step s + NB lies within the contraction, so nothing has to be asked
+    auto step = [&](int s, auto parity, auto mid) {
+      constexpr int P = decltype(parity)::value;  // buffers of the step's first phase
+      constexpr bool MID = decltype(mid)::value;
+      const int na = ca + 1 == NA ? 0 : ca + 1, nbs = cb + 1 == NB ? 0 : cb + 1;  // stages of the next step
+#pragma unroll
+      for (int ph = 0; ph < PH; ++ph) {
+        const int abuf = (P * PH + ph) & 1, bbuf = (P * KK + ph / HALVES) & 1;
+        const bool last = ph + 1 == PH;
+        const int nh = (ph + 1) % HALVES, nkk = last ? 0 : (ph + 1) / HALVES;  // the next phase
+        const int reads = nh == 0 ? NI + MH : MH, loads = last && MID ? JA + JB : 0;
+        const bool more = !last || MID || s + 1 < steps;
+        if (last && more) {
+          if constexpr (MID) {
+            wait_vmcnt<BEHIND>();
+            __syncthreads();
+          } else {
+            arrive(s + 1);
+#pragma unroll
+            for (int j = 0; j < JA; ++j)
+              if (s + NA < steps) issue_a(s + NA, ca, j, std::false_type{});
+#pragma unroll
+            for (int j = 0; j < JB; ++j)
+              if (s + NB < steps) issue_b(s + NB, cb, j, std::false_type{});
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int M = MH * NI;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const int i = (ph % HALVES) * MH + m / NI, ni = m % NI;
+          acc[i][ni] = T::mfma(fb[bbuf][ni], fa[abuf][m / NI], acc[i][ni]);
+          // one after each instruction, so that the reads are back before the phase (or the barrier) ends
+          const int n = reads + loads, k0 = n > M ? m * n / M : m, k1 = n > M ? (m + 1) * n / M : (m < n ? m + 1 : m);
+#pragma unroll
+          for (int k = k0; k < k1; ++k) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (k >= reads + JA) issue_b(s + NB, cb, k - reads - JA, std::true_type{});
+            else if (k >= reads) issue_a(s + NA, ca, k - reads, std::true_type{});
+            else if (more) read_one(last ? na : ca, last ? nbs : cb, nkk, nh, abuf ^ 1, bbuf ^ 1, k);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      ca = na;
+      cb = nbs;
+    };
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    int s = 0;
+    for (; s + 1 + NB < full; s += 2) {
+      step(s, even, std::true_type{});
+      step(s + 1, odd, std::true_type{});
     }
+    for (; s + 1 < steps; s += 2) {
+      step(s, even, std::false_type{});
+      step(s + 1, odd, std::false_type{});
+    }
+    if (s < steps) step(s, even, std::false_type{});
   };
   if constexpr (MODE == kDw) {
-    for (pass0 = 0; pass0 < t.rows; pass0 += dw_ids<BM>()) {
-      kd = min(t.rows - pass0, dw_ids<BM>());
-      if (p.a_row_of) {
-        __syncthreads();  // the last pass's indexes and stages are no longer read
-        for (int i = tid; i < kd; i += NW * 64) sRow[i] = p.a_row_of[t.row0 + pass0 + i] / p.a_row_div;
+    for (int pass = 0; pass < t.rows; pass += kDwIds) {
+      kd = min(t.rows - pass, kDwIds);
+      full = kd / CR;
+      __syncthreads();  // the last pass's indexes and stages are no longer read
+      if (gather) {
+        for (int i = tid; i < kd; i += NW * 64) sRow[i] = p.a_row_of[t.row0 + pass + i] / p.a_row_div;
+        __syncthreads();
       }
-      __syncthreads();
       run((kd + CR - 1) / CR);
     }
   } else {
-    run((KD + CR - 1) / CR);
+    run((kd + CR - 1) / CR);
   }
 
   // Epilogue: lane (q, l16) holds columns 4q .. 4q+3 of each 16 x 16 block, of row l16.
   const bool whole = (ND & 3) == 0;  // rows are stored four columns at a time
+  constexpr int NO = EPI == MOE_EPI_SILU_MUL ? NI / 2 : NI;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const int row = wm * (BM / WM) + mi * 16 + l16;
@@ -359,23 +542,27 @@ __global__ __launch_bounds__(WM * WN * 64) void ragged_gemm_kernel(RaggedArgs p)
       at = (size_t)(t.row0 + row) * ND;
     }
     float sa = 1.f;
-    if constexpr (T::kBytes == 1) sa = p.As[sRow[row]];
-    constexpr int NO = EPI == MOE_EPI_SILU_MUL ? NI / 2 : NI;
+    if constexpr (I8) sa = sScaleA[row];
 #pragma unroll
     for (int ni = 0; ni < NO; ++ni) {
       const int col = nb * BC + wn * (BC / WN) + ni * 16 + 4 * q;
       if (col >= ND) continue;
       float v[4], u[4];
+      f32x4 ws = {1.f, 1.f, 1.f, 1.f}, us = ws;
+      if constexpr (I8) {  // the integer sums are exact; one scale a row and a channel
+        ws = *reinterpret_cast<const f32x4*>(&sScaleW[wn * (BN / WN) + ni * 16 + 4 * q]);
+        if constexpr (EPI == MOE_EPI_SILU_MUL)
+          us = *reinterpret_cast<const f32x4*>(&sScaleW[wn * (BN / WN) + (ni + NO) * 16 + 4 * q]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = (float)acc[mi][ni][i];
-        if constexpr (EPI == MOE_EPI_SILU_MUL) u[i] = (float)acc[mi][ni + NO][i];
-        if constexpr (T::kBytes == 1) {  // the integer sums are exact; one scale a row and a channel
-          const float* ws = p.Ws + (size_t)t.e * N + min(col + i, ND - 1);
-          v[i] *= sa * ws[0];
-          if constexpr (EPI == MOE_EPI_SILU_MUL) u[i] *= sa * ws[ND];
+        if constexpr (I8) v[i] *= sa * ws[i];
+        if constexpr (EPI == MOE_EPI_SILU_MUL) {
+          u[i] = (float)acc[mi][ni + NO][i];
+          if constexpr (I8) u[i] *= sa * us[i];
+          v[i] = silu_f32(v[i]) * u[i];
         }
-        if constexpr (EPI == MOE_EPI_SILU_MUL) v[i] = silu_f32(v[i]) * u[i];
       }
       if (whole) {
         store4(p.C, p.out, at + col, v);
@@ -388,21 +575,77 @@ __global__ __launch_bounds__(WM * WN * 64) void ragged_gemm_kernel(RaggedArgs p)
   }
 }
 
+template <class T, int MODE, int EPI, class S0, class S1, class S2>
+__global__ __launch_bounds__(S0::WM * S0::WN * 64) void ragged_gemm_kernel(RaggedArgs p) {
+  constexpr int BM = S0::BM, BN = S0::BN;
+  constexpr int kLds = S0::kLds > S1::kLds ? (S0::kLds > S2::kLds ? S0::kLds : S2::kLds) : (S1::kLds > S2::kLds ? S1::kLds : S2::kLds);
+  constexpr bool I8 = T::kBytes == 1;
+  static_assert(S1::BM == 0 || (S1::BN == BN && S1::WM * S1::WN == S0::WM * S0::WN), "one grid and workgroup size");
+  static_assert(S2::BM == 0 || (S2::BN == BN && S2::WM * S2::WN == S0::WM * S0::WN), "one grid and workgroup size");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  // the 16-bit tiles keep their row indexes in what the last stage later takes, so that the stages may fill the LDS
+  constexpr bool kShareRow = !I8 && MODE != kDw;
+  __shared__ int32_t sRowOwn[MODE == kDw ? kDwIds : (kShareRow ? 1 : BM)];
+  int32_t* sRow = kShareRow ? reinterpret_cast<int32_t*>(smem + kLds - BM * 4) : sRowOwn;
+  __shared__ __attribute__((aligned(16))) float sScaleA[I8 ? (BM < 64 ? 64 : BM) : 1], sScaleW[I8 ? BN : 1];
+  const int N = p.N, K = p.K;
+  const int ND = MODE == kFwd ? (EPI == MOE_EPI_SILU_MUL ? N / 2 : N) : K;  // output columns
+  constexpr int BC = EPI == MOE_EPI_SILU_MUL ? BN / 2 : BN;
+  const int nbn = (ND + BC - 1) / BC;
+  if constexpr (MODE == kDw) {
+    // every expert's tiles are shared evenly by the XCDs (an expert with many rows keeps all of them
+    // busy), each share a piece of the expert's list; fewer than 8 tiles an expert are dealt one by one
+    const int nbm = (N + BM - 1) / BM, per_e = nbm * nbn;
+    const long long b = linear_block();
+    int e, i, mb, nb;
+    if (per_e >= 8) {
+      const int xcd = (int)(b & 7), slots = (per_e + 7) / 8;
+      e = (int)((b >> 3) / slots);
+      i = (int)(((long long)xcd * per_e) >> 3) + (int)((b >> 3) % slots);
+      if (i >= (int)(((long long)(xcd + 1) * per_e) >> 3)) return;
+    } else {
+      e = (int)(b / per_e);
+      i = (int)(b % per_e);
+    }
+    if (e >= p.E) return;
+    band_place(i, nbm, nbn, mb, nb);
+    const int r0 = group_end(p.offsets, e, p.R);
+    const RowTile t{e, r0, max(group_end(p.offsets, e + 1, p.R) - r0, 0), 0};
+    ragged_tile<T, MODE, EPI, S0>(p, t, nb, mb * BM, smem, sRow, sScaleA, sScaleW);
+  } else {
+    RowTile t;
+    int nb;
+    if (!find_row_tile<BM, S1::BM, S2::BM>(p.offsets, p.E, p.R, nbn, t, nb)) return;
+    if (S1::BM == 0 || t.cls == 0) {
+      ragged_tile<T, MODE, EPI, S0>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
+    } else if constexpr (S1::BM > 0) {
+      if (S2::BM == 0 || t.cls == 1) {
+        ragged_tile<T, MODE, EPI, S1>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
+      } else if constexpr (S2::BM > 0) {
+        ragged_tile<T, MODE, EPI, S2>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
+      }
+    }
+  }
+}
+
 // Launch of one configuration.
-template <class T, int MODE, int EPI, int BM, int BN, int WM, int WN, int RB, int NS>
+template <class T, int MODE, int EPI, class S0, class S1 = NoTile, class S2 = NoTile>
 static hipError_t launch_ragged_cfg(const RaggedArgs& a, hipStream_t s) {
+  constexpr int BM = S0::BM, BN = S0::BN;
   const int nd = MODE == kFwd ? (EPI == MOE_EPI_SILU_MUL ? a.N / 2 : a.N) : a.K;
   const int bc = EPI == MOE_EPI_SILU_MUL ? BN / 2 : BN;
-  const int nbn = (nd + bc - 1) / bc;
+  const long long nbn = (nd + bc - 1) / bc;
   dim3 grid;
   if (MODE == kDw) {
     const long long per_e = (long long)((a.N + BM - 1) / BM) * nbn;
     grid = grid2d(per_e >= 8 ? (per_e + 7) / 8 * 8 * a.E : per_e * a.E);
   } else {
-    const int tiles = a.offsets ? a.R / BM + (a.E < a.R ? a.E : a.R) : (a.R + BM - 1) / BM;
-    grid = mm_grid(nbn, tiles);
+    // most row tiles that any groups of R rows give, and up to one more a list and XCD by the shares' rounding
+    const long long m = a.offsets ? (a.E < a.R ? a.E : a.R) : 1;
+    const long long tiles = a.R / BM + (S2::BM > 0 ? 2 * m : m);
+    grid = grid2d(8 * ((tiles * nbn + 7) / 8 + (S1::BM > 0 ? 3 : 0)));
   }
-  ragged_gemm_kernel<T, MODE, EPI, BM, BN, WM, WN, RB, NS><<<grid, WM * WN * 64, 0, s>>>(a);
+  ragged_gemm_kernel<T, MODE, EPI, S0, S1, S2><<<grid, S0::WM * S0::WN * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -10,29 +10,29 @@ namespace moe {
 // Tile choice by the mean rows of a group (groups without rows count, as the host knows no better).
 template <class T, int EPI>
 static hipError_t launch_fwd(const RaggedArgs& a, hipStream_t s) {
-  const long long mean = a.offsets ? ((long long)a.R + a.E - 1) / a.E : a.R;
-  if (mean <= 16) return launch_ragged_cfg<T, kFwd, EPI, 16, 128, 1, 4, 128, 4>(a, s);
-  if (mean <= 32) return launch_ragged_cfg<T, kFwd, EPI, 32, 128, 1, 4, 128, 3>(a, s);
-  if (mean <= 64) return launch_ragged_cfg<T, kFwd, EPI, 64, 128, 1, 4, 128, 3>(a, s);
-  if (mean <= 256) return launch_ragged_cfg<T, kFwd, EPI, 128, 128, 2, 2, 64, 4>(a, s);
-  return launch_ragged_cfg<T, kFwd, EPI, 256, 256, 2, 4, 64, 4>(a, s);
+  const long long mean = ((long long)a.R + a.E - 1) / a.E;
+  if (mean <= 16) return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 128, 1, 4, 128, 4>>(a, s);
+  if (mean <= 32) return launch_ragged_cfg<T, kFwd, EPI, TileShape<32, 128, 1, 4, 128, 3>>(a, s);
+  if (mean <= 64) return launch_ragged_cfg<T, kFwd, EPI, TileShape<64, 128, 1, 4, 128, 3>>(a, s);
+  if (mean <= 256) return launch_ragged_cfg<T, kFwd, EPI, TileShape<128, 128, 2, 2, 64, 4>>(a, s);
+  return launch_ragged_cfg<T, kFwd, EPI, TileShape<256, 256, 2, 4, 128, 2, 3>, TileShape<128, 256, 2, 4, 128, 3>>(a, s);
 }
 
 template <class T>
 static hipError_t launch_dx(const RaggedArgs& a, hipStream_t s) {
   const long long mean = ((long long)a.R + a.E - 1) / a.E;
-  if (mean <= 16) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 16, 128, 1, 4, 128, 4>(a, s);
-  if (mean <= 32) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 32, 128, 1, 4, 128, 3>(a, s);
-  if (mean <= 64) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 64, 128, 1, 4, 128, 3>(a, s);
-  if (mean <= 256) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 128, 128, 2, 2, 64, 4>(a, s);
-  return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, 256, 256, 2, 4, 64, 4>(a, s);
+  if (mean <= 16) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<16, 128, 1, 4, 128, 4>>(a, s);
+  if (mean <= 32) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<32, 128, 1, 4, 128, 3>>(a, s);
+  if (mean <= 64) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<64, 128, 1, 4, 128, 3>>(a, s);
+  if (mean <= 256) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<128, 128, 2, 2, 64, 4>>(a, s);
+  return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<256, 256, 2, 4, 64, 4>>(a, s);
 }
 
 template <class T>
 static hipError_t launch_dw(const RaggedArgs& a, hipStream_t s) {
   const long long mean = ((long long)a.R + a.E - 1) / a.E;
-  if (mean <= 256) return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, 128, 128, 2, 2, 64, 3>(a, s);
-  return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, 256, 256, 2, 4, 64, 4>(a, s);
+  if (mean <= 256) return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<128, 128, 2, 2, 64, 3>>(a, s);
+  return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<256, 256, 2, 4, 64, 4>>(a, s);
 }
 
 template <class T>
