@@ -122,19 +122,9 @@ hipError_t launch_i8_quant(const void* x, int in_dtype, int rows, int K, int8_t*
   return launch_quant<MOE_IN_BF16>(x, rows, K, q, s, stream);
 }
 
-// Tile choice by the mean rows of a group.
-template <int EPI>
-static hipError_t launch_i8(const RaggedArgs& a, hipStream_t s) {
-  const long long mean = ((long long)a.R + a.E - 1) / a.E;
-  if (mean <= 16) return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<16, 128, 1, 4, 128, 4>>(a, s);
-  if (mean <= 32) return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<32, 128, 1, 4, 128, 3>>(a, s);
-  if (mean <= 64) return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<64, 128, 1, 4, 128, 3>>(a, s);
-  if (mean <= 256) return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<128, 128, 2, 2, 64, 4>>(a, s);
-  return launch_ragged_cfg<ElemI8, kFwd, EPI, TileShape<256, 256, 2, 4, 128, 2>, TileShape<128, 256, 2, 4, 128, 2>>(a, s);
-}
-
 hipError_t launch_ragged_i8(const RaggedArgs& a, int epilogue, hipStream_t stream) {
-  return epilogue == MOE_EPI_SILU_MUL ? launch_i8<MOE_EPI_SILU_MUL>(a, stream) : launch_i8<MOE_EPI_NONE>(a, stream);
+  return epilogue == MOE_EPI_SILU_MUL ? launch_ragged_fwd<ElemI8, MOE_EPI_SILU_MUL>(a, stream)
+                                      : launch_ragged_fwd<ElemI8, MOE_EPI_NONE>(a, stream);
 }
 
 }  // namespace moe

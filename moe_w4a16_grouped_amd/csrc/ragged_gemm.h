@@ -145,25 +145,26 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
   return v;
 }
 
-// Finds the workgroup's row tile and column block from the offsets: every wave counts the tiles of E / 64
-// experts a lane, scans the counts over its lanes and walks the experts of the lane that holds the wanted
-// tile.  Offsets are clamped to [0, R], so no list of offsets leads out of the rows.
-template <int H0, int H1, int H2>
-__device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ off, int E, int R, int nbn, RowTile& t, int& nb) {
+// Finds the workgroup's row tile and column block from the offsets: every wave takes PER consecutive experts a
+// lane (all their offsets in one round trip), counts their tiles, scans the counts over its lanes, and the lane
+// that holds the wanted tile finds its expert.  Offsets are clamped to [0, R], so no list of offsets leads out
+// of the rows.
+template <int H0, int H1, int H2, int PER>
+__device__ __forceinline__ bool find_row_tile_per(const int32_t* __restrict__ off, int E, int R, int nbn, RowTile& t, int& nb) {
   const int lane = threadIdx.x & 63;
-  const int per = off ? (E + 63) / 64 : 1;
-  const int e0 = min(lane * per, E), e1 = min(e0 + per, E);
-  // without offsets one group holds all rows
-  auto end_of = [&](int e) { return off ? group_end(off, e, R) : (e > 0 ? R : 0); };
-  int at = end_of(e0);
+  int end[PER + 1];  // offsets of this lane's experts; past the last expert the groups are empty
+#pragma unroll
+  for (int i = 0; i <= PER; ++i) {
+    const int e = min(lane * PER + i, E);
+    end[i] = off ? group_end(off, e, R) : (e > 0 ? R : 0);  // without offsets one group holds all rows
+  }
   TileCount n{0, 0, 0};
-  for (int e = e0; e < e1; ++e) {
-    const int end = end_of(e + 1);
-    const TileCount c = count_tiles<H0, H1, H2>(max(end - at, 0));
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const TileCount c = count_tiles<H0, H1, H2>(max(end[i + 1] - end[i], 0));
     n.n0 += c.n0;
     n.n1 += c.n1;
     n.n2 += c.n2;
-    at = end;
   }
   long long j = linear_block() >> 3, item;
   int incl = wave_scan(n.n0, lane), mine = n.n0, cls = 0;
@@ -178,23 +179,42 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ off, i
   }
   const int place = (int)(item / nbn);  // names the expert: its tiles x nbn items follow each other
   const int src = __builtin_ctzll(__ballot(incl > place));  // place < total: some lane's sum is past it
-  int before = __builtin_amdgcn_readlane(incl, src) - __builtin_amdgcn_readlane(mine, src);  // tiles before expert e
-  int e = src * per;
-  at = end_of(e);
-  for (;; ++e) {
-    const int end = end_of(e + 1);
-    const TileCount c = count_tiles<H0, H1, H2>(max(end - at, 0));
+  // every lane walks its own experts; lane src's answer counts
+  int before = incl - mine, at_i = 0, at_before = before, at_nt = 0, r0 = 0, r1 = 0, full0 = 0, half0 = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const TileCount c = count_tiles<H0, H1, H2>(max(end[i + 1] - end[i], 0));
     const int nt = cls == 0 ? c.n0 : (cls == 1 ? c.n1 : c.n2);
-    if (place < before + nt || e == E - 1) {
-      int tile;
-      band_place(item - (long long)before * nbn, nt, nbn, tile, nb);
-      const int r0 = at + (cls == 0 ? tile : c.n0) * H0 + (cls == 2 ? c.n1 * H1 : 0);
-      t = RowTile{e, r0, min(cls == 0 ? H0 : (cls == 1 ? H1 : H2), end - r0), cls};
-      return true;
-    }
+    if (i == 0 || before <= place) at_i = i, at_before = before, at_nt = nt, r0 = end[i], r1 = end[i + 1], full0 = c.n0, half0 = c.n1;
     before += nt;
-    at = end;
   }
+  at_i = __builtin_amdgcn_readlane(at_i, src);
+  at_before = __builtin_amdgcn_readlane(at_before, src);
+  at_nt = __builtin_amdgcn_readlane(at_nt, src);
+  r0 = __builtin_amdgcn_readlane(r0, src);
+  r1 = __builtin_amdgcn_readlane(r1, src);
+  int tile;
+  band_place(item - (long long)at_before * nbn, at_nt, nbn, tile, nb);
+  int first = tile * H0, high = H0;
+  if (H1 > 0 && cls > 0) {
+    first = __builtin_amdgcn_readlane(full0, src) * H0;
+    high = H1;
+    if (H2 > 0 && cls == 2) {
+      first += __builtin_amdgcn_readlane(half0, src) * H1;
+      high = H2;
+    }
+  }
+  t = RowTile{src * PER + at_i, r0 + first, min(high, r1 - r0 - first), cls};
+  return true;
+}
+
+template <int H0, int H1, int H2>
+__device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ off, int E, int R, int nbn, RowTile& t, int& nb) {
+  if (E <= 64) return find_row_tile_per<H0, H1, H2, 1>(off, E, R, nbn, t, nb);
+  if (E <= 128) return find_row_tile_per<H0, H1, H2, 2>(off, E, R, nbn, t, nb);
+  if (E <= 256) return find_row_tile_per<H0, H1, H2, 4>(off, E, R, nbn, t, nb);
+  if (E <= 512) return find_row_tile_per<H0, H1, H2, 8>(off, E, R, nbn, t, nb);
+  return find_row_tile_per<H0, H1, H2, MOE_MAX_EXPERTS / 64>(off, E, R, nbn, t, nb);
 }
 
 __device__ __forceinline__ void store4(void* C, int out, size_t at, const float (&v)[4]) {
@@ -227,7 +247,8 @@ struct NoTile {
 };
 
 // One output tile: rows t (DW: weight rows from m0) by column block nb.
-template <class T, int MODE, int EPI, class S>
+// LATE: the scales are loaded after the contraction, into the first stages (int8 tiles whose stages fill the LDS).
+template <class T, int MODE, int EPI, class S, bool LATE>
 __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& t, int nb, int m0, uint8_t* smem, int32_t* sRow,
                                             float* sScaleA, float* sScaleW) {
   constexpr int BM = S::BM, BN = S::BN, WM = S::WM, WN = S::WN, RB = S::RB, NA = S::NA, NB = S::NB;
@@ -243,7 +264,9 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   // loads behind those of the next step when it is about to be read (see run)
   constexpr int BEHIND = (NA - 2) * LMIN + (NB > NA ? LB / NW : 0);
   static_assert(EPI != MOE_EPI_SILU_MUL || (MODE == kFwd && NI % 2 == 0), "SiLU*mul pairs gate and up blocks");
+  static_assert((!I8 || BN % 64 == 0) && (!B_T || BN >= 128) && (!A_T || BM >= 128), "scales are loaded by 64 columns, windows permuted by 8");
   static_assert(!I8 || MODE == kFwd, "transposing reads are of 16-bit elements");
+  static_assert(BM <= NW * 64 && (RB == 64 || RB == 128), "rows");
   static_assert(SA % 1024 == 0 && SB % 1024 == 0 && LMIN >= 1 && BEHIND < 64 && NA >= 2 && NB - NA <= 1 && NB >= NA && NW % 2 == 0, "loads");
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -254,10 +277,12 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   // output columns and contraction length
   const int ND = MODE == kFwd ? (EPI == MOE_EPI_SILU_MUL ? N / 2 : N) : K;
   constexpr int BC = EPI == MOE_EPI_SILU_MUL ? BN / 2 : BN;  // output columns of a tile
+  int my_row = 0;  // the activation row of tile row tid
   if constexpr (MODE != kDw) {
-    for (int i = tid; i < BM; i += NW * 64) {  // padding rows repeat the tile's first row
-      const int r = t.row0 + (i < t.rows ? i : 0);
-      sRow[i] = MODE == kFwd && p.a_row_of ? p.a_row_of[r] / p.a_row_div : r;
+    if (tid < BM) {  // padding rows repeat the tile's first row
+      const int r = t.row0 + (tid < t.rows ? tid : 0);
+      my_row = MODE == kFwd && p.a_row_of ? p.a_row_of[r] / p.a_row_div : r;
+      sRow[tid] = my_row;
     }
     __syncthreads();
   }
@@ -278,12 +303,13 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
     const int n = nb * BN + nt;
     return n < N ? n : 0;
   };
-  if constexpr (I8) {  // the tile's scales, for the epilogue: older than every load of a stage
-    for (int i = wave; i < (BM + 63) / 64; i += NW)
-      g2lds4_at(p.As + sRow[min(i * 64 + lane, BM - 1)], lds_address(sScaleA) + i * 256);
+  // the tile's scales, for the epilogue
+  auto load_scales = [&]() {
+    if (wave < (BM + 63) / 64) g2lds4_at(p.As + my_row, lds_address(sScaleA) + wave * 256);
     for (int i = wave; i < BN / 64; i += NW)
       g2lds4_at(p.Ws + (size_t)t.e * N + weight_row(i * 64 + lane), lds_address(sScaleW) + i * 256);
-  }
+  };
+  if constexpr (I8 && !LATE) load_scales();  // older than every load of a stage
 
   // Sources of this wave's loads; load j of an operand is its wave-wide load wave + NW * j of a step.
   // Rows kind: lane's chunk at row (wave + NW j) * 1024 / RB + lane / (RB / 16), contraction byte pos in the step
@@ -332,7 +358,7 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   }
   const size_t step_a = MODE == kDw ? (size_t)CR * N * 2 : RB, step_b = MODE == kFwd ? RB : (size_t)CR * K * 2;
 
-  if constexpr (!I8 && MODE != kDw) __syncthreads();  // every wave has its rows: the stages may be filled
+  if constexpr ((!I8 || LATE) && MODE != kDw) __syncthreads();  // every wave has its rows: the stages may be filled
 
   // contraction elements of this pass (DW: rows of the expert, as many at a time as sRow holds) and its full steps
   int kd = MODE == kFwd ? K : N;
@@ -403,7 +429,7 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
 
   // Fragments of one 64-byte group of a stage: the tile columns, and one half of the wave's row blocks.
   constexpr int KK = RB / 64;  // 64-byte groups of a step
-  constexpr int HALVES = MI >= 2 ? 2 : 1, MH = MI / HALVES;
+  constexpr int HALVES = MI % 2 == 0 ? 2 : 1, MH = MI / HALVES;
   constexpr int PH = KK * HALVES;  // phases of a step
   u32x4 fa[2][MH], fb[2][NI];
   // Read r of a phase's fragments: its NI column blocks first where it starts a group, then its MH row blocks.
@@ -527,43 +553,82 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
     run((kd + CR - 1) / CR);
   }
 
+  if constexpr (I8 && LATE) {
+    __syncthreads();  // the stages are no longer read
+    load_scales();
+    wait_vmcnt<0>();
+    __syncthreads();
+  }
   // Epilogue: lane (q, l16) holds columns 4q .. 4q+3 of each 16 x 16 block, of row l16.
-  const bool whole = (ND & 3) == 0;  // rows are stored four columns at a time
   constexpr int NO = EPI == MOE_EPI_SILU_MUL ? NI / 2 : NI;
+  auto results = [&](int mi, int ni, float sa, float (&v)[4]) {
+    f32x4 ws = {1.f, 1.f, 1.f, 1.f}, us = ws;
+    if constexpr (I8) {  // the integer sums are exact; one scale a row and a channel
+      ws = *reinterpret_cast<const f32x4*>(&sScaleW[wn * (BN / WN) + ni * 16 + 4 * q]);
+      if constexpr (EPI == MOE_EPI_SILU_MUL)
+        us = *reinterpret_cast<const f32x4*>(&sScaleW[wn * (BN / WN) + (ni + NO) * 16 + 4 * q]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = (float)acc[mi][ni][i];
+      if constexpr (I8) v[i] *= sa * ws[i];
+      if constexpr (EPI == MOE_EPI_SILU_MUL) {
+        float u = (float)acc[mi][ni + NO][i];
+        if constexpr (I8) u *= sa * us[i];
+        v[i] = silu_f32(v[i]) * u;
+      }
+    }
+  };
+  const int rows = MODE == kDw ? min(N - m0, BM) : t.rows;
+  const size_t first = MODE == kDw ? w_e + (size_t)m0 * K : (size_t)t.row0 * ND;  // the tile's first row in C
+  // 16-bit results of the higher tiles pass through LDS (the stages are free) and are stored as whole rows, 16
+  // bytes a lane; stored from the registers they are 32-byte pieces of 16 rows (weight gradients of 256 experts of
+  // 1024 x 2048 over 800 tokens: 385 us, staged 296 us).  After SiLU*mul, whose arithmetic covers the stores, the
+  // detour costs more than it gains (int8 gate_up, 256 x 256 tiles of 512 experts: 430 -> 460 us).
+  constexpr bool kStaged = EPI == MOE_EPI_NONE && BM >= 64 && (LATE ? 4 * (BM + BN) : 0) + BM * BC * 2 <= S::kLds;
+  if (kStaged && p.out != MOE_OUT_F32 && (ND & 7) == 0) {
+    constexpr int NCH = BC / 8;  // 16-byte chunks of a row, permuted by the row's number
+    uint8_t* buf = smem + (LATE ? 4 * (BM + BN) : 0);
+    __syncthreads();
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      const int row = wm * (BM / WM) + mi * 16 + l16;
+      const float sa = I8 ? sScaleA[row] : 1.f;
+#pragma unroll
+      for (int ni = 0; ni < NO; ++ni) {
+        float v[4];
+        results(mi, ni, sa, v);
+        const int chunk = (wn * (BC / WN) + ni * 16) / 8 + (q >> 1);
+        u16x4 b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = p.out == MOE_OUT_F16 ? f32_to_f16_bits(v[i]) : f32_to_bf16_bits(v[i]);
+        *reinterpret_cast<u16x4*>(buf + row * (BC * 2) + ((chunk ^ (row & (NCH - 1) & 15)) * 16) + (q & 1) * 8) = b;
+      }
+    }
+    __syncthreads();
+    uint16_t* C = static_cast<uint16_t*>(p.C) + first + nb * BC;
+    const int cols = min(BC, ND - nb * BC);
+#pragma unroll 4
+    for (int i = tid; i < BM * NCH; i += NW * 64) {
+      const int row = i / NCH, chunk = i % NCH;
+      const u32x4 w = *reinterpret_cast<const u32x4*>(buf + row * (BC * 2) + ((chunk ^ (row & (NCH - 1) & 15)) * 16));
+      if (row < rows && chunk * 8 < cols) *reinterpret_cast<u32x4*>(C + (size_t)row * ND + chunk * 8) = w;
+    }
+    return;
+  }
+  const bool whole = (ND & 3) == 0;  // rows are stored four columns at a time
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const int row = wm * (BM / WM) + mi * 16 + l16;
-    size_t at;
-    if constexpr (MODE == kDw) {
-      if (m0 + row >= N) continue;
-      at = w_e + (size_t)(m0 + row) * K;
-    } else {
-      if (row >= t.rows) continue;
-      at = (size_t)(t.row0 + row) * ND;
-    }
-    float sa = 1.f;
-    if constexpr (I8) sa = sScaleA[row];
+    if (row >= rows) continue;
+    const size_t at = first + (size_t)row * ND;
+    const float sa = I8 ? sScaleA[row] : 1.f;
 #pragma unroll
     for (int ni = 0; ni < NO; ++ni) {
       const int col = nb * BC + wn * (BC / WN) + ni * 16 + 4 * q;
       if (col >= ND) continue;
-      float v[4], u[4];
-      f32x4 ws = {1.f, 1.f, 1.f, 1.f}, us = ws;
-      if constexpr (I8) {  // the integer sums are exact; one scale a row and a channel
-        ws = *reinterpret_cast<const f32x4*>(&sScaleW[wn * (BN / WN) + ni * 16 + 4 * q]);
-        if constexpr (EPI == MOE_EPI_SILU_MUL)
-          us = *reinterpret_cast<const f32x4*>(&sScaleW[wn * (BN / WN) + (ni + NO) * 16 + 4 * q]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = (float)acc[mi][ni][i];
-        if constexpr (I8) v[i] *= sa * ws[i];
-        if constexpr (EPI == MOE_EPI_SILU_MUL) {
-          u[i] = (float)acc[mi][ni + NO][i];
-          if constexpr (I8) u[i] *= sa * us[i];
-          v[i] = silu_f32(v[i]) * u[i];
-        }
-      }
+      float v[4];
+      results(mi, ni, sa, v);
       if (whole) {
         store4(p.C, p.out, at + col, v);
       } else {
@@ -583,11 +648,16 @@ __global__ __launch_bounds__(S0::WM * S0::WN * 64) void ragged_gemm_kernel(Ragge
   static_assert(S1::BM == 0 || (S1::BN == BN && S1::WM * S1::WN == S0::WM * S0::WN), "one grid and workgroup size");
   static_assert(S2::BM == 0 || (S2::BN == BN && S2::WM * S2::WN == S0::WM * S0::WN), "one grid and workgroup size");
   __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
-  // the 16-bit tiles keep their row indexes in what the last stage later takes, so that the stages may fill the LDS
-  constexpr bool kShareRow = !I8 && MODE != kDw;
+  // the row indexes lie in what the last stage later takes, so that the stages may fill the LDS; int8 tiles keep
+  // room for the scales where there is any
+  constexpr bool kLate = I8 && kLds + BM * 4 + (BM < 64 ? 64 : BM) * 4 + BN * 4 > 160 * 1024;
+  constexpr bool kShareRow = (!I8 || kLate) && MODE != kDw;
   __shared__ int32_t sRowOwn[MODE == kDw ? kDwIds : (kShareRow ? 1 : BM)];
   int32_t* sRow = kShareRow ? reinterpret_cast<int32_t*>(smem + kLds - BM * 4) : sRowOwn;
-  __shared__ __attribute__((aligned(16))) float sScaleA[I8 ? (BM < 64 ? 64 : BM) : 1], sScaleW[I8 ? BN : 1];
+  constexpr bool kOwnScales = I8 && !kLate;
+  __shared__ __attribute__((aligned(16))) float sScaleOwn[kOwnScales ? (BM < 64 ? 64 : BM) + BN : 1];
+  float* sScaleA = I8 && kLate ? reinterpret_cast<float*>(smem) : sScaleOwn;
+  float* sScaleW = sScaleA + (BM < 64 ? 64 : BM);
   const int N = p.N, K = p.K;
   const int ND = MODE == kFwd ? (EPI == MOE_EPI_SILU_MUL ? N / 2 : N) : K;  // output columns
   constexpr int BC = EPI == MOE_EPI_SILU_MUL ? BN / 2 : BN;
@@ -611,21 +681,28 @@ __global__ __launch_bounds__(S0::WM * S0::WN * 64) void ragged_gemm_kernel(Ragge
     band_place(i, nbm, nbn, mb, nb);
     const int r0 = group_end(p.offsets, e, p.R);
     const RowTile t{e, r0, max(group_end(p.offsets, e + 1, p.R) - r0, 0), 0};
-    ragged_tile<T, MODE, EPI, S0>(p, t, nb, mb * BM, smem, sRow, sScaleA, sScaleW);
+    ragged_tile<T, MODE, EPI, S0, kLate>(p, t, nb, mb * BM, smem, sRow, sScaleA, sScaleW);
   } else {
     RowTile t;
     int nb;
     if (!find_row_tile<BM, S1::BM, S2::BM>(p.offsets, p.E, p.R, nbn, t, nb)) return;
     if (S1::BM == 0 || t.cls == 0) {
-      ragged_tile<T, MODE, EPI, S0>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
+      ragged_tile<T, MODE, EPI, S0, kLate>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
     } else if constexpr (S1::BM > 0) {
       if (S2::BM == 0 || t.cls == 1) {
-        ragged_tile<T, MODE, EPI, S1>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
+        ragged_tile<T, MODE, EPI, S1, kLate>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
       } else if constexpr (S2::BM > 0) {
-        ragged_tile<T, MODE, EPI, S2>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
+        ragged_tile<T, MODE, EPI, S2, kLate>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
       }
     }
   }
+}
+
+// Whether tiles of bm rows by bc of nd columns give every CU a workgroup (estimated: the host does not know the
+// groups' sizes).
+static inline bool fills(const RaggedArgs& a, int bm, int nd, int bc) {
+  const long long groups = a.E < a.R ? a.E : a.R, tiles = a.R / bm > groups ? a.R / bm : groups;
+  return tiles * ((nd + bc - 1) / bc) >= 192;
 }
 
 // Launch of one configuration.
@@ -647,6 +724,31 @@ static hipError_t launch_ragged_cfg(const RaggedArgs& a, hipStream_t s) {
   }
   ragged_gemm_kernel<T, MODE, EPI, S0, S1, S2><<<grid, S0::WM * S0::WN * 64, 0, s>>>(a);
   return hipGetLastError();
+}
+
+// Tile choice of the forward product, by the mean rows of a group (groups without rows count, as the host knows
+// no better).  Measured with weights from HBM, TB/s of weights or PFLOP/s, 64 experts of 1024 x 2048 unless said:
+//   mean   1: 16 x 64 tiles with 2 stages (8 workgroups a CU) against 16 x 128 with 4: int8, 53 of 128 experts of
+//             1536 x 2048, 5.2 against 4.6 TB/s; fp16 5.1 against 4.9;
+//   mean  25: 32 x 128 against 64 x 128: int8 4.6 against 4.3, fp16 5.5 against 5.5 (256 experts);
+//   mean  50: 64 x 128 against 32 x 128: int8 4.4 against 3.5, fp16 3.8 against 3.3;
+//   mean 100: 64 x 128 against 256 x 256: fp16 0.29 against 0.29, int8 0.60 against 0.59;
+//   mean 200: 256 x 256 against 64 x 128: fp16 0.53 against 0.47, int8 0.88 against 0.87;
+//   mean 400: fp16 0.79 against 0.60, int8 1.33 against 1.10.
+// A tile that would leave CUs idle gives way to a smaller one: one group of 77 rows, 1536 columns: 6.4 us with 16-row
+// tiles, 12.3 us with 64.
+template <class T, int EPI>
+static hipError_t launch_ragged_fwd(const RaggedArgs& a, hipStream_t s) {
+  const long long mean = ((long long)a.R + a.E - 1) / a.E;
+  const int cols = EPI == MOE_EPI_SILU_MUL ? 2 : 1;  // weight rows per output column
+  if (mean > 128 && fills(a, 256, a.N, 256))
+    return launch_ragged_cfg<T, kFwd, EPI, TileShape<256, 256, 2, 4, 128, 2, 3>, TileShape<128, 256, 2, 4, 128, 3>>(a, s);
+  if (mean > 32 && fills(a, 64, a.N / cols, 128 / cols))
+    return launch_ragged_cfg<T, kFwd, EPI, TileShape<64, 128, 1, 4, 128, 2>>(a, s);
+  if (mean > 16 && fills(a, 32, a.N / cols, 128 / cols))
+    return launch_ragged_cfg<T, kFwd, EPI, TileShape<32, 128, 1, 4, 128, 2>>(a, s);
+  if (fills(a, 16, a.N / cols, 64 / cols)) return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 2>>(a, s);
+  return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 4>>(a, s);
 }
 
 }  // namespace moe

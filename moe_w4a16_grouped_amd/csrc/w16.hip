@@ -7,31 +7,29 @@
 
 namespace moe {
 
-// Tile choice by the mean rows of a group (groups without rows count, as the host knows no better).
-template <class T, int EPI>
-static hipError_t launch_fwd(const RaggedArgs& a, hipStream_t s) {
-  const long long mean = ((long long)a.R + a.E - 1) / a.E;
-  if (mean <= 16) return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 128, 1, 4, 128, 4>>(a, s);
-  if (mean <= 32) return launch_ragged_cfg<T, kFwd, EPI, TileShape<32, 128, 1, 4, 128, 3>>(a, s);
-  if (mean <= 64) return launch_ragged_cfg<T, kFwd, EPI, TileShape<64, 128, 1, 4, 128, 3>>(a, s);
-  if (mean <= 256) return launch_ragged_cfg<T, kFwd, EPI, TileShape<128, 128, 2, 2, 64, 4>>(a, s);
-  return launch_ragged_cfg<T, kFwd, EPI, TileShape<256, 256, 2, 4, 128, 2, 3>, TileShape<128, 256, 2, 4, 128, 3>>(a, s);
-}
-
+// Tile choice of the gradients, by the mean rows of a group.  Measured (fp16, weights from HBM): row gradients of 256
+// experts of 1024 x 2048 with 25 rows 195 us with 64 x 256 tiles, 206 us with 32 x 256, 226 us with 32 x 128; 64
+// experts, mean 200: 97 us with 128 x 256 (two workgroups a CU) against 99 us with 256 x 256 and 109 with 64 x 256;
+// mean 400: 143 against 159 and 181; mean 1024 (8 experts of 4096 x 14336): 1085 against 1010.
 template <class T>
 static hipError_t launch_dx(const RaggedArgs& a, hipStream_t s) {
   const long long mean = ((long long)a.R + a.E - 1) / a.E;
-  if (mean <= 16) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<16, 128, 1, 4, 128, 4>>(a, s);
-  if (mean <= 32) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<32, 128, 1, 4, 128, 3>>(a, s);
-  if (mean <= 64) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<64, 128, 1, 4, 128, 3>>(a, s);
-  if (mean <= 256) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<128, 128, 2, 2, 64, 4>>(a, s);
-  return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<256, 256, 2, 4, 64, 4>>(a, s);
+  if (mean > 512 && fills(a, 256, a.K, 256)) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<256, 256, 2, 4, 64, 4>>(a, s);
+  if (mean > 64 && fills(a, 128, a.K, 256))
+    return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<128, 256, 1, 4, 64, 3>, TileShape<64, 256, 1, 4, 64, 3>>(a, s);
+  if (fills(a, 64, a.K, 256)) return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<64, 256, 1, 4, 64, 2>>(a, s);
+  return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<16, 128, 1, 4, 128, 4>>(a, s);
 }
 
+// Weight gradients of 64 experts of 1024 x 2048, mean 100: 84 us with 256 x 128 tiles (two workgroups a CU), 83 us
+// with 128 x 128, 93 us with 256 x 256; mean 400: 162, 170, 166; mean 1024 (8 experts of 4096 x 14336): 1239 against
+// 1173 us with 256 x 256.
 template <class T>
 static hipError_t launch_dw(const RaggedArgs& a, hipStream_t s) {
   const long long mean = ((long long)a.R + a.E - 1) / a.E;
-  if (mean <= 256) return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<128, 128, 2, 2, 64, 3>>(a, s);
+  const long long tiles = (long long)a.E * ((a.N + 255) / 256) * ((a.K + 127) / 128);
+  if (tiles < 512) return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<128, 128, 2, 2, 64, 3>>(a, s);
+  if (mean <= 512) return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<256, 128, 2, 2, 64, 3>>(a, s);
   return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<256, 256, 2, 4, 64, 4>>(a, s);
 }
 
@@ -39,8 +37,8 @@ template <class T>
 static hipError_t launch_w16(const RaggedArgs& a, int mode, int epilogue, hipStream_t s) {
   if (mode == kDw) return launch_dw<T>(a, s);
   if (mode == kDx) return launch_dx<T>(a, s);
-  if (epilogue == MOE_EPI_SILU_MUL) return launch_fwd<T, MOE_EPI_SILU_MUL>(a, s);
-  return launch_fwd<T, MOE_EPI_NONE>(a, s);
+  if (epilogue == MOE_EPI_SILU_MUL) return launch_ragged_fwd<T, MOE_EPI_SILU_MUL>(a, s);
+  return launch_ragged_fwd<T, MOE_EPI_NONE>(a, s);
 }
 
 hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilogue, hipStream_t stream) {
