@@ -685,14 +685,17 @@ _ACT = tuple(_IN)
 
 def _need(t, dtypes, shape, name, dev=None):
     """A contiguous GPU tensor of one of the dtypes and of this shape (None = any size), on dev."""
-    d = t.device
-    if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous() or (dev is not None and d != dev):
-        raise ValueError(f"{name} must be a contiguous {' or '.join(str(x) for x in dtypes)} CUDA tensor"
-                         f"{'' if dev is None else f' on {dev}'} (got {t.dtype}, {d})")
     s = t.shape
-    if len(s) != len(shape) or any(w is not None and g != w for g, w in zip(s, shape)):
+    if t.dtype in dtypes and t.is_cuda and t.is_contiguous() and (dev is None or t.device == dev):
+        if len(s) == len(shape):
+            for got, want in zip(s, shape):
+                if want is not None and got != want:
+                    break
+            else:
+                return s
         raise ValueError(f"{name} must have the shape {shape} (got {tuple(s)})")
-    return s
+    raise ValueError(f"{name} must be a contiguous {' or '.join(str(x) for x in dtypes)} CUDA tensor"
+                     f"{'' if dev is None else f' on {dev}'} (got {t.dtype}, {t.device})")
 
 
 def _call(fn, dev, stream, made, *args):
@@ -708,7 +711,7 @@ def _call(fn, dev, stream, made, *args):
         for t in made:
             if t is not None:
                 t.record_stream(stream)
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -792,12 +795,15 @@ def moe_linear_i8(x, Wq, Ws, epilogue: int = MOE_EPI_NONE, out_dtype: int = MOE_
     N, _ = _need(Wq, _I8, (None, K), "Wq", dev)
     _need(Ws, _F32, (N,), "Ws", dev)
     y = _out(y, (T, _cols(N, epilogue)), out_dtype, dev, "y")
-    if workspace is None:
-        workspace = torch.empty(max(moe_linear_i8_workspace_bytes(T, K), 256), dtype=torch.uint8, device=dev)
+    lib, size = load(), 0
+    if workspace is not None:
+        size, = _need(workspace, _U8, (None,), "workspace", dev)
     else:
-        _need(workspace, _U8, (None,), "workspace", dev)
-    _call(load().moe_linear_i8, dev, stream, (y, workspace), x.data_ptr(), _IN[x.dtype], Wq.data_ptr(), Ws.data_ptr(), T, N,
-          K, epilogue, y.data_ptr(), out_dtype, workspace.data_ptr(), workspace.numel())
+        size = lib.moe_linear_i8_workspace_bytes(T, K)
+        if size:
+            workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
+    _call(lib.moe_linear_i8, dev, stream, (y, workspace), x.data_ptr(), _IN[x.dtype], Wq.data_ptr(), Ws.data_ptr(), T, N, K,
+          epilogue, y.data_ptr(), out_dtype, _ptr(workspace), size)
     return y
 
 

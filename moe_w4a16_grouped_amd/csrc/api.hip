@@ -1526,7 +1526,7 @@ moe_status_t moe_gemm_i8(const int8_t* Aq, const float* As, const int8_t* Wq, co
 
 size_t moe_linear_i8_workspace_bytes(int32_t T, int32_t K) {
   if (T < 0 || K < 16 || K % 16 != 0 || (int64_t)T >= kMaxRows || K > MOE_I8_MAX_K) return 0;
-  return up256((size_t)T * K) + up256((size_t)T * 4);
+  return moe::i8_few_fits(T, K) ? 0 : up256((size_t)T * K) + up256((size_t)T * 4);
 }
 
 moe_status_t moe_linear_i8(const void* x, int32_t in_dtype, const int8_t* Wq, const float* Ws, int32_t T, int32_t N,
@@ -1536,11 +1536,18 @@ moe_status_t moe_linear_i8(const void* x, int32_t in_dtype, const int8_t* Wq, co
   if (in_dtype != MOE_IN_BF16 && in_dtype != MOE_IN_F16 && in_dtype != MOE_IN_F32)
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown in_dtype %d", who, in_dtype);
   if (T > 0 && !x) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
-  int8_t* q = static_cast<int8_t*>(workspace);
-  float* s = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256((size_t)(T < 0 ? 0 : T) * (K < 0 ? 0 : K)));
-  if (moe_status_t st = check_i8_gemm(q, workspace ? s : nullptr, Wq, Ws, T, 1, N, K, epilogue, y, out_dtype, who)) return st;
+  const bool few = T > 0 && K > 0 && moe::i8_few_fits(T, K);  // one launch, no workspace
+  int8_t* q = few ? nullptr : static_cast<int8_t*>(workspace);
+  float* s = q ? reinterpret_cast<float*>(reinterpret_cast<char*>(q) + up256((size_t)(T < 0 ? 0 : T) * (K < 0 ? 0 : K))) : nullptr;
+  // (the few-rows form reads x itself, which stands for codes and scales in the checks)
+  if (moe_status_t st = check_i8_gemm(few ? static_cast<const int8_t*>(x) : q, few ? static_cast<const float*>(x) : s, Wq, Ws,
+                                      T, 1, N, K, epilogue, y, out_dtype, who))
+    return st;
   if (T == 0) return ok();
   if (!aligned16(x)) return fail(MOE_ERR_MISALIGNED, "%s: x needs 16-byte alignment", who);
+  if (few)
+    return hip_status(moe::launch_linear_i8_few(x, in_dtype, Wq, Ws, T, N, K, epilogue, y, out_dtype, (hipStream_t)stream),
+                      "moe_linear_i8 launch");
   const size_t need = moe_linear_i8_workspace_bytes(T, K);
   if (workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu B < required %zu B", who, workspace_bytes, need);

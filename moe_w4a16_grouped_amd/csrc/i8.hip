@@ -122,6 +122,142 @@ hipError_t launch_i8_quant(const void* x, int in_dtype, int rows, int K, int8_t*
   return launch_quant<MOE_IN_BF16>(x, rows, K, q, s, stream);
 }
 
+// ---------------------------------------------------------------------------------------------------
+// A few rows (T <= 16, T * K <= kI8FewElems) in one launch: every workgroup quantizes the rows itself, into LDS, while
+// its first weights are on their way.  Four waves: two halves of the contraction by two blocks of 32 weight rows
+// (SiLU*mul: 16 gate and their 16 up rows); weights go straight to registers, kI8FewAhead 64-byte groups at a time;
+// the halves' integer sums are exact in any order and meet in LDS.  Bound by latency: 1 x 2048 x 768 takes one round
+// trip for x and the weights, the arithmetic of a row, and a launch (the two launches: 12.3 us a call, this one: see
+// kI8FewElems' figures).
+constexpr int kI8FewRows = 16;
+constexpr int kI8FewElems = 8192;
+constexpr int kI8FewAhead = 8;
+
+bool i8_few_fits(int T, int K) { return T <= kI8FewRows && (long long)T * K <= kI8FewElems; }
+
+template <int IN, int EPI>
+__global__ __launch_bounds__(256) void linear_i8_few_kernel(const void* __restrict__ x, const int8_t* __restrict__ W,
+                                                            const float* __restrict__ Ws, int T, int N, int K,
+                                                            void* __restrict__ y, int out) {
+  // codes [T][K rounded to 64, and 16 more], rows 16 bytes apart in the banks
+  __shared__ __attribute__((aligned(16))) uint8_t codes[kI8FewElems + kI8FewRows * 80];
+  __shared__ float sx[kI8FewRows];
+  __shared__ uint32_t wmax[4];
+  __shared__ int32_t part[2 * 64 * 8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l16 = lane & 15, q = lane >> 4;
+  const int wk = wave >> 1, wn = wave & 1;
+  const int ND = EPI == MOE_EPI_SILU_MUL ? N / 2 : N;
+  constexpr int BC = EPI == MOE_EPI_SILU_MUL ? 32 : 64;
+  const int col0 = blockIdx.x * BC + wn * (BC / 2);
+  const int groups = (K + 63) / 64, half = (groups + 1) / 2;
+  const int g0 = wk * half, g1 = min(groups, g0 + half);
+  const int stride = groups * 64 + 16;
+
+  const int8_t* wrow[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    int n = EPI == MOE_EPI_SILU_MUL ? col0 + l16 : col0 + 16 * b + l16;
+    if (n >= ND) n = 0;  // only reaches results that are not stored
+    if (EPI == MOE_EPI_SILU_MUL && b == 1) n += ND;
+    wrow[b] = W + (size_t)n * K;
+  }
+  u32x4 w[kI8FewAhead][2];
+  auto load = [&](int g) {  // groups g .. g + kI8FewAhead - 1 of this wave's share; zeros past the row's end
+#pragma unroll
+    for (int i = 0; i < kI8FewAhead; ++i) {
+      const int k = (g + i) * 64 + 16 * q;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        w[i][b] = g + i < g1 && k < K ? *reinterpret_cast<const u32x4*>(wrow[b] + k) : u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+  load(g0);
+
+  // 256 threads a row for one row, 128 for two, 64 (a wave) for more
+  const int tpr = T == 1 ? 256 : (T == 2 ? 128 : 64), rpp = 256 / tpr;
+  const int nc = K / 8;
+  for (int r0 = 0; r0 < T; r0 += rpp) {
+    const int r = r0 + tid / tpr, rr = min(r, T - 1), c0 = tid % tpr;
+    uint32_t m = 0;
+    float v[8];
+    for (int c = c0; c < nc; c += tpr) {
+      i8_load8<IN>(x, (size_t)rr * K + 8 * (size_t)c, v);
+      m = i8_amax8(v, m);
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    if (tpr > 64) {  // T <= 2: one pass, whole waves a row
+      if (lane == 0) wmax[wave] = m;
+      __syncthreads();
+      const int w0 = wave / (tpr / 64) * (tpr / 64);
+      for (int i = 0; i < tpr / 64; ++i) m = max(m, wmax[w0 + i]);
+    }
+    const float sc = i8_scale(m);
+    if (r < T) {
+      if (c0 == 0) sx[r] = sc;
+      for (int c = c0; c < nc; c += tpr) {
+        if (nc > tpr) i8_load8<IN>(x, (size_t)r * K + 8 * (size_t)c, v);  // else v still holds them
+        *reinterpret_cast<u32x2*>(codes + r * stride + 8 * c) = i8_codes8(v, sc);
+      }
+      // codes past the row's end meet weights of zero
+    }
+  }
+  __syncthreads();
+
+  i32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  const uint8_t* arow = codes + min(l16, T - 1) * stride + 16 * q;
+  for (int g = g0; g < g1; g += kI8FewAhead) {
+    if (g > g0) load(g);
+#pragma unroll
+    for (int i = 0; i < kI8FewAhead; ++i) {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(arow + min(g + i, groups - 1) * 64);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) acc[b] = ElemI8::mfma(w[i][b], a, acc[b]);
+    }
+  }
+  if (wk == 1) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[(wn * 64 + lane) * 8 + b * 4 + i] = acc[b][i];
+  }
+  __syncthreads();
+  if (wk == 1 || l16 >= T) return;
+  const float sa = sx[l16];
+#pragma unroll
+  for (int b = 0; b < (EPI == MOE_EPI_SILU_MUL ? 1 : 2); ++b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = col0 + b * 16 + 4 * q + i;
+      if (col >= ND) continue;
+      float v = (float)(acc[b][i] + part[(wn * 64 + lane) * 8 + b * 4 + i]) * (sa * Ws[col]);
+      if constexpr (EPI == MOE_EPI_SILU_MUL) {
+        const float u = (float)(acc[1][i] + part[(wn * 64 + lane) * 8 + 4 + i]) * (sa * Ws[ND + col]);
+        v = silu_f32(v) * u;
+      }
+      store1(y, out, (size_t)l16 * ND + col, v);
+    }
+  }
+}
+
+template <int IN>
+static hipError_t launch_few(const void* x, const int8_t* Wq, const float* Ws, int T, int N, int K, int epilogue, void* y,
+                             int out, hipStream_t s) {
+  if (epilogue == MOE_EPI_SILU_MUL)
+    linear_i8_few_kernel<IN, MOE_EPI_SILU_MUL><<<(N / 2 + 31) / 32, 256, 0, s>>>(x, Wq, Ws, T, N, K, y, out);
+  else
+    linear_i8_few_kernel<IN, MOE_EPI_NONE><<<(N + 63) / 64, 256, 0, s>>>(x, Wq, Ws, T, N, K, y, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_i8_few(const void* x, int in_dtype, const int8_t* Wq, const float* Ws, int T, int N, int K,
+                                int epilogue, void* y, int out, hipStream_t stream) {
+  if (in_dtype == MOE_IN_F32) return launch_few<MOE_IN_F32>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
+  if (in_dtype == MOE_IN_F16) return launch_few<MOE_IN_F16>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
+  return launch_few<MOE_IN_BF16>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
+}
+
 hipError_t launch_ragged_i8(const RaggedArgs& a, int epilogue, hipStream_t stream) {
   return epilogue == MOE_EPI_SILU_MUL ? launch_ragged_fwd<ElemI8, MOE_EPI_SILU_MUL>(a, stream)
                                       : launch_ragged_fwd<ElemI8, MOE_EPI_NONE>(a, stream);

@@ -191,6 +191,10 @@ hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilog
 hipError_t launch_ragged_i8(const RaggedArgs& a, int epilogue, hipStream_t stream);
 // x (MOE_IN_*) [rows, K] -> codes [rows, K] and scales [rows].
 hipError_t launch_i8_quant(const void* x, int in_dtype, int rows, int K, int8_t* q, float* s, hipStream_t stream);
+// The quantization and the dense product of a few rows in one launch, without a workspace.
+bool i8_few_fits(int T, int K);
+hipError_t launch_linear_i8_few(const void* x, int in_dtype, const int8_t* Wq, const float* Ws, int T, int N, int K,
+                                int epilogue, void* y, int out, hipStream_t stream);
 // gate_up G [R, 2I] -> h [R, I], and its gradient (16-bit types).
 hipError_t launch_silu_mul(const uint16_t* G, bool f16, long long R, int I, uint16_t* h, hipStream_t stream);
 hipError_t launch_silu_mul_grad(const uint16_t* G, const uint16_t* dh, bool f16, long long R, int I, uint16_t* dG,

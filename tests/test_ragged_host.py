@@ -23,7 +23,8 @@ REFUSALS = [
     ("moe_gemm_i8", dict(Ws=None), ARG), ("moe_gemm_i8", dict(Aq=FAKE + 4), ALIGN), ("moe_gemm_i8", dict(C=FAKE + 4), ALIGN),
     ("moe_linear_i8", dict(in_dtype=3), ARG), ("moe_linear_i8", dict(x=None), ARG), ("moe_linear_i8", dict(workspace=None), ARG),
     ("moe_linear_i8", dict(workspace_bytes=16), WS), ("moe_linear_i8", dict(workspace=FAKE + 8), ALIGN),
-    ("moe_linear_i8", dict(x=FAKE + 8), ALIGN), ("moe_linear_i8", dict(T=-1), ARG), ("moe_linear_i8", dict(K=24), SHAPE),
+    ("moe_linear_i8", dict(x=FAKE + 8), ALIGN), ("moe_linear_i8", dict(T=4, x=FAKE + 8), ALIGN),
+    ("moe_linear_i8", dict(T=4, y=None), ARG), ("moe_linear_i8", dict(T=4, Ws=None), ARG), ("moe_linear_i8", dict(T=4, N=0), ARG), ("moe_linear_i8", dict(T=-1), ARG), ("moe_linear_i8", dict(K=24), SHAPE),
     ("moe_grouped_gemm_i8", dict(E=0), ARG), ("moe_grouped_gemm_i8", dict(E=1025), SHAPE),
     ("moe_grouped_gemm_i8", dict(expert_offsets=None), ARG), ("moe_grouped_gemm_i8", dict(a_row_div=0), ARG),
     ("moe_grouped_gemm_i8", dict(R=1 << 26), SHAPE), ("moe_grouped_gemm_i8", dict(a_row_of=FAKE + 2), ALIGN),
@@ -51,7 +52,7 @@ REFUSALS = [
 VALID = {
     "moe_i8_quantize": dict(x=FAKE, in_dtype=BF16, rows=4, K=64, q=FAKE, s=FAKE),
     "moe_gemm_i8": dict(Aq=FAKE, As=FAKE, Wq=FAKE, Ws=FAKE, M=4, N=64, K=64, epilogue=0, C=FAKE, out_dtype=0),
-    "moe_linear_i8": dict(x=FAKE, in_dtype=BF16, Wq=FAKE, Ws=FAKE, T=4, N=64, K=64, epilogue=0, y=FAKE, out_dtype=0,
+    "moe_linear_i8": dict(x=FAKE, in_dtype=BF16, Wq=FAKE, Ws=FAKE, T=400, N=64, K=64, epilogue=0, y=FAKE, out_dtype=0,
                           workspace=FAKE, workspace_bytes=1 << 20),
     "moe_grouped_gemm_i8": dict(Aq=FAKE, As=FAKE, a_row_of=FAKE, a_row_div=2, Wq=FAKE, Ws=FAKE, expert_offsets=FAKE, R=4, E=8,
                                 N=64, K=64, epilogue=0, C=FAKE, out_dtype=0),
@@ -82,7 +83,8 @@ def test_refusals(entry, change, status):
 def test_workspace_sizes():
     lib = moe.load()
     assert moe.moe_linear_i8_workspace_bytes(77, 2048) >= 77 * 2048 + 77 * 4
-    assert moe.moe_linear_i8_workspace_bytes(0, 2048) == 0
+    assert moe.moe_linear_i8_workspace_bytes(0, 2048) == moe.moe_linear_i8_workspace_bytes(4, 2048) == 0
+    assert moe.moe_linear_i8_workspace_bytes(5, 2048) > 0 and moe.moe_linear_i8_workspace_bytes(17, 16) > 0
     assert moe.moe_linear_i8_workspace_bytes(-1, 2048) == moe.moe_linear_i8_workspace_bytes(5, 24) == 0
     T, H, I, E, k = 800, 2048, 512, 256, 8
     R = T * k
