@@ -581,40 +581,60 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   };
   const int rows = MODE == kDw ? min(N - m0, BM) : t.rows;
   const size_t first = MODE == kDw ? w_e + (size_t)m0 * K : (size_t)t.row0 * ND;  // the tile's first row in C
-  // 16-bit results of the higher tiles pass through LDS (the stages are free) and are stored as whole rows, 16
-  // bytes a lane; stored from the registers they are 32-byte pieces of 16 rows (weight gradients of 256 experts of
-  // 1024 x 2048 over 800 tokens: 385 us, staged 296 us).  After SiLU*mul, whose arithmetic covers the stores, the
-  // detour costs more than it gains (int8 gate_up, 256 x 256 tiles of 512 experts: 430 -> 460 us).
-  constexpr bool kStaged = EPI == MOE_EPI_NONE && BM >= 64 && (LATE ? 4 * (BM + BN) : 0) + BM * BC * 2 <= S::kLds;
-  if (kStaged && p.out != MOE_OUT_F32 && (ND & 7) == 0) {
-    constexpr int NCH = BC / 8;  // 16-byte chunks of a row, permuted by the row's number
-    uint8_t* buf = smem + (LATE ? 4 * (BM + BN) : 0);
-    __syncthreads();
+  // Results pass through LDS (the stages are free) and are stored as whole rows, 16 bytes a lane; stored from the
+  // registers they are 32- or 64-byte pieces of 16 rows (16-bit weight gradients of 256 experts of 1024 x 2048 over 800
+  // tokens: 385 us, staged 296 us).  After SiLU*mul, whose arithmetic covers the stores, the detour costs more than it
+  // gains (int8 gate_up, 256 x 256 tiles of 512 experts: 430 -> 460 us); so it does in the low tiles.
+  // 16-bit results go in one piece, 32-bit ones a wave row (BM / WM rows) at a time.
+  constexpr int kTop = LATE ? 4 * (BM + BN) : 0;  // the scales
+  constexpr bool kStaged = EPI == MOE_EPI_NONE && BM >= 64;
+  auto staged = [&](auto bytes) {
+    constexpr int ES = decltype(bytes)::value, PASSES = ES == 4 ? WM : 1, PR = BM / PASSES;
+    constexpr int NCH = BC * ES / 16, CE = 16 / ES;  // 16-byte chunks of a row, permuted by the row's number
+    uint8_t* buf = smem + kTop;
+    const int cols = min(BC, ND - nb * BC);
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      const int row = wm * (BM / WM) + mi * 16 + l16;
-      const float sa = I8 ? sScaleA[row] : 1.f;
+    for (int ps = 0; ps < PASSES; ++ps) {
+      __syncthreads();
+      if (PASSES == 1 || wm == ps) {
 #pragma unroll
-      for (int ni = 0; ni < NO; ++ni) {
-        float v[4];
-        results(mi, ni, sa, v);
-        const int chunk = (wn * (BC / WN) + ni * 16) / 8 + (q >> 1);
-        u16x4 b;
+        for (int mi = 0; mi < MI; ++mi) {
+          const int row = wm * (BM / WM) + mi * 16 + l16;
+          const float sa = I8 ? sScaleA[row] : 1.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = p.out == MOE_OUT_F16 ? f32_to_f16_bits(v[i]) : f32_to_bf16_bits(v[i]);
-        *reinterpret_cast<u16x4*>(buf + row * (BC * 2) + ((chunk ^ (row & (NCH - 1) & 15)) * 16) + (q & 1) * 8) = b;
+          for (int ni = 0; ni < NO; ++ni) {
+            float v[4];
+            results(mi, ni, sa, v);
+            const int col = wn * (BC / WN) + ni * 16 + 4 * q, chunk = col / CE;
+            uint8_t* at = buf + (row - ps * PR) * (BC * ES) + ((chunk ^ (row & (NCH - 1) & 15)) * 16);
+            if constexpr (ES == 4) {
+              *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+            } else {
+              u16x4 b;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) b[i] = p.out == MOE_OUT_F16 ? f32_to_f16_bits(v[i]) : f32_to_bf16_bits(v[i]);
+              *reinterpret_cast<u16x4*>(at + (q & 1) * 8) = b;
+            }
+          }
+        }
+      }
+      __syncthreads();
+      uint8_t* C = static_cast<uint8_t*>(p.C) + (first + nb * BC) * ES;
+#pragma unroll 4
+      for (int i = tid; i < PR * NCH; i += NW * 64) {
+        const int r = i / NCH, row = ps * PR + r, chunk = i % NCH;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(buf + r * (BC * ES) + ((chunk ^ (row & (NCH - 1) & 15)) * 16));
+        if (row < rows && chunk * CE < cols) *reinterpret_cast<u32x4*>(C + ((size_t)row * ND + chunk * CE) * ES) = w;
       }
     }
-    __syncthreads();
-    uint16_t* C = static_cast<uint16_t*>(p.C) + first + nb * BC;
-    const int cols = min(BC, ND - nb * BC);
-#pragma unroll 4
-    for (int i = tid; i < BM * NCH; i += NW * 64) {
-      const int row = i / NCH, chunk = i % NCH;
-      const u32x4 w = *reinterpret_cast<const u32x4*>(buf + row * (BC * 2) + ((chunk ^ (row & (NCH - 1) & 15)) * 16));
-      if (row < rows && chunk * 8 < cols) *reinterpret_cast<u32x4*>(C + (size_t)row * ND + chunk * 8) = w;
+  };
+  if constexpr (kStaged) {
+    if constexpr (kTop + BM * BC * 2 <= S::kLds) {
+      if (p.out != MOE_OUT_F32 && (ND & 7) == 0) return staged(std::integral_constant<int, 2>{});
     }
-    return;
+    if constexpr (kTop + BM / WM * BC * 4 <= S::kLds) {
+      if (p.out == MOE_OUT_F32 && (ND & 3) == 0) return staged(std::integral_constant<int, 4>{});
+    }
   }
   const bool whole = (ND & 3) == 0;  // rows are stored four columns at a time
 #pragma unroll
