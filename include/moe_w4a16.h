@@ -698,15 +698,22 @@ moe_status_t moe_grouped_gemm_w16_dx(const uint16_t* dC, const uint16_t* W, int3
                                      int32_t R, int32_t E, int32_t N, int32_t K, void* dA, int32_t out_dtype,
                                      void* stream);
 
+/* Workspace bytes moe_grouped_gemm_w16_dw needs (host-only, pure; 0 where the rows are not cut into parts, and on
+ * invalid sizes). */
+size_t moe_grouped_gemm_w16_dw_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K);
+
 /*
  * Gradient of moe_grouped_gemm_w16 (NONE) with respect to its weights:
  *   dW[e, n, k] = sum over the rows r of expert e of dC[r, n] * A[a(r), k],
  * dC [R, N] and A [*, K] of dtype, dW [E, N, K] of out_dtype, every element written (zeros for an expert
- * without rows, also when R is 0).  N and K multiples of 8; otherwise as moe_grouped_gemm_w16.
+ * without rows, also when R is 0).  Few weights with many rows a group are summed in parts of the rows, which are
+ * then added in order: workspace of at least moe_grouped_gemm_w16_dw_workspace_bytes(R, E, N, K) bytes, 16-byte
+ * aligned (NULL where that is 0).  N and K multiples of 8; otherwise as moe_grouped_gemm_w16.
  */
 moe_status_t moe_grouped_gemm_w16_dw(const uint16_t* dC, const uint16_t* A, const int32_t* a_row_of, int32_t a_row_div,
                                      int32_t dtype, const int32_t* expert_offsets, int32_t R, int32_t E, int32_t N,
-                                     int32_t K, void* dW, int32_t out_dtype, void* stream);
+                                     int32_t K, void* dW, int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream);
 
 /*
  * SiLU*mul of a stored gate_up result G [R, 2I] (columns [0, I) the gate g, [I, 2I) the up projection u), for

@@ -18,7 +18,7 @@ from ._lib import (MOE_ACT_ROWS, MOE_ACT_TILED, MOE_EPI_NONE, MOE_EPI_SILU_MUL, 
                    moe_x_to_f16, moe_grouped_gemm_w4f16,
                    moe_i8_quantize, moe_gemm_i8, moe_linear_i8_workspace_bytes, moe_linear_i8, moe_grouped_gemm_i8,
                    moe_ffn_i8_workspace_bytes, moe_ffn_forward_i8, moe_grouped_gemm_w16, moe_grouped_gemm_w16_dx,
-                   moe_grouped_gemm_w16_dw, moe_silu_mul, moe_silu_mul_grad, moe_ffn_w16_workspace_bytes,
+                   moe_grouped_gemm_w16_dw, moe_grouped_gemm_w16_dw_workspace_bytes, moe_silu_mul, moe_silu_mul_grad, moe_ffn_w16_workspace_bytes,
                    moe_ffn_forward_w16, MOE_IN_F16, MOE_OUT_F16)
 
 __all__ = ["MOE_ACT_ROWS", "MOE_ACT_TILED", "MOE_EPI_NONE", "MOE_EPI_SILU_MUL", "MOE_LAYOUT_CANONICAL", "MOE_LAYOUT_PACKED", "MOE_OUT_BF16",
@@ -34,5 +34,5 @@ __all__ = ["MOE_ACT_ROWS", "MOE_ACT_TILED", "MOE_EPI_NONE", "MOE_EPI_SILU_MUL", 
            "moe_grouped_gemm_w4f16",
            "moe_i8_quantize", "moe_gemm_i8", "moe_linear_i8_workspace_bytes", "moe_linear_i8", "moe_grouped_gemm_i8",
            "moe_ffn_i8_workspace_bytes", "moe_ffn_forward_i8", "moe_grouped_gemm_w16", "moe_grouped_gemm_w16_dx",
-           "moe_grouped_gemm_w16_dw", "moe_silu_mul", "moe_silu_mul_grad", "moe_ffn_w16_workspace_bytes",
+           "moe_grouped_gemm_w16_dw", "moe_grouped_gemm_w16_dw_workspace_bytes", "moe_silu_mul", "moe_silu_mul_grad", "moe_ffn_w16_workspace_bytes",
            "moe_ffn_forward_w16", "MOE_IN_F16", "MOE_OUT_F16"]

@@ -107,7 +107,8 @@ def load() -> ctypes.CDLL:
         "moe_ffn_forward_i8": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P], I32),
         "moe_grouped_gemm_w16": ([P, P, I32, P, I32, P, I32, I32, I32, I32, I32, P, I32, P], I32),
         "moe_grouped_gemm_w16_dx": ([P, P, I32, P, I32, I32, I32, I32, P, I32, P], I32),
-        "moe_grouped_gemm_w16_dw": ([P, P, P, I32, I32, P, I32, I32, I32, I32, P, I32, P], I32),
+        "moe_grouped_gemm_w16_dw_workspace_bytes": ([I32, I32, I32, I32], SZ),
+        "moe_grouped_gemm_w16_dw": ([P, P, P, I32, I32, P, I32, I32, I32, I32, P, I32, P, SZ, P], I32),
         "moe_silu_mul": ([P, I32, I32, I32, P, P], I32),
         "moe_silu_mul_grad": ([P, P, I32, I32, I32, P, P], I32),
         "moe_ffn_w16_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
@@ -134,7 +135,7 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_last_error", "moe_route
             "moe_ffn_forward_w4a8", "moe_ffn_noalloc_scratch_bytes", "moe_ffn_forward_noalloc", "moe_x_to_f16",
             "moe_grouped_gemm_w4f16", "moe_i8_quantize", "moe_gemm_i8", "moe_linear_i8_workspace_bytes", "moe_linear_i8",
             "moe_grouped_gemm_i8", "moe_ffn_i8_workspace_bytes", "moe_ffn_forward_i8", "moe_grouped_gemm_w16",
-            "moe_grouped_gemm_w16_dx", "moe_grouped_gemm_w16_dw", "moe_silu_mul", "moe_silu_mul_grad",
+            "moe_grouped_gemm_w16_dx", "moe_grouped_gemm_w16_dw_workspace_bytes", "moe_grouped_gemm_w16_dw", "moe_silu_mul", "moe_silu_mul_grad",
             "moe_ffn_w16_workspace_bytes", "moe_ffn_forward_w16")
 
 
@@ -891,7 +892,12 @@ def moe_grouped_gemm_w16_dx(dC, W, expert_offsets, out_dtype: int = None, dA=Non
     return dA
 
 
-def moe_grouped_gemm_w16_dw(dC, A, a_row_of, a_row_div: int, expert_offsets, out_dtype: int = None, dW=None, stream=None):
+def moe_grouped_gemm_w16_dw_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
+    return int(load().moe_grouped_gemm_w16_dw_workspace_bytes(R, E, N, K))
+
+
+def moe_grouped_gemm_w16_dw(dC, A, a_row_of, a_row_div: int, expert_offsets, out_dtype: int = None, dW=None,
+                            workspace=None, stream=None):
     """Weight gradients of moe_grouped_gemm_w16: dC [R, N] and A [*, K] of one type -> dW [E, N, K] of out_dtype
     (default: the operands' type); zeros for experts without rows."""
     R, N = _need(dC, _W16, (None, None), "dC")
@@ -903,8 +909,15 @@ def moe_grouped_gemm_w16_dw(dC, A, a_row_of, a_row_div: int, expert_offsets, out
     _groups(A, R, a_row_of, a_row_div, expert_offsets, E, dev)
     out_dtype = _OUT[dt] if out_dtype is None else out_dtype
     dW = _out(dW, (E, N, K), out_dtype, dev, "dW")
-    _call(load().moe_grouped_gemm_w16_dw, dev, stream, (dW,), dC.data_ptr(), A.data_ptr(), _ptr(a_row_of), a_row_div,
-          _IN[dt], expert_offsets.data_ptr(), R, E, N, K, dW.data_ptr(), out_dtype)
+    lib, size = load(), 0
+    if workspace is not None:
+        size, = _need(workspace, _U8, (None,), "workspace", dev)
+    else:
+        size = lib.moe_grouped_gemm_w16_dw_workspace_bytes(R, E, N, K)
+        if size:
+            workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
+    _call(lib.moe_grouped_gemm_w16_dw, dev, stream, (dW, workspace), dC.data_ptr(), A.data_ptr(), _ptr(a_row_of), a_row_div,
+          _IN[dt], expert_offsets.data_ptr(), R, E, N, K, dW.data_ptr(), out_dtype, _ptr(workspace), size)
     return dW
 
 

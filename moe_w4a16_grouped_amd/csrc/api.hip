@@ -1612,9 +1612,16 @@ moe_status_t moe_grouped_gemm_w16_dx(const uint16_t* dC, const uint16_t* W, int3
   return hip_status(moe::launch_ragged_w16(a, 1, dtype == MOE_IN_F16, MOE_EPI_NONE, (hipStream_t)stream), "moe_grouped_gemm_w16_dx launch");
 }
 
+size_t moe_grouped_gemm_w16_dw_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K) {
+  if (R < 0 || E < 1 || N < 1 || K < 1 || E > MOE_MAX_EXPERTS || N > MOE_RAGGED_MAX_DIM || K > MOE_RAGGED_MAX_DIM) return 0;
+  const int split = moe::dw_split(R, E, N, K);
+  return split > 1 ? (size_t)split * E * N * K * sizeof(float) : 0;
+}
+
 moe_status_t moe_grouped_gemm_w16_dw(const uint16_t* dC, const uint16_t* A, const int32_t* a_row_of, int32_t a_row_div,
                                      int32_t dtype, const int32_t* expert_offsets, int32_t R, int32_t E, int32_t N,
-                                     int32_t K, void* dW, int32_t out_dtype, void* stream) {
+                                     int32_t K, void* dW, int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
   const char* who = "moe_grouped_gemm_w16_dw";
   if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
   if (moe_status_t st = check_ragged(R, E, N, K, 8, 8, 2, who)) return st;
@@ -1622,7 +1629,13 @@ moe_status_t moe_grouped_gemm_w16_dw(const uint16_t* dC, const uint16_t* A, cons
   if (!dW || (R > 0 && (!dC || !A))) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned16(dC) || !aligned16(A) || !aligned16(dW)) return fail(MOE_ERR_MISALIGNED, "%s: dC, A, dW need 16-byte alignment", who);
   if (moe_status_t st = check_groups(a_row_of, a_row_div, expert_offsets, who)) return st;
+  const size_t need = moe_grouped_gemm_w16_dw_workspace_bytes(R, E, N, K);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu B < required %zu B", who, workspace_bytes, need);
+  if (need > 0 && !aligned16(workspace)) return fail(MOE_ERR_MISALIGNED, "%s: workspace needs 16-byte alignment", who);
   moe::RaggedArgs a{A, nullptr, a_row_of, a_row_div, dC, nullptr, expert_offsets, R, E, N, K, dW, out_dtype};
+  a.split = moe::dw_split(R, E, N, K);
+  a.parts = static_cast<float*>(workspace);
   return hip_status(moe::launch_ragged_w16(a, 2, dtype == MOE_IN_F16, MOE_EPI_NONE, (hipStream_t)stream), "moe_grouped_gemm_w16_dw launch");
 }
 

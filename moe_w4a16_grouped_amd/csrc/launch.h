@@ -186,7 +186,11 @@ struct RaggedArgs {
   int R, E, N, K;
   void* C;                  // FWD: [R, N] or [R, N/2]; DX: [R, K]; DW: [E, N, K]
   int out;                  // MOE_OUT_BF16, MOE_OUT_F16 or MOE_OUT_F32
+  int split = 1;            // DW: parts of each expert's rows (dw_split)
+  float* parts = nullptr;   // DW with split > 1: [E, split, N, K], the parts' sums
 };
+// Parts that the weight gradients' rows are cut into: 1 unless the output tiles are few and the rows many.
+int dw_split(int R, int E, int N, int K);
 hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilogue, hipStream_t stream);
 hipError_t launch_ragged_i8(const RaggedArgs& a, int epilogue, hipStream_t stream);
 // x (MOE_IN_*) [rows, K] -> codes [rows, K] and scales [rows].

@@ -697,10 +697,16 @@ __global__ __launch_bounds__(S0::WM * S0::WN * 64) void ragged_gemm_kernel(Ragge
       e = (int)(b / per_e);
       i = (int)(b % per_e);
     }
-    if (e >= p.E) return;
+    // (with a split, e names a part of an expert's rows; each part's sums are an output of their own)
+    if (e >= p.E * p.split) return;
     band_place(i, nbm, nbn, mb, nb);
-    const int r0 = group_end(p.offsets, e, p.R);
-    const RowTile t{e, r0, max(group_end(p.offsets, e + 1, p.R) - r0, 0), 0};
+    int r0 = group_end(p.offsets, e / p.split, p.R), rows = max(group_end(p.offsets, e / p.split + 1, p.R) - r0, 0);
+    if (p.split > 1) {
+      const int part = ((rows + p.split - 1) / p.split + 31) & ~31, from = min((e % p.split) * part, rows);
+      rows = min(part, rows - from);
+      r0 += from;
+    }
+    const RowTile t{e, r0, rows, 0};
     ragged_tile<T, MODE, EPI, S0, kLate>(p, t, nb, mb * BM, smem, sRow, sScaleA, sScaleW);
   } else {
     RowTile t;
@@ -735,7 +741,7 @@ static hipError_t launch_ragged_cfg(const RaggedArgs& a, hipStream_t s) {
   dim3 grid;
   if (MODE == kDw) {
     const long long per_e = (long long)((a.N + BM - 1) / BM) * nbn;
-    grid = grid2d(per_e >= 8 ? (per_e + 7) / 8 * 8 * a.E : per_e * a.E);
+    grid = grid2d((per_e >= 8 ? (per_e + 7) / 8 * 8 : per_e) * a.E * a.split);
   } else {
     // most row tiles that any groups of R rows give, and up to one more a list and XCD by the shares' rounding
     const long long m = a.offsets ? (a.E < a.R ? a.E : a.R) : 1;

@@ -24,10 +24,42 @@ static hipError_t launch_dx(const RaggedArgs& a, hipStream_t s) {
 // Weight gradients of 64 experts of 1024 x 2048, mean 100: 84 us with 256 x 128 tiles (two workgroups a CU), 83 us
 // with 128 x 128, 93 us with 256 x 256; mean 400: 162, 170, 166; mean 1024 (8 experts of 4096 x 14336): 1239 against
 // 1173 us with 256 x 256.
+//
+// A few output tiles with many rows leave most CUs idle: the rows are then cut into parts, whose sums (fp32, in the
+// workspace) a second launch adds in order.  One group of 8192 rows, 1024 x 2048 weights (128 tiles): see dw_split.
+int dw_split(int R, int E, int N, int K) {
+  const long long tiles = (long long)E * ((N + 127) / 128) * ((K + 127) / 128), mean = (long long)R / E;
+  const long long most = 512 / tiles < mean / 256 ? 512 / tiles : mean / 256;  // two workgroups a CU, 256 rows a part
+  return most < 2 ? 1 : (most > 8 ? 8 : (int)most);
+}
+
+__global__ __launch_bounds__(256) void add_parts_kernel(const f32x4* __restrict__ parts, long long per, int split, int out,
+                                                        void* __restrict__ dW) {
+  const long long i = linear_block() * 256 + threadIdx.x;  // four elements of expert blockIdx.z
+  if (i >= per) return;
+  const long long e = blockIdx.z;
+  f32x4 sum = parts[e * split * per + i];
+  for (int k = 1; k < split; ++k) sum += parts[(e * split + k) * per + i];
+  const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+  store4(dW, out, (size_t)(e * per + i) * 4, v);
+}
+
 template <class T>
 static hipError_t launch_dw(const RaggedArgs& a, hipStream_t s) {
   const long long mean = ((long long)a.R + a.E - 1) / a.E;
   const long long tiles = (long long)a.E * ((a.N + 255) / 256) * ((a.K + 127) / 128);
+  if (a.split > 1) {
+    RaggedArgs b = a;
+    b.C = a.parts;
+    b.out = MOE_OUT_F32;
+    hipError_t e = launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<128, 128, 2, 2, 64, 3>>(b, s);
+    if (e != hipSuccess) return e;
+    const long long per = (long long)a.N * a.K / 4;  // N and K are multiples of 8
+    dim3 grid = grid2d((per + 255) / 256);
+    grid.z = a.E;
+    add_parts_kernel<<<grid, 256, 0, s>>>(reinterpret_cast<const f32x4*>(a.parts), per, a.split, a.out, a.C);
+    return hipGetLastError();
+  }
   if (tiles < 512) return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<128, 128, 2, 2, 64, 3>>(a, s);
   if (mean <= 512) return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<256, 128, 2, 2, 64, 3>>(a, s);
   return launch_ragged_cfg<T, kDw, MOE_EPI_NONE, TileShape<256, 256, 2, 4, 64, 4>>(a, s);

@@ -89,6 +89,21 @@ def test_weight_gradients_of_long_groups(counts):
     ru.assert_close(dW, ref, ru.sum_bound(max(counts), mass))
 
 
+@pytest.mark.parametrize("counts,N,K,out", [([4000], 128, 256, F16), ([700, 0, 33, 5000], 72, 104, F32),
+                                            ([31, 2049], 264, 8, BF16)])
+def test_weight_gradients_in_parts(counts, N, K, out):
+    """Few weights with many rows: the rows are cut into parts; groups shorter than a part, empty ones, ends inside
+    one, gathered and plain rows, and the parts' sums added the same way each time."""
+    R, E = sum(counts), len(counts)
+    assert moe.moe_grouped_gemm_w16_dw_workspace_bytes(R, E, N, K) > 0
+    x, row_of, rows = _case(counts, 500, K, BF16, seed=9)
+    dC, off = _rand((R, N), BF16, 10), ru.offsets_of(counts)
+    dW = moe.moe_grouped_gemm_w16_dw(dC, x, row_of, 3, off, out_dtype=OUT[out])
+    ref, mass = ru.grouped_dw(dC, rows, counts)
+    ru.assert_close(dW, ref, ru.sum_bound(max(counts), mass))
+    assert torch.equal(dW, moe.moe_grouped_gemm_w16_dw(dC, rows.contiguous(), None, 1, off, out_dtype=OUT[out]))
+
+
 def test_gradients_against_differences():
     """dA and dW against central differences of the 64-bit product along random directions: the loss
     sum(C * dC) is linear in A and in W, so a difference quotient is exact up to rounding."""

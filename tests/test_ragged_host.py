@@ -36,6 +36,8 @@ REFUSALS = [
     ("moe_grouped_gemm_w16_dw", dict(N=12), SHAPE), ("moe_grouped_gemm_w16_dw", dict(K=12), SHAPE),
     ("moe_grouped_gemm_w16_dw", dict(dW=None, R=0), ARG), ("moe_grouped_gemm_w16_dw", dict(expert_offsets=None, R=0), ARG),
     ("moe_grouped_gemm_w16_dw", dict(dW=FAKE + 4), ALIGN), ("moe_grouped_gemm_w16_dw", dict(dtype=3), ARG),
+    ("moe_grouped_gemm_w16_dw", dict(R=8192), WS), ("moe_grouped_gemm_w16_dw", dict(R=8192, workspace=FAKE, workspace_bytes=4096), WS),
+    ("moe_grouped_gemm_w16_dw", dict(R=8192, workspace=FAKE + 8, workspace_bytes=1 << 20), ALIGN),
     ("moe_silu_mul", dict(I=12), ARG), ("moe_silu_mul", dict(dtype=1), ARG), ("moe_silu_mul", dict(R=-1), ARG),
     ("moe_silu_mul", dict(h=FAKE + 2), ALIGN), ("moe_silu_mul_grad", dict(dh=None), ARG), ("moe_silu_mul_grad", dict(I=1 << 21), SHAPE),
     ("moe_ffn_forward_i8", dict(H=72), SHAPE), ("moe_ffn_forward_i8", dict(k=9), ARG), ("moe_ffn_forward_i8", dict(w2_s=None), ARG),
@@ -60,7 +62,7 @@ VALID = {
                                  epilogue=0, C=FAKE, out_dtype=0),
     "moe_grouped_gemm_w16_dx": dict(dC=FAKE, W=FAKE, dtype=F16, expert_offsets=FAKE, R=4, E=8, N=64, K=64, dA=FAKE, out_dtype=1),
     "moe_grouped_gemm_w16_dw": dict(dC=FAKE, A=FAKE, a_row_of=None, a_row_div=1, dtype=F16, expert_offsets=FAKE, R=4, E=8, N=64,
-                                    K=64, dW=FAKE, out_dtype=1),
+                                    K=64, dW=FAKE, out_dtype=1, workspace=None, workspace_bytes=0),
     "moe_silu_mul": dict(G=FAKE, dtype=BF16, R=4, I=64, h=FAKE),
     "moe_silu_mul_grad": dict(G=FAKE, dh=FAKE, dtype=BF16, R=4, I=64, dG=FAKE),
     "moe_ffn_forward_i8": dict(x=FAKE, logits=FAKE, T=4, H=64, I=64, E=8, k=2, w13_q=FAKE, w13_s=FAKE, w2_q=FAKE, w2_s=FAKE, y=FAKE,
@@ -86,6 +88,10 @@ def test_workspace_sizes():
     assert moe.moe_linear_i8_workspace_bytes(0, 2048) == moe.moe_linear_i8_workspace_bytes(4, 2048) == 0
     assert moe.moe_linear_i8_workspace_bytes(5, 2048) > 0 and moe.moe_linear_i8_workspace_bytes(17, 16) > 0
     assert moe.moe_linear_i8_workspace_bytes(-1, 2048) == moe.moe_linear_i8_workspace_bytes(5, 24) == 0
+    assert moe.moe_grouped_gemm_w16_dw_workspace_bytes(8192, 8, 64, 64) >= 2 * 8 * 64 * 64 * 4
+    assert moe.moe_grouped_gemm_w16_dw_workspace_bytes(6400, 256, 1024, 2048) == 0  # enough tiles
+    assert moe.moe_grouped_gemm_w16_dw_workspace_bytes(300, 8, 64, 64) == 0         # few rows
+    assert moe.moe_grouped_gemm_w16_dw_workspace_bytes(8192, 0, 64, 64) == 0
     T, H, I, E, k = 800, 2048, 512, 256, 8
     R = T * k
     assert moe.moe_ffn_i8_workspace_bytes(T, H, I, E, k) >= T * H + T * 4 + R * I * 3 + R * 4 + R * H * 4
