@@ -52,9 +52,13 @@ __device__ __forceinline__ float i8_scale(uint32_t m) {
 __device__ __forceinline__ u32x2 i8_codes8(const float (&v)[8], float s) {
   u32x2 w = {0u, 0u};
   if (!(s > 0.f)) return w;  // an all-zero row, or NaN
+  // the quotients of a row of tiny values are taken 2^64 times as large (exactly): 1 / s must not overflow, nor a
+  // difference be too small for fp32
+  const float up = s < 0x1p-64f ? 0x1p64f : 1.0f;
+  s *= up;
   const float inv = 1.0f / s;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)(i8_code(v[j], s, inv) & 0xFF) << (8 * (j & 3));
+  for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)(i8_code(v[j] * up, s, inv) & 0xFF) << (8 * (j & 3));
   return w;
 }
 

@@ -254,6 +254,23 @@ def test_i8_quantize_extremes():
     assert torch.all(q[3] == -127)
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -70, 2.0 ** -110, 2.0 ** -126])
+def test_i8_quantize_tiny_rows(scale):
+    """Rows whose scale is near the least fp32 number or subnormal, zeros among them, in every path of the codes."""
+    for rows, K, dtype in ((3, 64, F32), (40, 1040, BF16), (2, 8208, F32)):
+        x = (_rand((rows, K), F32, K) * scale).to(dtype)
+        x[:, ::5] = 0
+        q, s = moe.moe_i8_quantize(x)
+        rq, rs = _codes_64(x)
+        rq = torch.where(rs[:, None] > 0, torch.round(x.double() / rs.double()[:, None]).clamp(-127, 127), 0).to(torch.int8)
+        assert torch.equal(s, rs) and torch.equal(q, rq), (rows, K)
+        if dtype == F32:
+            w = torch.ones((8, K), dtype=torch.int8, device="cuda")
+            y = moe.moe_linear_i8(x, w, torch.full((8,), 2.0 ** 60, device="cuda"), out_dtype=OUT[F32])
+            ref, err = _i8_reference(q, s, w, torch.full((8,), 2.0 ** 60, device="cuda"))
+            ru.assert_close(y, ref, err, (rows, K))
+
+
 def _i8_reference(q, s, wq, ws):
     """(G, error): the integer sums are exact; the sum's conversion, the scales' product and their product round
     once each."""
