@@ -65,10 +65,12 @@ __device__ __forceinline__ u32x2 i8_codes8(const float (&v)[8], float s) {
 // One workgroup per row, 8 elements a thread and chunk.  J chunks a thread stay in registers between the
 // maximum and the codes; with J == 0 (longer rows) they are read again.
 template <int IN, int J, int TH>
-__global__ __launch_bounds__(TH) void i8_quant_kernel(const void* __restrict__ x, int K, int8_t* __restrict__ q,
-                                                      float* __restrict__ s) {
+__global__ __launch_bounds__(TH) void i8_quant_kernel(const void* __restrict__ x, int rows, int K,
+                                                      int8_t* __restrict__ q, float* __restrict__ s) {
   __shared__ uint32_t wmax[TH / 64];
-  const int row = blockIdx.x, tid = threadIdx.x, nc = K / 8;
+  const long long row = linear_block();
+  if (row >= rows) return;
+  const int tid = threadIdx.x, nc = K / 8;
   const size_t base = (size_t)row * K;
   float v[J > 0 ? J : 1][8];
   uint32_t m = 0;
@@ -113,10 +115,11 @@ __global__ __launch_bounds__(TH) void i8_quant_kernel(const void* __restrict__ x
 
 template <int IN>
 static hipError_t launch_quant(const void* x, int rows, int K, int8_t* q, float* s, hipStream_t st) {
-  if (K <= 512) i8_quant_kernel<IN, 1, 64><<<rows, 64, 0, st>>>(x, K, q, s);
-  else if (K <= 2048) i8_quant_kernel<IN, 1, 256><<<rows, 256, 0, st>>>(x, K, q, s);
-  else if (K <= 8192) i8_quant_kernel<IN, 4, 256><<<rows, 256, 0, st>>>(x, K, q, s);
-  else i8_quant_kernel<IN, 0, 256><<<rows, 256, 0, st>>>(x, K, q, s);
+  const dim3 grid = grid2d(rows);  // a launch dimension holds fewer than 2^32 threads
+  if (K <= 512) i8_quant_kernel<IN, 1, 64><<<grid, 64, 0, st>>>(x, rows, K, q, s);
+  else if (K <= 2048) i8_quant_kernel<IN, 1, 256><<<grid, 256, 0, st>>>(x, rows, K, q, s);
+  else if (K <= 8192) i8_quant_kernel<IN, 4, 256><<<grid, 256, 0, st>>>(x, rows, K, q, s);
+  else i8_quant_kernel<IN, 0, 256><<<grid, 256, 0, st>>>(x, rows, K, q, s);
   return hipGetLastError();
 }
 

@@ -271,6 +271,18 @@ def test_i8_quantize_tiny_rows(scale):
             ru.assert_close(y, ref, err, (rows, K))
 
 
+def test_i8_quantize_many_rows():
+    """The most rows: more threads than a launch dimension holds."""
+    rows = 2 ** 26 - 1
+    x = torch.zeros((rows, 16), dtype=BF16, device="cuda")
+    at = torch.tensor([0, 2 ** 19 - 1, 2 ** 19, 2 ** 24 - 1, 2 ** 24, 2 ** 25 + 3, rows - 1], device="cuda")
+    x[at] = _rand((at.numel(), 16), BF16, 7)
+    q, s = moe.moe_i8_quantize(x)
+    rq, rs = _codes_64(x[at])
+    assert torch.equal(s[at], rs) and torch.equal(q[at], rq)
+    assert int((s != 0).sum()) == at.numel() and int(q.view(torch.int32).ne(0).any(dim=1).sum()) == at.numel()
+
+
 def _i8_reference(q, s, wq, ws):
     """(G, error): the integer sums are exact; the sum's conversion, the scales' product and their product round
     once each."""
