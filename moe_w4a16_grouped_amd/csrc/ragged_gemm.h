@@ -247,8 +247,9 @@ struct NoTile {
 };
 
 // One output tile: rows t (DW: weight rows from m0) by column block nb.
-// LATE: the scales are loaded after the contraction, into the first stages (int8 tiles whose stages fill the LDS).
-template <class T, int MODE, int EPI, class S, bool LATE>
+// LATE: the bytes of the scales where they are loaded after the contraction, into the first stages (int8 tiles whose
+// stages fill the LDS), else 0.
+template <class T, int MODE, int EPI, class S, int LATE>
 __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& t, int nb, int m0, uint8_t* smem, int32_t* sRow,
                                             float* sScaleA, float* sScaleW) {
   constexpr int BM = S::BM, BN = S::BN, WM = S::WM, WN = S::WN, RB = S::RB, NA = S::NA, NB = S::NB;
@@ -309,7 +310,7 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
     for (int i = wave; i < BN / 64; i += NW)
       g2lds4_at(p.Ws + (size_t)t.e * N + weight_row(i * 64 + lane), lds_address(sScaleW) + i * 256);
   };
-  if constexpr (I8 && !LATE) load_scales();  // older than every load of a stage
+  if constexpr (I8 && LATE == 0) load_scales();  // older than every load of a stage
 
   // Sources of this wave's loads; load j of an operand is its wave-wide load wave + NW * j of a step.
   // Rows kind: lane's chunk at row (wave + NW j) * 1024 / RB + lane / (RB / 16), contraction byte pos in the step
@@ -358,7 +359,7 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   }
   const size_t step_a = MODE == kDw ? (size_t)CR * N * 2 : RB, step_b = MODE == kFwd ? RB : (size_t)CR * K * 2;
 
-  if constexpr ((!I8 || LATE) && MODE != kDw) __syncthreads();  // every wave has its rows: the stages may be filled
+  if constexpr ((!I8 || LATE > 0) && MODE != kDw) __syncthreads();  // every wave has its rows: the stages may be filled
 
   // contraction elements of this pass (DW: rows of the expert, as many at a time as sRow holds) and its full steps
   int kd = MODE == kFwd ? K : N;
@@ -553,7 +554,7 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
     run((kd + CR - 1) / CR);
   }
 
-  if constexpr (I8 && LATE) {
+  if constexpr (I8 && LATE > 0) {
     __syncthreads();  // the stages are no longer read
     load_scales();
     wait_vmcnt<0>();
@@ -586,7 +587,7 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   // tokens: 385 us, staged 296 us).  After SiLU*mul, whose arithmetic covers the stores, the detour costs more than it
   // gains (int8 gate_up, 256 x 256 tiles of 512 experts: 430 -> 460 us); so it does in the low tiles.
   // 16-bit results go in one piece, 32-bit ones a wave row (BM / WM rows) at a time.
-  constexpr int kTop = LATE ? 4 * (BM + BN) : 0;  // the scales
+  constexpr int kTop = LATE;  // the scales stay
   constexpr bool kStaged = EPI == MOE_EPI_NONE && BM >= 64;
   auto staged = [&](auto bytes) {
     constexpr int ES = decltype(bytes)::value, PASSES = ES == 4 ? WM : 1, PR = BM / PASSES;
@@ -670,13 +671,14 @@ __global__ __launch_bounds__(S0::WM * S0::WN * 64) void ragged_gemm_kernel(Ragge
   __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
   // the row indexes lie in what the last stage later takes, so that the stages may fill the LDS; int8 tiles keep
   // room for the scales where there is any
-  constexpr bool kLate = I8 && kLds + BM * 4 + (BM < 64 ? 64 : BM) * 4 + BN * 4 > 160 * 1024;
-  constexpr bool kShareRow = (!I8 || kLate) && MODE != kDw;
+  constexpr int kScales = ((BM < 64 ? 64 : BM) + BN) * 4;  // of the highest tile, which the lower ones keep to
+  constexpr int kLate = I8 && kLds + BM * 4 + kScales > 160 * 1024 ? kScales : 0;
+  constexpr bool kShareRow = (!I8 || kLate > 0) && MODE != kDw;
   __shared__ int32_t sRowOwn[MODE == kDw ? kDwIds : (kShareRow ? 1 : BM)];
   int32_t* sRow = kShareRow ? reinterpret_cast<int32_t*>(smem + kLds - BM * 4) : sRowOwn;
-  constexpr bool kOwnScales = I8 && !kLate;
-  __shared__ __attribute__((aligned(16))) float sScaleOwn[kOwnScales ? (BM < 64 ? 64 : BM) + BN : 1];
-  float* sScaleA = I8 && kLate ? reinterpret_cast<float*>(smem) : sScaleOwn;
+  constexpr bool kOwnScales = I8 && kLate == 0;
+  __shared__ __attribute__((aligned(16))) float sScaleOwn[kOwnScales ? kScales / 4 : 1];
+  float* sScaleA = I8 && kLate > 0 ? reinterpret_cast<float*>(smem) : sScaleOwn;
   float* sScaleW = sScaleA + (BM < 64 ? 64 : BM);
   const int N = p.N, K = p.K;
   const int ND = MODE == kFwd ? (EPI == MOE_EPI_SILU_MUL ? N / 2 : N) : K;  // output columns

@@ -104,6 +104,54 @@ def test_weight_gradients_in_parts(counts, N, K, out):
     assert torch.equal(dW, moe.moe_grouped_gemm_w16_dw(dC, rows.contiguous(), None, 1, off, out_dtype=OUT[out]))
 
 
+# calls that fill the card, one for each range of the tile choice: (experts, counts drawn from)
+FULL = {
+    "decode": (200, [0, 0, 1, 2, 16, 17]),
+    "mean20": (200, [0, 1, 15, 16, 17, 31, 32, 33, 50]),
+    "mean50": (120, [0, 1, 33, 63, 64, 65, 129]),
+    "mean200": (100, [0, 1, 127, 128, 129, 255, 256, 257, 500]),
+    "mean600": (50, [0, 1, 128, 129, 256, 385, 512, 1100, 2000]),
+}
+
+
+def _full(name):
+    E, pick = FULL[name]
+    g = torch.Generator().manual_seed(E)
+    return [pick[i] for i in torch.randint(0, len(pick), (E,), generator=g).tolist()]
+
+
+@pytest.mark.parametrize("name", list(FULL))
+@pytest.mark.parametrize("N,K,dtype,out,epi", [(520, 264, BF16, BF16, NONE), (514, 136, F16, F32, NONE), (516, 72, F16, F32, NONE),
+                                               (514, 40, BF16, F16, NONE), (1040, 520, BF16, BF16, SILU), (1030, 8, F16, F16, SILU)])
+def test_full_grid_w16(name, N, K, dtype, out, epi):
+    counts = _full(name)
+    x, row_of, rows = _case(counts, 333, K, dtype, seed=N + K)
+    W = _rand((len(counts), N, K), dtype, 7, K ** -0.5)
+    C = moe.moe_grouped_gemm_w16(x, row_of, 3, W, ru.offsets_of(counts), sum(counts), epilogue=epi, out_dtype=OUT[out])
+    ref, mass = ru.grouped(rows, W, counts)
+    err = ru.sum_bound(K, mass)
+    if epi == SILU:
+        ref, err = ru.silu_mul(ref), ru.silu_bound(ref, err)
+    ru.assert_close(C, ref, err, f"{name} {N} {K}")
+
+
+@pytest.mark.parametrize("name", list(FULL))
+@pytest.mark.parametrize("N,K,dtype,out", [(520, 520, BF16, BF16), (264, 1032, F16, F32), (776, 392, F16, F16)])
+def test_full_grid_w16_gradients(name, N, K, dtype, out):
+    counts = _full(name)
+    R = sum(counts)
+    x, row_of, rows = _case(counts, 333, K, dtype, seed=N + K)
+    W, dC = _rand((len(counts), N, K), dtype, 3, K ** -0.5), _rand((R, N), dtype, 4)
+    off = ru.offsets_of(counts)
+    dA = moe.moe_grouped_gemm_w16_dx(dC, W, off, out_dtype=OUT[out])
+    ref, mass = ru.grouped(dC, W.transpose(1, 2), counts)
+    ru.assert_close(dA, ref, ru.sum_bound(N, mass), f"dA {name}")
+    dW = moe.moe_grouped_gemm_w16_dw(dC, x, row_of, 3, off, out_dtype=OUT[out])
+    ref, mass = ru.grouped_dw(dC, rows, counts)
+    ru.assert_close(dW, ref, ru.sum_bound(max(counts), mass), f"dW {name}")
+    assert torch.equal(dW, moe.moe_grouped_gemm_w16_dw(dC, rows.contiguous(), None, 1, off, out_dtype=OUT[out]))
+
+
 def test_gradients_against_differences():
     """dA and dW against central differences of the 64-bit product along random directions: the loss
     sum(C * dC) is linear in A and in W, so a difference quotient is exact up to rounding."""
@@ -327,6 +375,37 @@ def test_grouped_i8(name, N, K, out, epi):
     ru.assert_close(C, ref, err, name)
 
 
+@pytest.mark.parametrize("name", list(FULL))
+@pytest.mark.parametrize("N,K,out,epi", [(520, 272, BF16, NONE), (514, 144, F32, NONE), (516, 528, F32, NONE), (1040, 400, F16, SILU)])
+def test_full_grid_i8(name, N, K, out, epi):
+    counts = _full(name)
+    E, R = len(counts), sum(counts)
+    x, row_of, _ = _case(counts, 333, K, BF16, seed=K)
+    wq, ws = moe.moe_i8_quantize(_rand((E * N, K), F32, 2, K ** -0.5))
+    q, s = moe.moe_i8_quantize(x)
+    C = moe.moe_grouped_gemm_i8(q, s, row_of, 3, wq.view(E, N, K), ws.view(E, N), ru.offsets_of(counts), R, epilogue=epi, out_dtype=OUT[out])
+    tok = (row_of // 3).long()
+    e_of = torch.repeat_interleave(torch.arange(E, device="cuda"), torch.tensor(counts, device="cuda"))
+    exact, _ = ru.grouped(q[tok].float(), wq.view(E, N, K).float(), counts)
+    ref = exact * (s.double()[tok, None] * ws.view(E, N).double()[e_of])
+    err = 3.01 * 2.0 ** -24 * ref.abs()  # as in _i8_reference
+    if epi == SILU:
+        ref, err = ru.silu_mul(ref), ru.silu_bound(ref, err)
+    ru.assert_close(C, ref, err, name)
+
+
+@pytest.mark.parametrize("M", [900, 4097])
+def test_dense_i8_of_many_columns(M):
+    """One group with enough columns for the large tiles."""
+    N, K = 12808, 80
+    q, s = moe.moe_i8_quantize(_rand((M, K), BF16, 1))
+    wq, ws = moe.moe_i8_quantize(_rand((N, K), F32, 2, K ** -0.5))
+    ref, err = _i8_reference(q, s, wq, ws)
+    ru.assert_close(moe.moe_gemm_i8(q, s, wq, ws), ref, err)
+    ref, err = ru.silu_mul(ref), ru.silu_bound(ref, err)
+    ru.assert_close(moe.moe_gemm_i8(q, s, wq, ws, epilogue=SILU), ref, err)
+
+
 def test_i8_sums_stay_exact_at_the_largest_K():
     K = 1 << 17
     q = torch.full((3, K), 127, dtype=torch.int8, device="cuda")
@@ -526,3 +605,83 @@ def test_given_stream():
     got = moe.moe_grouped_gemm_w16(x, row_of, 3, W, off, R, stream=st), moe.moe_linear_i8(x, wq[0], ws[0], stream=st)
     st.synchronize()
     assert all(torch.equal(p, r) for p, r in zip(got, want))
+
+
+def test_binding_refusals():
+    """Tensors that would be read wrongly are refused by name."""
+    x, logits = _rand((6, 64), BF16, 1), _rand((6, 2), F32, 2)
+    W, off = _rand((2, 32, 64), BF16, 3), ru.offsets_of([4, 2])
+    q, s = moe.moe_i8_quantize(x)
+    wq, ws = moe.moe_i8_quantize(W.view(-1, 64))
+    wq, ws = wq.view(2, 32, 64), ws.view(2, 32)
+    odd, down = _rand((2, 33, 64), BF16, 4), _rand((2, 64, 16), BF16, 5)
+    calls = {
+        "w13 must": lambda: moe.moe_ffn_forward_w16(x, logits, odd, down, 1),
+        "w13_q must": lambda: moe.moe_ffn_forward_i8(x, logits, torch.zeros((2, 33, 64), dtype=torch.int8, device="cuda"),
+                                                     torch.zeros((2, 32), device="cuda"), wq, ws, 1),
+        "A must": lambda: moe.moe_grouped_gemm_w16(x.t().contiguous().t(), None, 1, W, off, 6),
+        "W must": lambda: moe.moe_grouped_gemm_w16(x, None, 1, W.half(), off, 6),
+        "expert_offsets must": lambda: moe.moe_grouped_gemm_w16(x, None, 1, W, off.long(), 6),
+        "A has 6 rows": lambda: moe.moe_grouped_gemm_w16(x, None, 1, W, off, 7),
+        "a_row_of must hold": lambda: moe.moe_grouped_gemm_w16(x, off, 1, W, off, 7),
+        "even N": lambda: moe.moe_grouped_gemm_w16(x, None, 1, W[:, :31].contiguous(), off, 6, epilogue=SILU),
+        "As must": lambda: moe.moe_gemm_i8(q, s[:5], wq[0], ws[0]),
+        "Ws must": lambda: moe.moe_grouped_gemm_i8(q, s, None, 1, wq, ws[:1], off, 6),
+        "C must": lambda: moe.moe_gemm_i8(q, s, wq[0], ws[0], C=torch.empty((6, 32), device="cuda")),
+        "dh must": lambda: moe.moe_silu_mul_grad(x, x),
+        "G must": lambda: moe.moe_silu_mul(x[:, :63].contiguous()),
+        "unknown out_dtype": lambda: moe.moe_gemm_i8(q, s, wq[0], ws[0], out_dtype=9),
+        "workspace must": lambda: moe.moe_linear_i8(x, wq[0], ws[0], workspace=torch.empty(4096, device="cuda")),
+    }
+    for text, call in calls.items():
+        with pytest.raises(ValueError, match=text):
+            call()
+
+
+def test_graphs_of_parts_and_layers():
+    """Weight gradients in parts, the one-launch linear and the layers, captured together and replayed with other
+    inputs."""
+    N, K, E, R, T = 136, 144, 2, 2400, 90
+    live = {"A": (R, K), "dC": (R, N), "x": (T, 144), "few": (3, K)}
+    W, w13, w2 = _rand((E, N, K), BF16, 1, K ** -0.5), _rand((E, 96, 144), BF16, 2, 0.1), _rand((E, 144, 48), BF16, 3, 0.1)
+    wq, ws = moe.moe_i8_quantize(W.view(-1, K))
+    wq, ws = wq.view(E, N, K), ws.view(E, N)
+    w13q, w13s = moe.moe_i8_quantize(w13.view(-1, 144))
+    w2q, w2s = moe.moe_i8_quantize(w2.view(-1, 48))
+    w13q, w13s, w2q, w2s = w13q.view(E, 96, 144), w13s.view(E, 96), w2q.view(E, 144, 48), w2s.view(E, 144)
+
+    def inputs(seed):
+        t = {n: _rand(s, BF16, seed + i) for i, (n, s) in enumerate(live.items())}
+        t["logits"] = _rand((T, E), F32, seed + 9)
+        t["off"] = ru.offsets_of([1000 + seed, R - 1000 - seed])
+        return t
+
+    def calls(t):
+        q, s = moe.moe_i8_quantize(t["A"])
+        return [moe.moe_grouped_gemm_w16(t["A"], None, 1, W, t["off"], R), moe.moe_grouped_gemm_i8(q, s, None, 1, wq, ws, t["off"], R),
+                moe.moe_grouped_gemm_w16_dx(t["dC"], W, t["off"]), moe.moe_grouped_gemm_w16_dw(t["dC"], t["A"], None, 1, t["off"]),
+                moe.moe_linear_i8(t["few"], wq[0], ws[0]), moe.moe_linear_i8(t["A"], wq[0], ws[0]),
+                moe.moe_ffn_forward_w16(t["x"], t["logits"], w13, w2, 1),
+                moe.moe_ffn_forward_i8(t["x"], t["logits"], w13q, w13s, w2q, w2s, 1)]
+
+    assert moe.moe_grouped_gemm_w16_dw_workspace_bytes(R, E, N, K) > 0
+    sets = [inputs(s) for s in (1, 200, 777)]
+    buf = {n: t.clone() for n, t in sets[0].items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls(buf)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g in graphs:  # each its own outputs and workspaces
+        with torch.cuda.graph(g):
+            outs.append(calls(buf))
+    for n in (0, 1, 2, 1, 0):
+        for name, src in sets[n].items():
+            buf[name].copy_(src)
+        graphs[n % 2].replay()
+        want = calls(sets[n])
+        graphs[1 - n % 2].replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert all(torch.equal(p, r) for p, r in zip(out, want)), n
