@@ -828,6 +828,12 @@ def moe_ffn_i8_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
     return int(load().moe_ffn_i8_workspace_bytes(T, H, I, E, k))
 
 
+def _halves(N13, name):
+    if N13 % 2:
+        raise ValueError(f"{name} must hold as many gate as up rows (got {N13})")
+    return N13 // 2
+
+
 def _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace, need_bytes):
     """Checks a layer's activations and optional buffers, makes y and the workspace where none is given."""
     dev, T = x.device, x.shape[0]
@@ -851,7 +857,7 @@ def moe_ffn_forward_i8(x, router_logits, w13_q, w13_s, w2_q, w2_s, k: int, y=Non
     T, H = _need(x, (torch.bfloat16,), (None, None), "x")
     dev = x.device
     E, N13, _ = _need(w13_q, _I8, (None, None, H), "w13_q", dev)
-    I = N13 // 2
+    I = _halves(N13, "w13_q")
     _need(w13_s, _F32, (E, 2 * I), "w13_s", dev)
     _need(w2_q, _I8, (E, H, I), "w2_q", dev)
     _need(w2_s, _F32, (E, H), "w2_s", dev)
@@ -957,7 +963,7 @@ def moe_ffn_forward_w16(x, router_logits, w13, w2, k: int, y=None, topk_ids_out=
     T, H = _need(x, bf16, (None, None), "x")
     dev = x.device
     E, N13, _ = _need(w13, bf16, (None, None, H), "w13", dev)
-    I = N13 // 2
+    I = _halves(N13, "w13")
     _need(w2, bf16, (E, H, I), "w2", dev)
     y, workspace = _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
                              moe_ffn_w16_workspace_bytes(T, H, I, E, k))
