@@ -533,6 +533,47 @@ def test_layers(kind, T, E, k, H, I):
     assert float((y.double() - ref).norm() / ref.norm()) <= bound
 
 
+# ---- more than 2^32 elements -------------------------------------------------------------------------
+
+def test_results_past_32_bits():
+    counts, N, K = [5, 4_200_000, 300], 1040, 16
+    R = sum(counts)
+    assert R * N > 2 ** 32
+    off = ru.offsets_of(counts)
+    x, W = _rand((1000, K), BF16, 1), _rand((3, N, K), BF16, 2, K ** -0.5)
+    row_of = (torch.arange(R, device="cuda") * 7 % 3000).int()
+    C = moe.moe_grouped_gemm_w16(x, row_of, 3, W, off, R)
+    h, dA = moe.moe_silu_mul(C), moe.moe_grouped_gemm_w16_dx(C, W, off)
+    dG = moe.moe_silu_mul_grad(C, h)
+    q, s = moe.moe_i8_quantize(x)
+    wq, ws = moe.moe_i8_quantize(W.view(-1, K))
+    C8 = moe.moe_grouped_gemm_i8(q, s, row_of, 3, wq.view(3, N, K), ws.view(3, N), off, R)
+    edge = 2 ** 32 // N
+    for a, b, e in ((0, 5, 0), (5, 70, 1), (edge // 2 - 2, edge // 2 + 2, 1), (edge - 2, edge + 2, 1), (R - 303, R - 300, 1), (R - 300, R, 2)):
+        tok = (row_of[a:b] // 3).long()
+        ref, mass = ru.grouped(x[tok], W[e:e + 1], [b - a])
+        ru.assert_close(C[a:b], ref, ru.sum_bound(K, mass))
+        ref, err = _i8_reference(q[tok], s[tok], wq.view(3, N, K)[e], ws.view(3, N)[e])
+        ru.assert_close(C8[a:b], ref, err)
+        part = C[a:b].contiguous()
+        ref, mass = ru.grouped(part, W[e:e + 1].transpose(1, 2), [b - a])
+        ru.assert_close(dA[a:b], ref, ru.sum_bound(N, mass))
+        assert torch.equal(h[a:b], moe.moe_silu_mul(part)) and torch.equal(dG[a:b], moe.moe_silu_mul_grad(part, h[a:b].contiguous()))
+
+
+def test_weight_gradients_past_32_bits():
+    E, N, K = 1024, 2048, 2056
+    counts = [3] + [0] * 500 + [2] + [0] * 521 + [7]
+    R = sum(counts)
+    assert len(counts) == E and E * N * K > 2 ** 32
+    x, dC = _rand((R, K), BF16, 1), _rand((R, N), BF16, 2)
+    dW = moe.moe_grouped_gemm_w16_dw(dC, x, None, 1, ru.offsets_of(counts))
+    for e, a, b in ((0, 0, 3), (501, 3, 5), (1023, 5, 12)):
+        ref, mass = ru.grouped_dw(dC[a:b], x[a:b], [b - a])
+        ru.assert_close(dW[e], ref[0], ru.sum_bound(b - a, mass[0]))
+    assert sum(int(dW[e].count_nonzero()) for e in range(E) if counts[e] == 0) == 0
+
+
 # ---- streams, graphs, repeated calls -------------------------------------------------------------------
 
 def _all_ops(x, row_of, W, wq, ws, dC, off, R):
