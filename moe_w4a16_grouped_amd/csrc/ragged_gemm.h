@@ -72,12 +72,16 @@ __device__ __forceinline__ int row_swizzle(int row) {
 __device__ __forceinline__ int col_swizzle(int crow) { return (crow & 3) | ((crow >> 1) & 4); }
 
 // Direct global->LDS loads to a wave-uniform LDS byte address (lane l writes [16l, 16l+16), or [4l, 4l+4) from
-// it); the second takes a uniform base and a 32-bit offset a lane.
+// it); the second takes a uniform base and a 32-bit offset a lane, the third the same for bytes that no other workgroup
+// reads (nontemporal).
 __device__ __forceinline__ void g2lds16_at(const void* g, uint32_t lds) {
   asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void g2lds16_at(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void g2lds16_once_at(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("global_load_lds_dwordx4 %0, %1 nt" : : "v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void g2lds4_at(const void* g, uint32_t lds) {
   asm volatile("global_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
@@ -236,14 +240,16 @@ __device__ __forceinline__ void store1(void* C, int out, size_t at, float v) {
 constexpr int kDwIds = 1024;
 
 // Shape of one tile height's work: BM x BN by WM x WN waves, steps of RB bytes, NA stages of the A operand's tile
-// and NB >= NA of the B operand's.
-template <int BM_, int BN_, int WM_, int WN_, int RB_, int NA_, int NB_ = NA_>
+// and NB >= NA of the B operand's.  ONCE: most groups are one tile high, so that the B operand is read once.
+template <int BM_, int BN_, int WM_, int WN_, int RB_, int NA_, int NB_ = NA_, bool ONCE_ = false>
 struct TileShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, RB = RB_, NA = NA_, NB = NB_;
+  static constexpr bool ONCE = ONCE_;
   static constexpr int kLds = (NA * BM + NB * BN) * RB;
 };
 struct NoTile {
   static constexpr int BM = 0, BN = 0, WM = 0, WN = 0, RB = 0, NA = 0, NB = 0, kLds = 0;
+  static constexpr bool ONCE = false;
 };
 
 // One output tile: rows t (DW: weight rows from m0) by column block nb.
@@ -399,6 +405,8 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
       const uint8_t* from = base_b + ob[j];
       if (B_T ? cols_row(j, BN * 2) >= left : pos >= left * T::kBytes) from = zero;
       g2lds16_at(from, to);
+    } else if (S::ONCE) {
+      g2lds16_once_at(base_b, ob[j], to);
     } else {
       g2lds16_at(base_b, ob[j], to);
     }
@@ -583,12 +591,13 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   const int rows = MODE == kDw ? min(N - m0, BM) : t.rows;
   const size_t first = MODE == kDw ? w_e + (size_t)m0 * K : (size_t)t.row0 * ND;  // the tile's first row in C
   // Results pass through LDS (the stages are free) and are stored as whole rows, 16 bytes a lane; stored from the
-  // registers they are 32- or 64-byte pieces of 16 rows (16-bit weight gradients of 256 experts of 1024 x 2048 over 800
-  // tokens: 385 us, staged 296 us).  After SiLU*mul, whose arithmetic covers the stores, the detour costs more than it
-  // gains (int8 gate_up, 256 x 256 tiles of 512 experts: 430 -> 460 us); so it does in the low tiles.
+  // registers they are 32- or 64-byte pieces of 16 rows.  The stores do not stay in the L2 (nontemporal), which the
+  // operands need: 16-bit weight gradients of 256 experts of 1024 x 2048 over 800 tokens take 385 us stored from the
+  // registers, 285 us staged and 231 us staged past the L2; int8 products of 256 experts of 2048 x 512 with 32-bit
+  // results 73, 72 and 67 us; int8 SiLU*mul 4096 x 8192 x 4096 122, 118 and 116 us.
   // 16-bit results go in one piece, 32-bit ones a wave row (BM / WM rows) at a time.
   constexpr int kTop = LATE;  // the scales stay
-  constexpr bool kStaged = EPI == MOE_EPI_NONE && BM >= 64;
+  constexpr bool kStaged = BM >= (EPI == MOE_EPI_SILU_MUL ? 128 : 32);  // lower ones (SiLU*mul halves the rows) gain nothing
   auto staged = [&](auto bytes) {
     constexpr int ES = decltype(bytes)::value, PASSES = ES == 4 ? WM : 1, PR = BM / PASSES;
     constexpr int NCH = BC * ES / 16, CE = 16 / ES;  // 16-byte chunks of a row, permuted by the row's number
@@ -625,7 +634,8 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
       for (int i = tid; i < PR * NCH; i += NW * 64) {
         const int r = i / NCH, row = ps * PR + r, chunk = i % NCH;
         const u32x4 w = *reinterpret_cast<const u32x4*>(buf + r * (BC * ES) + ((chunk ^ (row & (NCH - 1) & 15)) * 16));
-        if (row < rows && chunk * CE < cols) *reinterpret_cast<u32x4*>(C + ((size_t)row * ND + chunk * CE) * ES) = w;
+        if (row < rows && chunk * CE < cols)
+          __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(C + ((size_t)row * ND + chunk * CE) * ES));
       }
     }
   };
@@ -775,7 +785,8 @@ static hipError_t launch_ragged_fwd(const RaggedArgs& a, hipStream_t s) {
     return launch_ragged_cfg<T, kFwd, EPI, TileShape<64, 128, 1, 4, 128, 2>>(a, s);
   if (mean > 16 && fills(a, 32, a.N / cols, 128 / cols))
     return launch_ragged_cfg<T, kFwd, EPI, TileShape<32, 128, 1, 4, 128, 2>>(a, s);
-  if (fills(a, 16, a.N / cols, 64 / cols)) return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 2>>(a, s);
+  if (fills(a, 16, a.N / cols, 64 / cols))
+    return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 2, 2, true>>(a, s);
   return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 4>>(a, s);
 }
 

@@ -21,12 +21,13 @@ static hipError_t launch_dx(const RaggedArgs& a, hipStream_t s) {
   return launch_ragged_cfg<T, kDx, MOE_EPI_NONE, TileShape<16, 128, 1, 4, 128, 4>>(a, s);
 }
 
-// Weight gradients of 64 experts of 1024 x 2048, mean 100: 84 us with 256 x 128 tiles (two workgroups a CU), 83 us
-// with 128 x 128, 93 us with 256 x 256; mean 400: 162, 170, 166; mean 1024 (8 experts of 4096 x 14336): 1239 against
-// 1173 us with 256 x 256.
+// Weight gradients (bf16) of 64 experts of 1024 x 2048, mean 100: 73 us with 256 x 128 tiles (two workgroups a CU), 73
+// with 128 x 128, 81 with 256 x 256; mean 375: 130, 133, 139; 256 experts, mean 25: 231, 230, 258; mean 1024 (8 experts
+// of 4096 x 14336, fp16, 32-bit results): 1239 against 1090 us with 256 x 256.
 //
 // A few output tiles with many rows leave most CUs idle: the rows are then cut into parts, whose sums (fp32, in the
-// workspace) a second launch adds in order.  One group of 8192 rows, 1024 x 2048 weights (128 tiles): see dw_split.
+// workspace) a second launch adds in order.  One group of 8192 rows, 1024 x 2048 weights (128 tiles): 101
+// -> 46 us; 128 x 256 weights: 73 -> 17 us; 4096 rows, 512 x 512 weights: 39 -> 16 us.
 int dw_split(int R, int E, int N, int K) {
   const long long tiles = (long long)E * ((N + 127) / 128) * ((K + 127) / 128), mean = (long long)R / E;
   const long long most = 512 / tiles < mean / 256 ? 512 / tiles : mean / 256;  // two workgroups a CU, 256 rows a part
@@ -81,7 +82,10 @@ hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilog
 // SiLU*mul of a stored gate_up result and its gradient.  With s = 1 / (1 + exp(-g)):
 //   h = g s u,   du = dh g s,   dg = dh u s (1 + g (1 - s)).
 // Pure traffic: a thread takes 8 columns (one 16-byte load of each operand), arithmetic in fp32, one
-// rounding per output.
+// rounding per output.  (s is 0 where exp(-g) passes fp32, g < -88.)  Results are stored past the L2 (nontemporal):
+// 512 x 14336 forward 9.0 -> 7.5 us, 8191 x 14336 121 -> 117 us.  Operands that the 256 MB memory-side cache cannot
+// hold (FAR) are loaded so too: 8191 x 14336 forward 117 -> 113 us (6.2 TB/s), gradient 202 -> 183 us (6.4 TB/s), but
+// 8191 x 768, whose operands lie in that cache, 6.8 -> 8.3 us.
 template <bool F16>
 __device__ __forceinline__ void unpack8(const u32x4& w, float (&v)[8]) {
 #pragma unroll
@@ -104,7 +108,12 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
 
 __device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-template <bool F16, bool GRAD>
+constexpr long long kFarBytes = 256ll << 20;
+
+template <bool FAR>
+__device__ __forceinline__ u32x4 load16(const u32x4* p) { return FAR ? __builtin_nontemporal_load(p) : *p; }
+
+template <bool F16, bool GRAD, bool FAR>
 __global__ __launch_bounds__(256) void silu_mul_kernel(const u32x4* G, const u32x4* dh, long long n, int chunks,
                                                        u32x4* out) {
   const long long at = linear_block() * 256 + threadIdx.x;
@@ -112,24 +121,32 @@ __global__ __launch_bounds__(256) void silu_mul_kernel(const u32x4* G, const u32
   const long long row = at / chunks;
   const int c = (int)(at - row * chunks);
   float g[8], u[8], v[8];
-  unpack8<F16>(G[row * 2 * chunks + c], g);
-  unpack8<F16>(G[row * 2 * chunks + chunks + c], u);
+  unpack8<F16>(load16<FAR>(G + row * 2 * chunks + c), g);
+  unpack8<F16>(load16<FAR>(G + row * 2 * chunks + chunks + c), u);
   if constexpr (!GRAD) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid_f32(g[i]) * u[i];
-    out[at] = pack8<F16>(v);
+    __builtin_nontemporal_store(pack8<F16>(v), out + at);
   } else {
     float d[8], w[8];
-    unpack8<F16>(dh[at], d);
+    unpack8<F16>(load16<FAR>(dh + at), d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float s = sigmoid_f32(g[i]);
       v[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
       w[i] = d[i] * g[i] * s;
     }
-    out[row * 2 * chunks + c] = pack8<F16>(v);
-    out[row * 2 * chunks + chunks + c] = pack8<F16>(w);
+    __builtin_nontemporal_store(pack8<F16>(v), out + row * 2 * chunks + c);
+    __builtin_nontemporal_store(pack8<F16>(w), out + row * 2 * chunks + chunks + c);
   }
+}
+
+template <bool F16, bool GRAD>
+static hipError_t launch_silu_of(const u32x4* G, const u32x4* dh, long long n, int chunks, u32x4* out, hipStream_t s) {
+  const dim3 grid = grid2d((n + 255) / 256);
+  if (n * (GRAD ? 48 : 32) > kFarBytes) silu_mul_kernel<F16, GRAD, true><<<grid, 256, 0, s>>>(G, dh, n, chunks, out);
+  else silu_mul_kernel<F16, GRAD, false><<<grid, 256, 0, s>>>(G, dh, n, chunks, out);
+  return hipGetLastError();
 }
 
 template <bool GRAD>
@@ -137,11 +154,9 @@ static hipError_t launch_silu(const uint16_t* G, const uint16_t* dh, bool f16, l
                               hipStream_t s) {
   const int chunks = I / 8;
   const long long n = R * chunks;
-  const dim3 grid = grid2d((n + 255) / 256);
   const u32x4 *g = reinterpret_cast<const u32x4*>(G), *d = reinterpret_cast<const u32x4*>(dh);
-  if (f16) silu_mul_kernel<true, GRAD><<<grid, 256, 0, s>>>(g, d, n, chunks, reinterpret_cast<u32x4*>(out));
-  else silu_mul_kernel<false, GRAD><<<grid, 256, 0, s>>>(g, d, n, chunks, reinterpret_cast<u32x4*>(out));
-  return hipGetLastError();
+  u32x4* o = reinterpret_cast<u32x4*>(out);
+  return f16 ? launch_silu_of<true, GRAD>(g, d, n, chunks, o, s) : launch_silu_of<false, GRAD>(g, d, n, chunks, o, s);
 }
 
 hipError_t launch_silu_mul(const uint16_t* G, bool f16, long long R, int I, uint16_t* h, hipStream_t stream) {
