@@ -644,7 +644,7 @@ size_t moe_linear_i8_workspace_bytes(int32_t T, int32_t K);
  * Linear layer with int8 weights and activations quantized on the fly [ATOM, 8.2]: moe_i8_quantize of x
  * [T, K] (in_dtype as there), then moe_gemm_i8 of it, with the same results as these two calls.  workspace: at
  * least moe_linear_i8_workspace_bytes(T, K) bytes, 16-byte aligned (0 bytes, and NULL, where one launch does
- * both: T <= 16 and T * K <= 8192).  Other arguments as for moe_gemm_i8.
+ * both whatever N is: T <= 4 and T * K <= 8192).  Other arguments as for moe_gemm_i8.
  */
 moe_status_t moe_linear_i8(const void* x, int32_t in_dtype, const int8_t* Wq, const float* Ws, int32_t T, int32_t N,
                            int32_t K, int32_t epilogue, void* y, int32_t out_dtype, void* workspace,

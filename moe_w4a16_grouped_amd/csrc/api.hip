@@ -1526,7 +1526,7 @@ moe_status_t moe_gemm_i8(const int8_t* Aq, const float* As, const int8_t* Wq, co
 
 size_t moe_linear_i8_workspace_bytes(int32_t T, int32_t K) {
   if (T < 0 || K < 16 || K % 16 != 0 || (int64_t)T >= kMaxRows || K > MOE_I8_MAX_K) return 0;
-  return moe::i8_few_fits(T, K) ? 0 : up256((size_t)T * K) + up256((size_t)T * 4);
+  return moe::i8_few_always(T, K) ? 0 : up256((size_t)T * K) + up256((size_t)T * 4);
 }
 
 moe_status_t moe_linear_i8(const void* x, int32_t in_dtype, const int8_t* Wq, const float* Ws, int32_t T, int32_t N,
@@ -1536,21 +1536,21 @@ moe_status_t moe_linear_i8(const void* x, int32_t in_dtype, const int8_t* Wq, co
   if (in_dtype != MOE_IN_BF16 && in_dtype != MOE_IN_F16 && in_dtype != MOE_IN_F32)
     return fail(MOE_ERR_INVALID_ARG, "%s: unknown in_dtype %d", who, in_dtype);
   if (T > 0 && !x) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
-  const bool few = T > 0 && K > 0 && moe::i8_few_fits(T, K);  // one launch, no workspace
-  int8_t* q = few ? nullptr : static_cast<int8_t*>(workspace);
+  const bool always = T > 0 && K > 0 && moe::i8_few_always(T, K);  // one launch, no workspace
+  int8_t* q = always ? nullptr : static_cast<int8_t*>(workspace);
   float* s = q ? reinterpret_cast<float*>(reinterpret_cast<char*>(q) + up256((size_t)(T < 0 ? 0 : T) * (K < 0 ? 0 : K))) : nullptr;
-  // (the few-rows form reads x itself, which stands for codes and scales in the checks)
-  if (moe_status_t st = check_i8_gemm(few ? static_cast<const int8_t*>(x) : q, few ? static_cast<const float*>(x) : s, Wq, Ws,
+  // (the one-launch form reads x itself, which stands for codes and scales in the checks)
+  if (moe_status_t st = check_i8_gemm(always ? static_cast<const int8_t*>(x) : q, always ? static_cast<const float*>(x) : s, Wq, Ws,
                                       T, 1, N, K, epilogue, y, out_dtype, who))
     return st;
   if (T == 0) return ok();
   if (!aligned16(x)) return fail(MOE_ERR_MISALIGNED, "%s: x needs 16-byte alignment", who);
-  if (few)
-    return hip_status(moe::launch_linear_i8_few(x, in_dtype, Wq, Ws, T, N, K, epilogue, y, out_dtype, (hipStream_t)stream),
-                      "moe_linear_i8 launch");
   const size_t need = moe_linear_i8_workspace_bytes(T, K);
   if (workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu B < required %zu B", who, workspace_bytes, need);
+  if (moe::i8_few_fits(T, K, epilogue == MOE_EPI_SILU_MUL ? N / 2 : N))
+    return hip_status(moe::launch_linear_i8_few(x, in_dtype, Wq, Ws, T, N, K, epilogue, y, out_dtype, (hipStream_t)stream),
+                      "moe_linear_i8 launch");
   hipError_t e = moe::launch_i8_quant(x, in_dtype, T, K, q, s, (hipStream_t)stream);
   if (e != hipSuccess) return hip_status(e, "x quantization launch");
   moe::RaggedArgs a{q, s, nullptr, 1, Wq, Ws, nullptr, T, 1, N, K, y, out_dtype};

@@ -130,88 +130,115 @@ hipError_t launch_i8_quant(const void* x, int in_dtype, int rows, int K, int8_t*
 }
 
 // ---------------------------------------------------------------------------------------------------
-// A few rows (T <= 16, T * K <= kI8FewElems) in one launch: every workgroup quantizes the rows itself, into LDS, while
-// its first weights are on their way.  Four waves: two halves of the contraction by two blocks of 32 weight rows
-// (SiLU*mul: 16 gate and their 16 up rows); weights go straight to registers, kI8FewAhead 64-byte groups at a time;
-// the halves' integer sums are exact in any order and meet in LDS.  Bound by latency: 1 x 2048 x 768 takes one round
-// trip for x and the weights, the arithmetic of a row, and a launch: 7.9 us a call, with the two launches 12.9 us.
+// A few rows (T <= 16, T * K <= kI8FewElems) in one launch: a workgroup takes all of them and 16 columns (SiLU*mul: 16
+// gate rows of the weights and their up rows), quantizes the rows itself, into LDS, and its four waves take a quarter
+// of the contraction each; their integer sums are exact in any order and meet in LDS.  x is asked for first and the
+// weights and their scales right behind it, straight to registers, kI8FewAhead 64-byte groups at a time, so that one
+// round trip covers them all.  Bound by latency, us on the device, this against the two launches: 1 x 2048 x 768 4.2
+// against 7.4, 1 x 28672 x 4096 26 against 34, 4 x 2048 x 2048 6.5 against 8.9, 8 x 2048 x 768 6.6 against 7.4, 16 x
+// 2048 x 512 7.2 against 7.1 (eager calls: 8 against 12).  Every workgroup repeats the quantization: with more than
+// kI8FewCols columns more than four rows take the two launches (5 x 8192 x 1600: 12.1 against 9.5, 8 x 28672 x 1024: 20
+// against 12.5).
 constexpr int kI8FewRows = 16;
 constexpr int kI8FewElems = 8192;
+constexpr int kI8FewCols = 4096;
 constexpr int kI8FewAhead = 8;
 
-bool i8_few_fits(int T, int K) { return T <= kI8FewRows && (long long)T * K <= kI8FewElems; }
+bool i8_few_always(int T, int K) { return T <= 4 && (long long)T * K <= kI8FewElems; }
+bool i8_few_fits(int T, int K, int cols) {
+  return i8_few_always(T, K) || (T <= kI8FewRows && (long long)T * K <= kI8FewElems && cols <= kI8FewCols);
+}
 
-template <int IN, int EPI>
+// 256 threads a row for one row, 128 for two, 64 (a wave) for more
+__device__ __forceinline__ int few_threads(int rows) { return rows == 1 ? 256 : (rows == 2 ? 128 : 64); }
+
+// ROWS: rows of a thread, at most; CH: chunks of 8 elements that it holds of each.
+template <int IN, int EPI, int ROWS, int CH>
 __global__ __launch_bounds__(256) void linear_i8_few_kernel(const void* __restrict__ x, const int8_t* __restrict__ W,
                                                             const float* __restrict__ Ws, int T, int N, int K,
                                                             void* __restrict__ y, int out) {
-  // codes [T][K rounded to 64, and 16 more], rows 16 bytes apart in the banks
+  constexpr bool SILU = EPI == MOE_EPI_SILU_MUL;
+  constexpr int NB = SILU ? 2 : 1;  // blocks of 16 weight rows
+  // codes [rows][K rounded to 64, and 16 more], rows 16 bytes apart in the banks
   __shared__ __attribute__((aligned(16))) uint8_t codes[kI8FewElems + kI8FewRows * 80];
   __shared__ float sx[kI8FewRows];
   __shared__ uint32_t wmax[4];
-  __shared__ int32_t part[2 * 64 * 8];
+  __shared__ int32_t part[3][NB * 4][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, q = lane >> 4;
-  const int wk = wave >> 1, wn = wave & 1;
-  const int ND = EPI == MOE_EPI_SILU_MUL ? N / 2 : N;
-  constexpr int BC = EPI == MOE_EPI_SILU_MUL ? 32 : 64;
-  const int col0 = blockIdx.x * BC + wn * (BC / 2);
-  const int groups = (K + 63) / 64, half = (groups + 1) / 2;
-  const int g0 = wk * half, g1 = min(groups, g0 + half);
+  const int ND = SILU ? N / 2 : N;
+  const int col0 = blockIdx.x * 16;
+  const int groups = (K + 63) / 64, share = (groups + 3) / 4;
+  const int g0 = min(wave * share, groups), g1 = min(groups, g0 + share);
   const int stride = groups * 64 + 16;
 
-  const int8_t* wrow[2];
+  const int tpr = few_threads(T), nc = K / 8, c0 = tid % tpr, r0 = tid / tpr;
+  float v[ROWS][CH][8];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    int n = EPI == MOE_EPI_SILU_MUL ? col0 + l16 : col0 + 16 * b + l16;
-    if (n >= ND) n = 0;  // only reaches results that are not stored
-    if (EPI == MOE_EPI_SILU_MUL && b == 1) n += ND;
-    wrow[b] = W + (size_t)n * K;
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = min(r0 + i * (256 / tpr), T - 1);
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+      if (c0 + j * tpr < nc) i8_load8<IN>(x, (size_t)r * K + 8 * (size_t)(c0 + j * tpr), v[i][j]);
   }
-  u32x4 w[kI8FewAhead][2];
+  __builtin_amdgcn_sched_barrier(0);
+
+  const int8_t* wrow[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int n = col0 + l16;  // past the edge row 0, which only reaches results that are not stored
+    wrow[b] = W + (size_t)((n < ND ? n : 0) + b * ND) * K;
+  }
+  u32x4 w[kI8FewAhead][NB];
   auto load = [&](int g) {  // groups g .. g + kI8FewAhead - 1 of this wave's share; zeros past the row's end
 #pragma unroll
     for (int i = 0; i < kI8FewAhead; ++i) {
       const int k = (g + i) * 64 + 16 * q;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
         w[i][b] = g + i < g1 && k < K ? *reinterpret_cast<const u32x4*>(wrow[b] + k) : u32x4{0u, 0u, 0u, 0u};
     }
   };
   load(g0);
-
-  // 256 threads a row for one row, 128 for two, 64 (a wave) for more
-  const int tpr = T == 1 ? 256 : (T == 2 ? 128 : 64), rpp = 256 / tpr;
-  const int nc = K / 8;
-  for (int r0 = 0; r0 < T; r0 += rpp) {
-    const int r = r0 + tid / tpr, rr = min(r, T - 1), c0 = tid % tpr;
-    uint32_t m = 0;
-    float v[8];
-    for (int c = c0; c < nc; c += tpr) {
-      i8_load8<IN>(x, (size_t)rr * K + 8 * (size_t)c, v);
-      m = i8_amax8(v, m);
+  float ws[NB][4];  // the scales of wave 0's results
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = col0 + 4 * q + i;
+      ws[b][i] = Ws[(n < ND ? n : 0) + b * ND];
     }
+  __builtin_amdgcn_sched_barrier(0);
+
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = r0 + i * (256 / tpr);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+      if (c0 + j * tpr < nc) m = i8_amax8(v[i][j], m);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-    if (tpr > 64) {  // T <= 2: one pass, whole waves a row
+    if (ROWS == 1 && tpr > 64) {  // one or two rows, whole waves a row
       if (lane == 0) wmax[wave] = m;
       __syncthreads();
       const int w0 = wave / (tpr / 64) * (tpr / 64);
-      for (int i = 0; i < tpr / 64; ++i) m = max(m, wmax[w0 + i]);
+      for (int k = 0; k < tpr / 64; ++k) m = max(m, wmax[w0 + k]);
     }
     const float sc = i8_scale(m);
     if (r < T) {
       if (c0 == 0) sx[r] = sc;
-      for (int c = c0; c < nc; c += tpr) {
-        if (nc > tpr) i8_load8<IN>(x, (size_t)r * K + 8 * (size_t)c, v);  // else v still holds them
-        *reinterpret_cast<u32x2*>(codes + r * stride + 8 * c) = i8_codes8(v, sc);
-      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        if (c0 + j * tpr < nc) *reinterpret_cast<u32x2*>(codes + r * stride + 8 * (c0 + j * tpr)) = i8_codes8(v[i][j], sc);
       // codes past the row's end meet weights of zero
     }
   }
   __syncthreads();
 
-  i32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  i32x4 acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = i32x4{0, 0, 0, 0};
   const uint8_t* arow = codes + min(l16, T - 1) * stride + 16 * q;
   for (int g = g0; g < g1; g += kI8FewAhead) {
     if (g > g0) load(g);
@@ -219,49 +246,62 @@ __global__ __launch_bounds__(256) void linear_i8_few_kernel(const void* __restri
     for (int i = 0; i < kI8FewAhead; ++i) {
       const u32x4 a = *reinterpret_cast<const u32x4*>(arow + min(g + i, groups - 1) * 64);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) acc[b] = ElemI8::mfma(w[i][b], a, acc[b]);
+      for (int b = 0; b < NB; ++b) acc[b] = ElemI8::mfma(w[i][b], a, acc[b]);
     }
   }
-  if (wk == 1) {
+  if (wave > 0) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) part[(wn * 64 + lane) * 8 + b * 4 + i] = acc[b][i];
+      for (int i = 0; i < 4; ++i) part[wave - 1][b * 4 + i][lane] = acc[b][i];
   }
   __syncthreads();
-  if (wk == 1 || l16 >= T) return;
+  if (wave > 0 || l16 >= T) return;
   const float sa = sx[l16];
+  auto sum = [&](int b, int i) {
+    return (float)(acc[b][i] + part[0][b * 4 + i][lane] + part[1][b * 4 + i][lane] + part[2][b * 4 + i][lane]) * (sa * ws[b][i]);
+  };
+  const int col = col0 + 4 * q;
+  const size_t at = (size_t)l16 * ND + col;
+  float r[4];
 #pragma unroll
-  for (int b = 0; b < (EPI == MOE_EPI_SILU_MUL ? 1 : 2); ++b) {
+  for (int i = 0; i < 4; ++i) r[i] = SILU ? silu_f32(sum(0, i)) * sum(NB - 1, i) : sum(0, i);
+  if ((ND & 3) == 0) {
+    if (col < ND) store4(y, out, at, r);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int col = col0 + b * 16 + 4 * q + i;
-      if (col >= ND) continue;
-      float v = (float)(acc[b][i] + part[(wn * 64 + lane) * 8 + b * 4 + i]) * (sa * Ws[col]);
-      if constexpr (EPI == MOE_EPI_SILU_MUL) {
-        const float u = (float)(acc[1][i] + part[(wn * 64 + lane) * 8 + 4 + i]) * (sa * Ws[ND + col]);
-        v = silu_f32(v) * u;
-      }
-      store1(y, out, (size_t)l16 * ND + col, v);
-    }
+    for (int i = 0; i < 4; ++i)
+      if (col + i < ND) store1(y, out, at + i, r[i]);
   }
 }
 
-template <int IN>
+template <int IN, int ROWS, int CH>
 static hipError_t launch_few(const void* x, const int8_t* Wq, const float* Ws, int T, int N, int K, int epilogue, void* y,
                              int out, hipStream_t s) {
-  if (epilogue == MOE_EPI_SILU_MUL)
-    linear_i8_few_kernel<IN, MOE_EPI_SILU_MUL><<<(N / 2 + 31) / 32, 256, 0, s>>>(x, Wq, Ws, T, N, K, y, out);
-  else
-    linear_i8_few_kernel<IN, MOE_EPI_NONE><<<(N + 63) / 64, 256, 0, s>>>(x, Wq, Ws, T, N, K, y, out);
+  const bool silu = epilogue == MOE_EPI_SILU_MUL;
+  const int nd = silu ? N / 2 : N;
+  const int grid = (nd + 15) / 16;
+  if (silu) linear_i8_few_kernel<IN, MOE_EPI_SILU_MUL, ROWS, CH><<<grid, 256, 0, s>>>(x, Wq, Ws, T, N, K, y, out);
+  else linear_i8_few_kernel<IN, MOE_EPI_NONE, ROWS, CH><<<grid, 256, 0, s>>>(x, Wq, Ws, T, N, K, y, out);
   return hipGetLastError();
+}
+
+// T * K <= kI8FewElems bounds the chunks of a row: K <= 8192, 4096 and 2730 for one, two and three rows (4, 4 and 6 of
+// 256, 128 and 64 threads), 2048 for four (4), 1638 for five (4), 910 for nine (2).
+template <int IN>
+static hipError_t launch_few_of(const void* x, const int8_t* Wq, const float* Ws, int T, int N, int K, int epilogue,
+                                void* y, int out, hipStream_t s) {
+  if (T == 3) return launch_few<IN, 1, 6>(x, Wq, Ws, T, N, K, epilogue, y, out, s);
+  if (T <= 4) return launch_few<IN, 1, 4>(x, Wq, Ws, T, N, K, epilogue, y, out, s);
+  if (T <= 8) return launch_few<IN, 2, 4>(x, Wq, Ws, T, N, K, epilogue, y, out, s);
+  return launch_few<IN, 4, 2>(x, Wq, Ws, T, N, K, epilogue, y, out, s);
 }
 
 hipError_t launch_linear_i8_few(const void* x, int in_dtype, const int8_t* Wq, const float* Ws, int T, int N, int K,
                                 int epilogue, void* y, int out, hipStream_t stream) {
-  if (in_dtype == MOE_IN_F32) return launch_few<MOE_IN_F32>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
-  if (in_dtype == MOE_IN_F16) return launch_few<MOE_IN_F16>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
-  return launch_few<MOE_IN_BF16>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
+  if (in_dtype == MOE_IN_F32) return launch_few_of<MOE_IN_F32>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
+  if (in_dtype == MOE_IN_F16) return launch_few_of<MOE_IN_F16>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
+  return launch_few_of<MOE_IN_BF16>(x, Wq, Ws, T, N, K, epilogue, y, out, stream);
 }
 
 hipError_t launch_ragged_i8(const RaggedArgs& a, int epilogue, hipStream_t stream) {

@@ -196,7 +196,8 @@ hipError_t launch_ragged_i8(const RaggedArgs& a, int epilogue, hipStream_t strea
 // x (MOE_IN_*) [rows, K] -> codes [rows, K] and scales [rows].
 hipError_t launch_i8_quant(const void* x, int in_dtype, int rows, int K, int8_t* q, float* s, hipStream_t stream);
 // The quantization and the dense product of a few rows in one launch, without a workspace.
-bool i8_few_fits(int T, int K);
+bool i8_few_fits(int T, int K, int cols);
+bool i8_few_always(int T, int K);  // for any number of columns
 hipError_t launch_linear_i8_few(const void* x, int in_dtype, const int8_t* Wq, const float* Ws, int T, int N, int K,
                                 int epilogue, void* y, int out, hipStream_t stream);
 // gate_up G [R, 2I] -> h [R, I], and its gradient (16-bit types).

@@ -354,6 +354,20 @@ def test_linear_i8(T, N, K, dtype, out, epi):
     assert torch.equal(y, moe.moe_gemm_i8(q2, s2, wq, ws, epilogue=epi, out_dtype=OUT[out]))
 
 
+@pytest.mark.parametrize("T,K", [(1, 16), (1, 8192), (2, 4096), (3, 2720), (4, 2048), (5, 1632), (8, 1024), (9, 896), (12, 672), (16, 512), (16, 16)])
+@pytest.mark.parametrize("N,dtype,out,epi", [(70, BF16, BF16, NONE), (4200, F16, F32, NONE), (100, F32, F16, SILU), (38, BF16, BF16, SILU)])
+def test_linear_i8_of_few_rows(T, K, N, dtype, out, epi):
+    """The most that one launch takes of each number of rows, with columns that end inside a block."""
+    x, (wq, ws) = _rand((T, K), dtype, T), moe.moe_i8_quantize(_rand((N, K), F32, N, K ** -0.5))
+    y = moe.moe_linear_i8(x, wq, ws, epilogue=epi, out_dtype=OUT[out])
+    q, s = moe.moe_i8_quantize(x)
+    ref, err = _i8_reference(q, s, wq, ws)
+    if epi == SILU:
+        ref, err = ru.silu_mul(ref), ru.silu_bound(ref, err)
+    ru.assert_close(y, ref, err)
+    assert torch.equal(y, moe.moe_gemm_i8(q, s, wq, ws, epilogue=epi, out_dtype=OUT[out]))
+
+
 @pytest.mark.parametrize("name", list(GROUPS))
 @pytest.mark.parametrize("N,K,out,epi", [(256, 256, BF16, SILU), (133, 80, F32, NONE), (260, 1040, F16, NONE)])
 def test_grouped_i8(name, N, K, out, epi):
