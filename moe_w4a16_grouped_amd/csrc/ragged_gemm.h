@@ -594,7 +594,9 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   // registers they are 32- or 64-byte pieces of 16 rows.  The stores do not stay in the L2 (nontemporal), which the
   // operands need: 16-bit weight gradients of 256 experts of 1024 x 2048 over 800 tokens take 385 us stored from the
   // registers, 285 us staged and 231 us staged past the L2; int8 products of 256 experts of 2048 x 512 with 32-bit
-  // results 73, 72 and 67 us; int8 SiLU*mul 4096 x 8192 x 4096 122, 118 and 116 us.
+  // results 73, 72 and 67 us; int8 SiLU*mul 4096 x 8192 x 4096 122, 118 and 116 us.  Rows that do not begin on 64 bytes
+  // stay, as the L2 has to put together the lines that two tiles share (16-bit weight gradients of 14 experts of 2424 x
+  // 4528: 70 us, past the L2 113 us).
   // 16-bit results go in one piece, 32-bit ones a wave row (BM / WM rows) at a time.
   constexpr int kTop = LATE;  // the scales stay
   constexpr bool kStaged = BM >= (EPI == MOE_EPI_SILU_MUL ? 128 : 32);  // lower ones (SiLU*mul halves the rows) gain nothing
@@ -630,13 +632,20 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
       }
       __syncthreads();
       uint8_t* C = static_cast<uint8_t*>(p.C) + (first + nb * BC) * ES;
+      auto copy_out = [&](auto way) {
 #pragma unroll 4
-      for (int i = tid; i < PR * NCH; i += NW * 64) {
-        const int r = i / NCH, row = ps * PR + r, chunk = i % NCH;
-        const u32x4 w = *reinterpret_cast<const u32x4*>(buf + r * (BC * ES) + ((chunk ^ (row & (NCH - 1) & 15)) * 16));
-        if (row < rows && chunk * CE < cols)
-          __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(C + ((size_t)row * ND + chunk * CE) * ES));
-      }
+        for (int i = tid; i < PR * NCH; i += NW * 64) {
+          const int r = i / NCH, row = ps * PR + r, chunk = i % NCH;
+          const u32x4 w = *reinterpret_cast<const u32x4*>(buf + r * (BC * ES) + ((chunk ^ (row & (NCH - 1) & 15)) * 16));
+          if (row >= rows || chunk * CE >= cols) continue;
+          u32x4* to = reinterpret_cast<u32x4*>(C + ((size_t)row * ND + chunk * CE) * ES);
+          if constexpr (decltype(way)::value) __builtin_nontemporal_store(w, to);
+          else *to = w;
+        }
+      };
+      // (a loop of its own for each: a choice at every store would lose the hint)
+      if ((size_t)ND * ES % 64 == 0) copy_out(std::true_type{});
+      else copy_out(std::false_type{});
     }
   };
   if constexpr (kStaged) {
@@ -768,6 +777,8 @@ static hipError_t launch_ragged_cfg(const RaggedArgs& a, hipStream_t s) {
 // no better).  Measured with weights from HBM, TB/s of weights or PFLOP/s, 64 experts of 1024 x 2048 unless said:
 //   mean   1: 16 x 64 tiles with 2 stages (8 workgroups a CU) against 16 x 128 with 4: int8, 53 of 128 experts of
 //             1536 x 2048, 5.2 against 4.6 TB/s; fp16 5.1 against 4.9;
+//             the weights loaded past the L2 where their rows are whole 128-byte lines (K 2048: int8 33 -> 28 us, fp16
+//             63 -> 57 us; K 2064, whose lines two steps share: int8 40 -> 57 us, fp16 91 -> 122 us);
 //   mean  25: 32 x 128 against 64 x 128: int8 4.6 against 4.3, fp16 5.5 against 5.5 (256 experts);
 //   mean  50: 64 x 128 against 32 x 128: int8 4.4 against 3.5, fp16 3.8 against 3.3;
 //   mean 100: 64 x 128 against 256 x 256: fp16 0.29 against 0.29, int8 0.60 against 0.59;
@@ -785,8 +796,10 @@ static hipError_t launch_ragged_fwd(const RaggedArgs& a, hipStream_t s) {
     return launch_ragged_cfg<T, kFwd, EPI, TileShape<64, 128, 1, 4, 128, 2>>(a, s);
   if (mean > 16 && fills(a, 32, a.N / cols, 128 / cols))
     return launch_ragged_cfg<T, kFwd, EPI, TileShape<32, 128, 1, 4, 128, 2>>(a, s);
-  if (fills(a, 16, a.N / cols, 64 / cols))
-    return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 2, 2, true>>(a, s);
+  if (fills(a, 16, a.N / cols, 64 / cols)) {
+    if ((long long)a.K * T::kBytes % 128 == 0) return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 2, 2, true>>(a, s);
+    return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 2>>(a, s);
+  }
   return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 4>>(a, s);
 }
 

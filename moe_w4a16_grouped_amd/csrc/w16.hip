@@ -82,10 +82,11 @@ hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilog
 // SiLU*mul of a stored gate_up result and its gradient.  With s = 1 / (1 + exp(-g)):
 //   h = g s u,   du = dh g s,   dg = dh u s (1 + g (1 - s)).
 // Pure traffic: a thread takes 8 columns (one 16-byte load of each operand), arithmetic in fp32, one
-// rounding per output.  (s is 0 where exp(-g) passes fp32, g < -88.)  Results are stored past the L2 (nontemporal):
-// 512 x 14336 forward 9.0 -> 7.5 us, 8191 x 14336 121 -> 117 us.  Operands that the 256 MB memory-side cache cannot
-// hold (FAR) are loaded so too: 8191 x 14336 forward 117 -> 113 us (6.2 TB/s), gradient 202 -> 183 us (6.4 TB/s), but
-// 8191 x 768, whose operands lie in that cache, 6.8 -> 8.3 us.
+// rounding per output.  (s is 0 where exp(-g) passes fp32, g < -88.)  PAST 1: results are stored past the L2
+// (nontemporal), 512 x 14336 forward 9.0 -> 7.5 us, 8191 x 14336 121 -> 117 us, but 512 x 776 3.0 -> 3.4 us, so not a few
+// megabytes, which the next launch finds in the L2s.  PAST 2: operands that the 256 MB memory-side cache cannot hold are
+// loaded so too: 8191 x 14336 forward 117 -> 113 us (6.2 TB/s), gradient 202 -> 183 us (6.4 TB/s), but 8191 x 768, whose
+// operands lie in that cache, 6.8 -> 8.3 us.
 template <bool F16>
 __device__ __forceinline__ void unpack8(const u32x4& w, float (&v)[8]) {
 #pragma unroll
@@ -108,12 +109,17 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
 
 __device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-constexpr long long kFarBytes = 256ll << 20;
+constexpr long long kNearBytes = 8ll << 20, kFarBytes = 256ll << 20;
 
-template <bool FAR>
-__device__ __forceinline__ u32x4 load16(const u32x4* p) { return FAR ? __builtin_nontemporal_load(p) : *p; }
+template <int PAST>
+__device__ __forceinline__ u32x4 load16(const u32x4* p) { return PAST > 1 ? __builtin_nontemporal_load(p) : *p; }
+template <int PAST>
+__device__ __forceinline__ void store16(const u32x4& v, u32x4* p) {
+  if (PAST > 0) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
 
-template <bool F16, bool GRAD, bool FAR>
+template <bool F16, bool GRAD, int PAST>
 __global__ __launch_bounds__(256) void silu_mul_kernel(const u32x4* G, const u32x4* dh, long long n, int chunks,
                                                        u32x4* out) {
   const long long at = linear_block() * 256 + threadIdx.x;
@@ -121,31 +127,32 @@ __global__ __launch_bounds__(256) void silu_mul_kernel(const u32x4* G, const u32
   const long long row = at / chunks;
   const int c = (int)(at - row * chunks);
   float g[8], u[8], v[8];
-  unpack8<F16>(load16<FAR>(G + row * 2 * chunks + c), g);
-  unpack8<F16>(load16<FAR>(G + row * 2 * chunks + chunks + c), u);
+  unpack8<F16>(load16<PAST>(G + row * 2 * chunks + c), g);
+  unpack8<F16>(load16<PAST>(G + row * 2 * chunks + chunks + c), u);
   if constexpr (!GRAD) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid_f32(g[i]) * u[i];
-    __builtin_nontemporal_store(pack8<F16>(v), out + at);
+    store16<PAST>(pack8<F16>(v), out + at);
   } else {
     float d[8], w[8];
-    unpack8<F16>(load16<FAR>(dh + at), d);
+    unpack8<F16>(load16<PAST>(dh + at), d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float s = sigmoid_f32(g[i]);
       v[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
       w[i] = d[i] * g[i] * s;
     }
-    __builtin_nontemporal_store(pack8<F16>(v), out + row * 2 * chunks + c);
-    __builtin_nontemporal_store(pack8<F16>(w), out + row * 2 * chunks + chunks + c);
+    store16<PAST>(pack8<F16>(v), out + row * 2 * chunks + c);
+    store16<PAST>(pack8<F16>(w), out + row * 2 * chunks + chunks + c);
   }
 }
 
 template <bool F16, bool GRAD>
 static hipError_t launch_silu_of(const u32x4* G, const u32x4* dh, long long n, int chunks, u32x4* out, hipStream_t s) {
   const dim3 grid = grid2d((n + 255) / 256);
-  if (n * (GRAD ? 48 : 32) > kFarBytes) silu_mul_kernel<F16, GRAD, true><<<grid, 256, 0, s>>>(G, dh, n, chunks, out);
-  else silu_mul_kernel<F16, GRAD, false><<<grid, 256, 0, s>>>(G, dh, n, chunks, out);
+  if (n * (GRAD ? 48 : 32) > kFarBytes) silu_mul_kernel<F16, GRAD, 2><<<grid, 256, 0, s>>>(G, dh, n, chunks, out);
+  else if (n * (GRAD ? 32 : 16) > kNearBytes) silu_mul_kernel<F16, GRAD, 1><<<grid, 256, 0, s>>>(G, dh, n, chunks, out);
+  else silu_mul_kernel<F16, GRAD, 0><<<grid, 256, 0, s>>>(G, dh, n, chunks, out);
   return hipGetLastError();
 }
 
