@@ -135,6 +135,27 @@ def test_full_grid_w16(name, N, K, dtype, out, epi):
     ru.assert_close(C, ref, err, f"{name} {N} {K}")
 
 
+@pytest.mark.parametrize("counts", [[700, 0, 580], [1280], [256, 256, 300, 129, 257], [1, 1400]])
+@pytest.mark.parametrize("dtype,out,epi", [(BF16, BF16, NONE), (F16, F32, NONE), (BF16, BF16, SILU)])
+def test_last_round_in_halves(counts, dtype, out, epi):
+    """A little more than one round of the highest tiles on the card, whose last ones are cut in halves."""
+    N, K, R = 14336, 2056, sum(counts)
+    A, W = _rand((R, K), dtype, 1), _rand((len(counts), N, K), dtype, 2, K ** -0.5)
+    C = moe.moe_grouped_gemm_w16(A, None, 1, W, ru.offsets_of(counts), R, epilogue=epi, out_dtype=OUT[out])
+    ref, mass = ru.grouped(A, W, counts)
+    err = ru.sum_bound(K, mass)
+    if epi == SILU:
+        ref, err = ru.silu_mul(ref), ru.silu_bound(ref, err)
+    ru.assert_close(C, ref, err, counts)
+    q, s = moe.moe_i8_quantize(A[:, :2048].contiguous().repeat(1, 2))
+    wq, ws = moe.moe_i8_quantize(W[0, :, :2048].repeat(1, 2))
+    C = moe.moe_gemm_i8(q, s, wq, ws, epilogue=epi, out_dtype=OUT[out])
+    ref, err = _i8_reference(q, s, wq, ws)
+    if epi == SILU:
+        ref, err = ru.silu_mul(ref), ru.silu_bound(ref, err)
+    ru.assert_close(C, ref, err, counts)
+
+
 @pytest.mark.parametrize("name", list(FULL))
 @pytest.mark.parametrize("N,K,dtype,out", [(520, 520, BF16, BF16), (264, 1032, F16, F32), (776, 392, F16, F16)])
 def test_full_grid_w16_gradients(name, N, K, dtype, out):
