@@ -15,7 +15,7 @@
 // column j).  16-byte chunks are XOR-swizzled so that neither kind of read has bank conflicts.
 //
 // What bounds it.  Many rows: the matrix units' power and the barrier of a step, one workgroup of 8 waves a CU: fp16
-// 8 experts of 4096 x 14336 over 8192 rows 950-1030 us (0.93-1.01 PFLOP/s, units busy 51 % of the cycles), int8 4096 x
+// 8 experts of 4096 x 14336 over 8192 rows 930-980 us (0.98-1.03 PFLOP/s, units busy 51 % of the cycles), int8 4096 x
 // 28672 x 4096 402 us (2.4 POP/s, 52 %).  Few rows: the weights' bytes, many small workgroups a CU: 64 rows over 128
 // experts of 1536 x 2048, int8 28 us, bf16 57 us (5.7-5.9 TB/s).
 //
