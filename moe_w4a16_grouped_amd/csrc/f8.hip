@@ -292,11 +292,12 @@ constexpr int kF8MmHLD = kF8MmBN / 2 + 4;  // padded LDS row of the h tile (floa
 constexpr int kF8MmA = kF8MmBM * 128, kF8MmB = kF8MmBN * 128;  // code bytes per stage
 constexpr int kF8MmStage = kF8MmA + kF8MmB + (kF8MmBM + kF8MmBN) * 4;
 
-// Direct global->LDS 4-byte load (lane l writes LDS bytes [4l, 4l+4) after the wave-uniform base).
+// Direct global->LDS 4-byte load (lane l writes LDS bytes [4l, 4l+4) after the wave-uniform base); the wait
+// state after the write of m0 as in g2lds16.
 __device__ __forceinline__ void g2lds4(const void* g, void* lds_wave_base) {
   const uint32_t lds = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds_wave_base);
-  asm volatile("global_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
 
 __device__ __forceinline__ int f8_swz(int row) { return (row >> 1) & 7; }

@@ -140,11 +140,14 @@ __device__ __forceinline__ void wait_vmcnt() {
 
 // Direct global->LDS 16-byte load (lane l writes LDS bytes [16l, 16l+16) after the wave-uniform
 // base).  Issued through inline assembly so that the compiler does not fence every later LDS read
-// behind it; the kernel orders these loads itself with explicit vmcnt waits and barriers.
+// behind it; the kernel orders these loads itself with explicit vmcnt waits and barriers.  The compiler does
+// not look into the assembly either for the wait states that the hardware leaves to the program: one between
+// the scalar write of m0 and a load to LDS (here s_nop 0), and five between a vector instruction's write of a
+// scalar register and a load whose address it is (see ragged_gemm.h).
 __device__ __forceinline__ void g2lds16(const void* g, void* lds_wave_base) {
   const uint32_t lds = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds_wave_base);
-  asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
 
 

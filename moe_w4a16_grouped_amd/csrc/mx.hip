@@ -623,11 +623,12 @@ constexpr int kMxMmA = kMxMmBM * 64, kMxMmB = kMxMmBN * 64;  // code bytes per s
 constexpr int kMxMmA8 = kMxMmBM * 128;                        // E4M3 activation bytes per stage (W4A8)
 constexpr int kMxMmHLD = kMxMmBN / 2 + 4;                     // padded LDS row of the h tile (floats)
 
-// Direct global->LDS 4-byte load (lane l writes LDS bytes [4l, 4l+4) after the wave-uniform base).
+// Direct global->LDS 4-byte load (lane l writes LDS bytes [4l, 4l+4) after the wave-uniform base); the wait
+// state after the write of m0 as in g2lds16.
 __device__ __forceinline__ void g2lds4_mx(const void* g, void* lds_wave_base) {
   const uint32_t lds = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds_wave_base);
-  asm volatile("global_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
 
 __device__ __forceinline__ int mx_swz(int row) { return (row >> 2) & 3; }

@@ -78,18 +78,23 @@ __device__ __forceinline__ int col_swizzle(int crow) { return (crow & 3) | ((cro
 
 // Direct global->LDS loads to a wave-uniform LDS byte address (lane l writes [16l, 16l+16), or [4l, 4l+4) from
 // it); the second takes a uniform base and a 32-bit offset a lane, the third the same for bytes that no other workgroup
-// reads (nontemporal).
+// reads (nontemporal).  The compiler adds no wait states inside assembly, and two are the program's to keep: one
+// after a scalar write of m0, and five after a vector instruction's write of the scalar base (v_readfirstlane, or
+// v_readlane of a spilled register; without them the load has taken an address of old and new halves).  A scalar
+// copy of the base waits for such a write by itself, and is the one state that m0 needs.
 __device__ __forceinline__ void g2lds16_at(const void* g, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void g2lds16_at(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds) : "memory");
+  const void* copy;
+  asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0" : "=&s"(copy) : "v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void g2lds16_once_at(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1 nt" : : "v"(off), "s"(base), "{m0}"(lds) : "memory");
+  const void* copy;
+  asm volatile("s_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0 nt" : "=&s"(copy) : "v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void g2lds4_at(const void* g, uint32_t lds) {
-  asm volatile("global_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
