@@ -1,8 +1,10 @@
 """ctypes binding of libmoe_w4a16.so: argument marshalling only.
 
 Each function has the name of the C entry point it calls, takes torch tensors on the GPU, passes
-their data pointers and the current HIP stream, and raises ``MoEError`` on a negative status.  Every
-step of the layer runs in the HIP kernels of the library; there is no fallback of any kind: if the
+their data pointers and the current HIP stream, and raises ``MoEError`` on a negative status.  With
+``stream=`` the call runs on that stream, to which the tensors made for it belong; the caller
+sees to it that the tensors given are ready there, and keeps them until it is done.  Every step
+of the layer runs in the HIP kernels of the library; there is no fallback of any kind: if the
 library is not built, loading fails with an error that says how to build it.
 """
 from __future__ import annotations
@@ -155,6 +157,19 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, dev, stream=None, keep=True):
+    """Memory that a wrapper makes for its call belongs to the stream of the call: a block that the current stream's
+    allocator gives may still be in use by work queued there, which another stream does not wait for.  keep: the caller
+    gets the tensor, and may use and free it on the current stream too (once that waits for the given one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if keep:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def _req(t, dtype, name):
     ok = t.element_size() == 2 if dtype == "16bit" else t.dtype == dtype
     if not ok or not t.is_cuda or not t.is_contiguous():
@@ -185,9 +200,9 @@ def moe_route_topk(logits: torch.Tensor, k: int, topk_ids=None, topk_w=None, str
     _req(logits, torch.float32, "logits")
     T, E = logits.shape
     if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        topk_ids = _empty((T, k), torch.int32, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        topk_w = _empty((T, k), torch.float32, logits.device, stream)
     _check(load().moe_route_topk(_p(logits), T, E, k, _p(topk_ids), _p(topk_w), _stream(stream)))
     return topk_ids, topk_w
 
@@ -203,15 +218,15 @@ def moe_align(topk_ids: torch.Tensor, E: int, block_m: int, stream=None, max_til
     if max_tiles is None:
         max_tiles = moe_max_tiles(T, k, E, block_m)
     out = dict(
-        counts=torch.empty(E, dtype=torch.int32, device=dev),
-        offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-        sorted_ids=torch.empty(max(R, 1), dtype=torch.int32, device=dev),
-        inv_perm=torch.empty(max(R, 1), dtype=torch.int32, device=dev),
-        tiles=torch.empty((max(max_tiles, 1), 3), dtype=torch.int32, device=dev),
-        num_tiles=torch.empty(1, dtype=torch.int32, device=dev),
+        counts=_empty(E, torch.int32, dev, stream),
+        offsets=_empty(E + 1, torch.int32, dev, stream),
+        sorted_ids=_empty(max(R, 1), torch.int32, dev, stream),
+        inv_perm=_empty(max(R, 1), torch.int32, dev, stream),
+        tiles=_empty((max(max_tiles, 1), 3), torch.int32, dev, stream),
+        num_tiles=_empty(1, torch.int32, dev, stream),
     )
     wsb = moe_align_workspace_bytes(T, k, E)
-    ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev) if wsb else None
+    ws = _empty(max(wsb, 16), torch.uint8, dev, stream, keep=False) if wsb else None
     _check(load().moe_align(_p(topk_ids), T, k, E, block_m, _p(out["counts"]), _p(out["offsets"]),
                             _p(out["sorted_ids"]), _p(out["inv_perm"]), _p(out["tiles"]), max_tiles,
                             _p(out["num_tiles"]), _p(ws), wsb, _stream(stream)))
@@ -227,9 +242,9 @@ def moe_w4_prepack(w_q, w_s, packed_q=None, packed_s=None, stream=None):
     _req(w_s, "16bit", "w_s")
     E, N, K2 = w_q.shape
     if packed_q is None:
-        packed_q = torch.empty_like(w_q)
+        packed_q = _empty(w_q.shape, w_q.dtype, w_q.device, stream)
     if packed_s is None:
-        packed_s = torch.empty_like(w_s)
+        packed_s = _empty(w_s.shape, w_s.dtype, w_s.device, stream)
     _check(load().moe_w4_prepack(_p(w_q), _p(w_s), E, N, 2 * K2, _p(packed_q), _p(packed_s), _stream(stream)))
     return packed_q, packed_s
 
@@ -246,9 +261,9 @@ def moe_grouped_gemm_w4a16(A, a_row_of, a_row_div: int, Wq, Ws, tiles, max_tiles
     ncols = N // 2 if epilogue == MOE_EPI_SILU_MUL else N
     if C is None:
         dt = {MOE_OUT_F32: torch.float32, MOE_OUT_F16E: torch.float16}.get(out_dtype, torch.bfloat16)
-        C = torch.empty((out_rows, ncols), dtype=dt, device=A.device)
+        C = _empty((out_rows, ncols), dt, A.device, stream)
     if out_dtype == MOE_OUT_F16E and C_side is None:
-        C_side = torch.empty((out_rows, (ncols + 7) // 8), dtype=torch.float32, device=A.device)
+        C_side = _empty((out_rows, (ncols + 7) // 8), torch.float32, A.device, stream)
     _check(load().moe_grouped_gemm_w4a16(_p(A), _p(a_row_of), a_row_div, _p(Wq), _p(Ws), weight_layout, E, N, K,
                                          _p(tiles),
                                          max_tiles, _p(num_tiles), block_m, epilogue, _p(C), out_dtype, _p(C_side),
@@ -261,9 +276,9 @@ def moe_x_to_f16(x, x16=None, x_exp=None, stream=None):
     _req(x, "16bit", "x")
     T, H = x.shape
     if x16 is None:
-        x16 = torch.empty((T, H), dtype=torch.float16, device=x.device)
+        x16 = _empty((T, H), torch.float16, x.device, stream)
     if x_exp is None:
-        x_exp = torch.empty((T,), dtype=torch.int32, device=x.device)
+        x_exp = _empty((T,), torch.int32, x.device, stream)
     _check(load().moe_x_to_f16(_p(x), T, H, _p(x16), _p(x_exp), _stream(stream)))
     return x16, x_exp
 
@@ -280,15 +295,14 @@ def moe_grouped_gemm_w4f16(A, a_row_exp, a_exps, a_row_of, a_row_div: int, Wq, W
     K = 2 * K2
     ncols = N // 2 if epilogue == MOE_EPI_SILU_MUL else N
     if C is None:
-        C = torch.empty((out_rows, ncols), dtype=torch.float32 if out_dtype == MOE_OUT_F32 else torch.float16,
-                        device=A.device)
+        C = _empty((out_rows, ncols), torch.float32 if out_dtype == MOE_OUT_F32 else torch.float16, A.device, stream)
     if out_dtype == MOE_OUT_H16:
         if C_aux is None:
-            C_aux = torch.empty((max(max_tiles, 1), (ncols + 31) // 32), dtype=torch.uint8, device=A.device)
+            C_aux = _empty((max(max_tiles, 1), (ncols + 31) // 32), torch.uint8, A.device, stream)
         if C_aux2 is None:
-            C_aux2 = torch.empty((out_rows, (ncols + 31) // 32), dtype=torch.uint8, device=A.device)
+            C_aux2 = _empty((out_rows, (ncols + 31) // 32), torch.uint8, A.device, stream)
     elif C_aux is None and out_dtype == MOE_OUT_F16E:
-        C_aux = torch.empty((out_rows, (ncols + 7) // 8), dtype=torch.float32, device=A.device)
+        C_aux = _empty((out_rows, (ncols + 7) // 8), torch.float32, A.device, stream)
     bf, be = (None, None) if a_exps is None else a_exps
     _check(load().moe_grouped_gemm_w4f16(_p(A), _p(a_row_exp), _p(bf), _p(be), _p(a_row_of), a_row_div, _p(Wq), _p(Ws),
                                          weight_layout, E, N, K, _p(tiles), max_tiles, _p(num_tiles), block_m, epilogue,
@@ -314,7 +328,7 @@ def moe_combine(O, inv_perm, topk_w, y=None, stream=None, shared=None, O_side=No
     T, k = topk_w.shape
     H = O.shape[1]
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=O.device)
+        y = _empty((T, H), torch.bfloat16, O.device, stream)
     _check(load().moe_combine(_p(O), o_dtype, _p(O_side) if o_dtype == MOE_OUT_F16E else None, _p(inv_perm),
                               _p(topk_w), _p(shared), T, k, H, _p(y), _stream(stream)))
     return y
@@ -327,7 +341,7 @@ def moe_router_logits(x, w_router, logits=None, stream=None):
     T, H = x.shape
     E = w_router.shape[0]
     if logits is None:
-        logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+        logits = _empty((T, E), torch.float32, x.device, stream)
     _check(load().moe_router_logits(_p(x), _p(w_router), T, H, E, _p(logits), _stream(stream)))
     return logits
 
@@ -343,10 +357,10 @@ def moe_dense_ffn_w4a16(x, w13_q, w13_s, w2_q, w2_s, out=None, workspace=None, s
     T, H = x.shape
     I = w13_q.shape[-2] // 2
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _empty((T, H), torch.float32, x.device, stream)
     wsb = moe_dense_ffn_workspace_bytes(T, H, I)
     if workspace is None:
-        workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(wsb, 256), torch.uint8, x.device, stream, keep=False)
     _check(load().moe_dense_ffn_w4a16(_p(x), T, H, I, _p(w13_q), _p(w13_s), _p(w2_q), _p(w2_s), weight_layout,
                                       _p(out), _p(workspace), workspace.numel() * workspace.element_size(),
                                       _stream(stream)))
@@ -371,10 +385,10 @@ def moe_ffn_block_forward(x, w_router, w13_q, w13_s, w2_q, w2_s, k: int, shared=
     else:
         Is, sh = shared[0].shape[-2] // 2, shared
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = _empty((T, H), torch.bfloat16, x.device, stream)
     wsb = moe_ffn_block_workspace_bytes(T, H, I, E, k, Is)
     if workspace is None:
-        workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(wsb, 256), torch.uint8, x.device, stream, keep=False)
     _check(load().moe_ffn_block_forward(_p(x), _p(w_router), T, H, I, E, k, _p(w13_q), _p(w13_s), _p(w2_q),
                                         _p(w2_s), Is, *(_p(t) for t in sh), weight_layout, _p(y), _p(logits_out),
                                         _p(topk_ids_out), _p(topk_w_out), _p(workspace),
@@ -389,10 +403,10 @@ def moe_ffn_forward(x, router_logits, w13_q, w13_s, w2_q, w2_s, k: int, y=None, 
     E, N13, _ = w13_q.shape
     I = N13 // 2
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = _empty((T, H), torch.bfloat16, x.device, stream)
     wsb = moe_ffn_workspace_bytes(T, H, I, E, k)
     if workspace is None:
-        workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(wsb, 256), torch.uint8, x.device, stream, keep=False)
     _check(load().moe_ffn_forward(_p(x), _p(router_logits), T, H, I, E, k, _p(w13_q), _p(w13_s), _p(w2_q),
                                   _p(w2_s), weight_layout, _p(y), _p(topk_ids_out), _p(topk_w_out), _p(workspace),
                                   workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -411,7 +425,7 @@ def moe_ffn_forward_noalloc(x, router_logits, w13_q, w13_s, w2_q, w2_s, k: int, 
     E, N13, _ = w13_q.shape
     I = N13 // 2
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = _empty((T, H), torch.bfloat16, x.device, stream)
     _check(load().moe_ffn_forward_noalloc(_p(x), _p(router_logits), T, H, I, E, k, _p(w13_q), _p(w13_s), _p(w2_q),
                                           _p(w2_s), weight_layout, _p(y), _p(topk_ids_out), _p(topk_w_out),
                                           _stream(stream)))
@@ -425,9 +439,9 @@ def moe_mx_quantize(x, q=None, s=None, stream=None):
     _req(x, "16bit", "x")
     rows, K = x.shape
     if q is None:
-        q = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+        q = _empty((rows, K // 2), torch.uint8, x.device, stream)
     if s is None:
-        s = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+        s = _empty((rows, K // 32), torch.uint8, x.device, stream)
     _check(load().moe_mx_quantize(_p(x), rows, K, _p(q), _p(s), _stream(stream)))
     return q, s
 
@@ -439,9 +453,9 @@ def moe_mx_prepack(w_q, w_e, packed_q=None, packed_e=None, stream=None):
     _req(w_e, torch.uint8, "w_e")
     E, N, K2 = w_q.shape
     if packed_q is None:
-        packed_q = torch.empty_like(w_q)
+        packed_q = _empty(w_q.shape, w_q.dtype, w_q.device, stream)
     if packed_e is None:
-        packed_e = torch.empty_like(w_e)
+        packed_e = _empty(w_e.shape, w_e.dtype, w_e.device, stream)
     _check(load().moe_mx_prepack(_p(w_q), _p(w_e), E, N, 2 * K2, _p(packed_q), _p(packed_e), _stream(stream)))
     return packed_q, packed_e
 
@@ -454,9 +468,9 @@ def moe_mx_quantize_tiles(x, a_row_of, a_row_div: int, tiles, max_tiles: int, nu
     T, K = x.shape
     rows = max(max_tiles, 1) * block_m
     if q is None:
-        q = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+        q = _empty((rows, K // 2), torch.uint8, x.device, stream)
     if s is None:
-        s = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+        s = _empty((rows, K // 32), torch.uint8, x.device, stream)
     if q.numel() < rows * (K // 2) or s.numel() < rows * (K // 32):
         raise ValueError(f"tile-blocked activations need {rows} rows (max_tiles * block_m)")
     _check(load().moe_mx_quantize_tiles(_p(x), T, K, _p(a_row_of), a_row_div, _p(tiles), max_tiles, _p(num_tiles),
@@ -480,11 +494,11 @@ def moe_grouped_gemm_mxfp4(Aq, As, a_row_of, a_row_div: int, Wq, We, tiles, max_
         out_rows = max(out_rows, max(max_tiles, 1) * block_m)  # h is written tile-blocked
     if epilogue == MOE_EPI_SILU_MUL:
         if C is None:
-            C = torch.empty((out_rows, N // 4), dtype=torch.uint8, device=dev)
+            C = _empty((out_rows, N // 4), torch.uint8, dev, stream)
         if Cs is None:
-            Cs = torch.empty((out_rows, N // 64), dtype=torch.uint8, device=dev)
+            Cs = _empty((out_rows, N // 64), torch.uint8, dev, stream)
     elif C is None:
-        C = torch.empty((out_rows, N), dtype=torch.float32 if out_dtype == MOE_OUT_F32 else torch.bfloat16, device=dev)
+        C = _empty((out_rows, N), torch.float32 if out_dtype == MOE_OUT_F32 else torch.bfloat16, dev, stream)
     if act_layout == MOE_ACT_TILED and epilogue == MOE_EPI_SILU_MUL:
         need = max(max_tiles, 1) * block_m
         if C.shape[0] < need or Cs.shape[0] < need:
@@ -512,10 +526,10 @@ def moe_ffn_forward_mxfp4(x, router_logits, w13_q, w13_e, w2_q, w2_e, k: int, y=
     E, N13, _ = w13_q.shape
     I = N13 // 2
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = _empty((T, H), torch.bfloat16, x.device, stream)
     wsb = moe_ffn_mxfp4_workspace_bytes(T, H, I, E, k)
     if workspace is None:
-        workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(wsb, 256), torch.uint8, x.device, stream, keep=False)
     _check(load().moe_ffn_forward_mxfp4(_p(x), _p(router_logits), T, H, I, E, k, _p(w13_q), _p(w13_e), _p(w2_q),
                                         _p(w2_e), weight_layout, _p(y), _p(topk_ids_out), _p(topk_w_out), _p(workspace),
                                         workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -529,9 +543,9 @@ def moe_mx8_quantize(x, q=None, s=None, stream=None):
     _req(x, "16bit", "x")
     rows, K = x.shape
     if q is None:
-        q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+        q = _empty((rows, K), torch.uint8, x.device, stream)
     if s is None:
-        s = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+        s = _empty((rows, K // 32), torch.uint8, x.device, stream)
     _check(load().moe_mx8_quantize(_p(x), rows, K, _p(q), _p(s), _stream(stream)))
     return q, s
 
@@ -543,9 +557,9 @@ def moe_mx8_quantize_tiles(x, a_row_of, a_row_div: int, tiles, max_tiles: int, n
     T, K = x.shape
     rows = max(max_tiles, 1) * block_m
     if q is None:
-        q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+        q = _empty((rows, K), torch.uint8, x.device, stream)
     if s is None:
-        s = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+        s = _empty((rows, K // 32), torch.uint8, x.device, stream)
     _check(load().moe_mx8_quantize_tiles(_p(x), T, K, _p(a_row_of), a_row_div, _p(tiles), max_tiles, _p(num_tiles),
                                          block_m, _p(q), _p(s), _stream(stream)))
     return q, s
@@ -567,11 +581,11 @@ def moe_grouped_gemm_w4a8(Aq, As, a_row_of, a_row_div: int, Wq, We, tiles, max_t
         out_rows = max(out_rows, max(max_tiles, 1) * block_m)  # h is written tile-blocked
     if epilogue == MOE_EPI_SILU_MUL:
         if C is None:
-            C = torch.empty((out_rows, N // 2), dtype=torch.uint8, device=dev)
+            C = _empty((out_rows, N // 2), torch.uint8, dev, stream)
         if Cs is None:
-            Cs = torch.empty((out_rows, N // 64), dtype=torch.uint8, device=dev)
+            Cs = _empty((out_rows, N // 64), torch.uint8, dev, stream)
     elif C is None:
-        C = torch.empty((out_rows, N), dtype=torch.float32 if out_dtype == MOE_OUT_F32 else torch.bfloat16, device=dev)
+        C = _empty((out_rows, N), torch.float32 if out_dtype == MOE_OUT_F32 else torch.bfloat16, dev, stream)
     _check(load().moe_grouped_gemm_w4a8(_p(Aq), _p(As), _p(a_row_of), a_row_div, _p(Wq), _p(We), weight_layout,
                                         act_layout, E, N, K, _p(tiles), max_tiles, _p(num_tiles), block_m, epilogue,
                                         _p(C), _p(Cs), out_dtype, _stream(stream)))
@@ -594,10 +608,10 @@ def moe_ffn_forward_w4a8(x, router_logits, w13_q, w13_e, w2_q, w2_e, k: int, y=N
     E, N13, _ = w13_q.shape
     I = N13 // 2
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = _empty((T, H), torch.bfloat16, x.device, stream)
     wsb = moe_ffn_w4a8_workspace_bytes(T, H, I, E, k)
     if workspace is None:
-        workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(wsb, 256), torch.uint8, x.device, stream, keep=False)
     _check(load().moe_ffn_forward_w4a8(_p(x), _p(router_logits), T, H, I, E, k, _p(w13_q), _p(w13_e), _p(w2_q),
                                        _p(w2_e), weight_layout, _p(y), _p(topk_ids_out), _p(topk_w_out), _p(workspace),
                                        workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -617,9 +631,9 @@ def moe_f8_quantize(x, q=None, s=None, stream=None):
         raise ValueError("x must be a contiguous CUDA tensor")
     rows, K = x.shape
     if q is None:
-        q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+        q = _empty((rows, K), torch.uint8, x.device, stream)
     if s is None:
-        s = torch.empty((rows, K // 128), dtype=torch.float32, device=x.device)
+        s = _empty((rows, K // 128), torch.float32, x.device, stream)
     _check(load().moe_f8_quantize(_p(x), in_dtype, rows, K, _p(q), _p(s), _stream(stream)))
     return q, s
 
@@ -634,13 +648,13 @@ def moe_grouped_gemm_f8(Aq, As, a_row_of, a_row_div: int, Wq, Ws, tiles, max_til
     E, N, K = Wq.shape
     if out_dtype == MOE_OUT_F8:
         if C is None:
-            C = torch.empty((out_rows, N // 2), dtype=torch.uint8, device=Aq.device)
+            C = _empty((out_rows, N // 2), torch.uint8, Aq.device, stream)
         if Cs is None:
-            Cs = torch.empty((out_rows, max(N // 256, 1)), dtype=torch.float32, device=Aq.device)
+            Cs = _empty((out_rows, max(N // 256, 1)), torch.float32, Aq.device, stream)
     elif C is None:
         cols = N // 2 if epilogue == MOE_EPI_SILU_MUL else N
         dt = torch.float32 if out_dtype == MOE_OUT_F32 else torch.bfloat16
-        C = torch.empty((out_rows, cols), dtype=dt, device=Aq.device)
+        C = _empty((out_rows, cols), dt, Aq.device, stream)
     _check(load().moe_grouped_gemm_f8(_p(Aq), _p(As), _p(a_row_of), a_row_div, _p(Wq), _p(Ws), E, N, K, _p(tiles),
                                       max_tiles, _p(num_tiles), block_m, epilogue, _p(C), _p(Cs), out_dtype,
                                       _stream(stream)))
@@ -664,10 +678,10 @@ def moe_ffn_forward_f8(x, router_logits, w13_q, w13_s, w2_q, w2_s, k: int, y=Non
     E, N13, _ = w13_q.shape
     I = N13 // 2
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        y = _empty((T, H), torch.bfloat16, x.device, stream)
     wsb = moe_ffn_f8_workspace_bytes(T, H, I, E, k)
     if workspace is None:
-        workspace = torch.empty(max(wsb, 256), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(wsb, 256), torch.uint8, x.device, stream, keep=False)
     _check(load().moe_ffn_forward_f8(_p(x), _p(router_logits), T, H, I, E, k, _p(w13_q), _p(w13_s), _p(w2_q),
                                      _p(w2_s), _p(y), _p(topk_ids_out), _p(topk_w_out), _p(workspace),
                                      workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -700,8 +714,8 @@ def _need(t, dtypes, shape, name, dev=None):
 
 
 def _call(fn, dev, stream, made, *args):
-    """Calls a C entry point on the tensors' device and stream.  Tensors made by the wrapper (outputs,
-    workspaces) belong to the current stream: their memory is kept until another given stream is done."""
+    """Calls a C entry point on the tensors' device and stream.  made: the call's outputs and workspaces, whose memory
+    is kept until a given stream is done (those that the caller gave may belong to another one)."""
     index = dev.index
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)
@@ -725,13 +739,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(made, shape, out_dtype, dev, name):
+def _out(made, shape, out_dtype, dev, name, stream):
     """The caller's output, checked, or a new one of out_dtype; a call's out_dtype defaults to bf16."""
     dt = _OUT_DTYPE.get(out_dtype)
     if dt is None:
         raise ValueError(f"unknown out_dtype {out_dtype}")
     if made is None:
-        return torch.empty(shape, dtype=dt, device=dev)
+        return _empty(shape, dt, dev, stream)
     _need(made, (dt,), shape, name, dev)
     return made
 
@@ -759,11 +773,11 @@ def moe_i8_quantize(x, q=None, s=None, stream=None):
     rows, K = _need(x, _ACT, (None, None), "x")
     dev = x.device
     if q is None:
-        q = torch.empty((rows, K), dtype=torch.int8, device=dev)
+        q = _empty((rows, K), torch.int8, dev, stream)
     else:
         _need(q, _I8, (rows, K), "q", dev)
     if s is None:
-        s = torch.empty((rows,), dtype=torch.float32, device=dev)
+        s = _empty((rows,), torch.float32, dev, stream)
     else:
         _need(s, _F32, (rows,), "s", dev)
     _call(load().moe_i8_quantize, dev, stream, (q, s), x.data_ptr(), _IN[x.dtype], rows, K, q.data_ptr(), s.data_ptr())
@@ -777,7 +791,7 @@ def moe_gemm_i8(Aq, As, Wq, Ws, epilogue: int = MOE_EPI_NONE, out_dtype: int = M
     _need(As, _F32, (M,), "As", dev)
     N, _ = _need(Wq, _I8, (None, K), "Wq", dev)
     _need(Ws, _F32, (N,), "Ws", dev)
-    C = _out(C, (M, _cols(N, epilogue)), out_dtype, dev, "C")
+    C = _out(C, (M, _cols(N, epilogue)), out_dtype, dev, "C", stream)
     _call(load().moe_gemm_i8, dev, stream, (C,), Aq.data_ptr(), As.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), M, N, K,
           epilogue, C.data_ptr(), out_dtype)
     return C
@@ -795,14 +809,14 @@ def moe_linear_i8(x, Wq, Ws, epilogue: int = MOE_EPI_NONE, out_dtype: int = MOE_
     dev = x.device
     N, _ = _need(Wq, _I8, (None, K), "Wq", dev)
     _need(Ws, _F32, (N,), "Ws", dev)
-    y = _out(y, (T, _cols(N, epilogue)), out_dtype, dev, "y")
+    y = _out(y, (T, _cols(N, epilogue)), out_dtype, dev, "y", stream)
     lib, size = load(), 0
     if workspace is not None:
         size, = _need(workspace, _U8, (None,), "workspace", dev)
     else:
         size = lib.moe_linear_i8_workspace_bytes(T, K)
         if size:
-            workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
+            workspace = _empty((size,), torch.uint8, dev, stream, keep=False)
     _call(lib.moe_linear_i8, dev, stream, (y, workspace), x.data_ptr(), _IN[x.dtype], Wq.data_ptr(), Ws.data_ptr(), T, N, K,
           epilogue, y.data_ptr(), out_dtype, _ptr(workspace), size)
     return y
@@ -818,7 +832,7 @@ def moe_grouped_gemm_i8(Aq, As, a_row_of, a_row_div: int, Wq, Ws, expert_offsets
     E, N, _ = _need(Wq, _I8, (None, None, K), "Wq", dev)
     _need(Ws, _F32, (E, N), "Ws", dev)
     _groups(Aq, out_rows, a_row_of, a_row_div, expert_offsets, E, dev)
-    C = _out(C, (out_rows, _cols(N, epilogue)), out_dtype, dev, "C")
+    C = _out(C, (out_rows, _cols(N, epilogue)), out_dtype, dev, "C", stream)
     _call(load().moe_grouped_gemm_i8, dev, stream, (C,), Aq.data_ptr(), As.data_ptr(), _ptr(a_row_of), a_row_div,
           Wq.data_ptr(), Ws.data_ptr(), expert_offsets.data_ptr(), out_rows, E, N, K, epilogue, C.data_ptr(), out_dtype)
     return C
@@ -834,7 +848,7 @@ def _halves(N13, name):
     return N13 // 2
 
 
-def _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace, need_bytes):
+def _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace, need_bytes, stream):
     """Checks a layer's activations and optional buffers, makes y and the workspace where none is given."""
     dev, T = x.device, x.shape[0]
     _need(router_logits, _F32, (T, E), "router_logits", dev)
@@ -842,9 +856,9 @@ def _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
         _need(topk_ids_out, _INT32, (T, k), "topk_ids_out", dev)
     if topk_w_out is not None:
         _need(topk_w_out, _F32, (T, k), "topk_w_out", dev)
-    y = _out(y, (T, H), MOE_OUT_BF16, dev, "y")
+    y = _out(y, (T, H), MOE_OUT_BF16, dev, "y", stream)
     if workspace is None:
-        workspace = torch.empty(max(need_bytes, 256), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(need_bytes, 256), torch.uint8, dev, stream, keep=False)
     else:
         _need(workspace, _U8, (None,), "workspace", dev)
     return y, workspace
@@ -862,7 +876,7 @@ def moe_ffn_forward_i8(x, router_logits, w13_q, w13_s, w2_q, w2_s, k: int, y=Non
     _need(w2_q, _I8, (E, H, I), "w2_q", dev)
     _need(w2_s, _F32, (E, H), "w2_s", dev)
     y, workspace = _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
-                             moe_ffn_i8_workspace_bytes(T, H, I, E, k))
+                             moe_ffn_i8_workspace_bytes(T, H, I, E, k), stream)
     _call(load().moe_ffn_forward_i8, dev, stream, (y, workspace), x.data_ptr(), router_logits.data_ptr(), T, H, I, E, k,
           w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(), y.data_ptr(), _ptr(topk_ids_out),
           _ptr(topk_w_out), workspace.data_ptr(), workspace.numel())
@@ -878,7 +892,7 @@ def moe_grouped_gemm_w16(A, a_row_of, a_row_div: int, W, expert_offsets, out_row
     E, N, _ = _need(W, (dt,), (None, None, K), "W", dev)
     _groups(A, out_rows, a_row_of, a_row_div, expert_offsets, E, dev)
     out_dtype = _OUT[dt] if out_dtype is None else out_dtype
-    C = _out(C, (out_rows, _cols(N, epilogue)), out_dtype, dev, "C")
+    C = _out(C, (out_rows, _cols(N, epilogue)), out_dtype, dev, "C", stream)
     _call(load().moe_grouped_gemm_w16, dev, stream, (C,), A.data_ptr(), _ptr(a_row_of), a_row_div, W.data_ptr(), _IN[dt],
           expert_offsets.data_ptr(), out_rows, E, N, K, epilogue, C.data_ptr(), out_dtype)
     return C
@@ -892,7 +906,7 @@ def moe_grouped_gemm_w16_dx(dC, W, expert_offsets, out_dtype: int = None, dA=Non
     E, _, K = _need(W, (dt,), (None, N, None), "W", dev)
     _need(expert_offsets, _INT32, (E + 1,), "expert_offsets", dev)
     out_dtype = _OUT[dt] if out_dtype is None else out_dtype
-    dA = _out(dA, (R, K), out_dtype, dev, "dA")
+    dA = _out(dA, (R, K), out_dtype, dev, "dA", stream)
     _call(load().moe_grouped_gemm_w16_dx, dev, stream, (dA,), dC.data_ptr(), W.data_ptr(), _IN[dt],
           expert_offsets.data_ptr(), R, E, N, K, dA.data_ptr(), out_dtype)
     return dA
@@ -914,14 +928,14 @@ def moe_grouped_gemm_w16_dw(dC, A, a_row_of, a_row_div: int, expert_offsets, out
     E = expert_offsets.shape[0] - 1
     _groups(A, R, a_row_of, a_row_div, expert_offsets, E, dev)
     out_dtype = _OUT[dt] if out_dtype is None else out_dtype
-    dW = _out(dW, (E, N, K), out_dtype, dev, "dW")
+    dW = _out(dW, (E, N, K), out_dtype, dev, "dW", stream)
     lib, size = load(), 0
     if workspace is not None:
         size, = _need(workspace, _U8, (None,), "workspace", dev)
     else:
         size = lib.moe_grouped_gemm_w16_dw_workspace_bytes(R, E, N, K)
         if size:
-            workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
+            workspace = _empty((size,), torch.uint8, dev, stream, keep=False)
     _call(lib.moe_grouped_gemm_w16_dw, dev, stream, (dW, workspace), dC.data_ptr(), A.data_ptr(), _ptr(a_row_of), a_row_div,
           _IN[dt], expert_offsets.data_ptr(), R, E, N, K, dW.data_ptr(), out_dtype, _ptr(workspace), size)
     return dW
@@ -937,7 +951,7 @@ def _silu_shape(G):
 def moe_silu_mul(G, h=None, stream=None):
     """G [R, 2I] (gate, up) bf16 or fp16 -> h = silu(gate) * up [R, I] of its type."""
     R, I = _silu_shape(G)
-    h = _out(h, (R, I), _OUT[G.dtype], G.device, "h")
+    h = _out(h, (R, I), _OUT[G.dtype], G.device, "h", stream)
     _call(load().moe_silu_mul, G.device, stream, (h,), G.data_ptr(), _IN[G.dtype], R, I, h.data_ptr())
     return h
 
@@ -946,7 +960,7 @@ def moe_silu_mul_grad(G, dh, dG=None, stream=None):
     """Gradient of moe_silu_mul: G [R, 2I], dh [R, I] -> dG [R, 2I]."""
     R, I = _silu_shape(G)
     _need(dh, (G.dtype,), (R, I), "dh", G.device)
-    dG = _out(dG, (R, 2 * I), _OUT[G.dtype], G.device, "dG")
+    dG = _out(dG, (R, 2 * I), _OUT[G.dtype], G.device, "dG", stream)
     _call(load().moe_silu_mul_grad, G.device, stream, (dG,), G.data_ptr(), dh.data_ptr(), _IN[G.dtype], R, I, dG.data_ptr())
     return dG
 
@@ -966,7 +980,7 @@ def moe_ffn_forward_w16(x, router_logits, w13, w2, k: int, y=None, topk_ids_out=
     I = _halves(N13, "w13")
     _need(w2, bf16, (E, H, I), "w2", dev)
     y, workspace = _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
-                             moe_ffn_w16_workspace_bytes(T, H, I, E, k))
+                             moe_ffn_w16_workspace_bytes(T, H, I, E, k), stream)
     _call(load().moe_ffn_forward_w16, dev, stream, (y, workspace), x.data_ptr(), router_logits.data_ptr(), T, H, I, E, k,
           w13.data_ptr(), w2.data_ptr(), y.data_ptr(), _ptr(topk_ids_out), _ptr(topk_w_out), workspace.data_ptr(),
           workspace.numel())
