@@ -1613,7 +1613,9 @@ moe_status_t moe_grouped_gemm_w16_dx(const uint16_t* dC, const uint16_t* W, int3
 }
 
 size_t moe_grouped_gemm_w16_dw_workspace_bytes(int32_t R, int32_t E, int32_t N, int32_t K) {
-  if (R < 0 || E < 1 || N < 1 || K < 1 || E > MOE_MAX_EXPERTS || N > MOE_RAGGED_MAX_DIM || K > MOE_RAGGED_MAX_DIM) return 0;
+  if (R < 0 || E < 1 || N < 1 || K < 1 || E > MOE_MAX_EXPERTS || N > MOE_RAGGED_MAX_DIM || K > MOE_RAGGED_MAX_DIM ||
+      R >= kMaxRows || N % 8 != 0 || K % 8 != 0 || (int64_t)N * K * 2 > kMaxExpertCodeBytes)
+    return 0;
   const int split = moe::dw_split(R, E, N, K);
   return split > 1 ? (size_t)split * E * N * K * sizeof(float) : 0;
 }

@@ -109,3 +109,11 @@ def test_python_refuses_before_the_library():
                  lambda: moe.moe_silu_mul(x), lambda: moe.moe_ffn_forward_w16(x, x, w, w, 1)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_no_weight_gradient_workspace_for_refused_sizes():
+    """0 for every size that the call itself refuses."""
+    size = moe.moe_grouped_gemm_w16_dw_workspace_bytes
+    assert size(8192, 8, 64, 64) > 0
+    assert size(8192, 8, 60, 64) == size(8192, 8, 64, 60) == size(1 << 26, 8, 64, 64) == size(8192, 1025, 64, 64) == 0
+    assert size((1 << 26) - 1, 1, 1 << 20, 4096) == 0
