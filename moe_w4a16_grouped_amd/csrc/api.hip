@@ -557,6 +557,9 @@ bool ragged_ffn_dims_ok(int32_t H, int32_t I) {
   return H >= 16 && I >= 16 && H % 16 == 0 && I % 16 == 0 && H <= MOE_I8_MAX_K && I <= MOE_I8_MAX_K;
 }
 
+// One expert's gate_up weights (bytes an element) are addressed by 32-bit offsets.
+bool ragged_ffn_weights_ok(int32_t H, int32_t I, bool i8) { return (int64_t)2 * I * H * (i8 ? 1 : 2) <= kMaxExpertCodeBytes; }
+
 // The layer on int8 (w_s set) or bf16 weights: route and permute, gate_up with SiLU*mul, down, combine.
 moe_status_t run_ragged_ffn(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E,
                             int32_t k, const void* w13, const float* w13_s, const void* w2, const float* w2_s,
@@ -566,7 +569,7 @@ moe_status_t run_ragged_ffn(const uint16_t* x, const float* router_logits, int32
   if (!ragged_ffn_dims_ok(H, I))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H=%d and I=%d must be positive multiples of 16, <= %d", who, H, I,
                 MOE_I8_MAX_K);
-  if ((int64_t)2 * I * H * (i8 ? 1 : 2) > kMaxExpertCodeBytes)
+  if (!ragged_ffn_weights_ok(H, I, i8))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: one expert's gate_up weights must stay below 4 GiB", who);
   if (T == 0) return ok();
   if (!x || !router_logits || !w13 || !w2 || (i8 && (!w13_s || !w2_s)) || !y || !workspace)
@@ -1569,7 +1572,7 @@ moe_status_t moe_grouped_gemm_i8(const int8_t* Aq, const float* As, const int32_
 }
 
 size_t moe_ffn_i8_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k) {
-  if (T < 0 || !ragged_ffn_dims_ok(H, I) || E < 1 || k < 1 || k > E || E > MOE_MAX_EXPERTS || (int64_t)T * k >= kMaxRows)
+  if (T < 0 || !ragged_ffn_dims_ok(H, I) || !ragged_ffn_weights_ok(H, I, true) || E < 1 || k < 1 || k > E || E > MOE_MAX_EXPERTS || (int64_t)T * k >= kMaxRows)
     return 0;
   return ragged_ffn_layout(T, H, I, E, k, true).total;
 }
@@ -1666,7 +1669,7 @@ moe_status_t moe_silu_mul_grad(const uint16_t* G, const uint16_t* dh, int32_t dt
 }
 
 size_t moe_ffn_w16_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k) {
-  if (T < 0 || !ragged_ffn_dims_ok(H, I) || E < 1 || k < 1 || k > E || E > MOE_MAX_EXPERTS || (int64_t)T * k >= kMaxRows)
+  if (T < 0 || !ragged_ffn_dims_ok(H, I) || !ragged_ffn_weights_ok(H, I, false) || E < 1 || k < 1 || k > E || E > MOE_MAX_EXPERTS || (int64_t)T * k >= kMaxRows)
     return 0;
   return ragged_ffn_layout(T, H, I, E, k, false).total;
 }

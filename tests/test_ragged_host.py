@@ -117,3 +117,9 @@ def test_no_weight_gradient_workspace_for_refused_sizes():
     assert size(8192, 8, 64, 64) > 0
     assert size(8192, 8, 60, 64) == size(8192, 8, 64, 60) == size(1 << 26, 8, 64, 64) == size(8192, 1025, 64, 64) == 0
     assert size((1 << 26) - 1, 1, 1 << 20, 4096) == 0
+
+
+def test_no_layer_workspace_for_refused_sizes():
+    """0 where one expert's gate_up weights pass 4 GiB, which the layers refuse (int8 and 16-bit elements)."""
+    for size, I in ((moe.moe_ffn_i8_workspace_bytes, 1 << 15), (moe.moe_ffn_w16_workspace_bytes, 1 << 14)):
+        assert size(4, 1 << 16, I, 8, 2) == 0 and size(4, 1 << 16, I - 16, 8, 2) > 0
