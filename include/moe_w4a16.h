@@ -719,7 +719,8 @@ moe_status_t moe_grouped_gemm_w16_dw(const uint16_t* dC, const uint16_t* A, cons
  * SiLU*mul of a stored gate_up result G [R, 2I] (columns [0, I) the gate g, [I, 2I) the up projection u), for
  * training, where the backward pass needs G: h = silu(g) * u [R, I]; and its gradient: with s = 1 / (1 + exp(-g)),
  *   dG = [dh * u * s * (1 + g * (1 - s)), dh * g * s]  [R, 2I].
- * All of dtype MOE_IN_BF16 or MOE_IN_F16, arithmetic in fp32, one rounding.  An infinite g has no defined
+ * All of dtype MOE_IN_BF16 or MOE_IN_F16, arithmetic in fp32, one rounding; s below 2^-126 (g < -87) counts as 0.
+ * Finite operands give a finite result unless the result itself passes the type.  An infinite g has no defined
  * result.  dG may be G.  Shapes: 0 <= R < 2^26, I a positive multiple of 8 and <= MOE_RAGGED_MAX_DIM.
  * Alignment: 16 bytes.
  */
