@@ -319,6 +319,8 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   static_assert((!I8 || BN % 64 == 0) && (!B_T || BN >= 128) && (!A_T || BM >= 128), "scales are loaded by 64 columns, windows permuted by 8");
   static_assert(!I8 || MODE == kFwd, "transposing reads are of 16-bit elements");
   static_assert(BM <= NW * 64 && (RB == 64 || RB == 128), "rows");
+  // (issue_a, issue_b: a wave without a last load would not move its uniform base on)
+  static_assert((LA % NW == 0 || JA == 1) && (LB % NW == 0 || JB == 1), "every wave has all its loads, or at most one");
   static_assert(SA % 1024 == 0 && SB % 1024 == 0 && LMIN >= 1 && BEHIND < 64 && NA >= 2 && NB - NA <= 1 && NB >= NA && NW % 2 == 0, "loads");
 
   const int tid = threadIdx.x, lane = tid & 63;
