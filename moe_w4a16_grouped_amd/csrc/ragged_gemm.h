@@ -107,19 +107,17 @@ struct RowTile {
 
 __device__ __forceinline__ int group_end(const int32_t* off, int i, int R) { return min(max(off[i], 0), R); }
 
-// Row tiles of one group, in up to three heights H0 = 2 H1 = 4 H2 (H1, H2 zero: not there): whole tiles of H0,
-// and the rest in the smaller heights where they hold it, so that at most H2 - 1 padding rows (with one height
-// H0 - 1) are multiplied.
+// Row tiles of one group, in one height H0 or two, H0 = 2 H1 (H1 zero: not there): whole tiles of H0, and the rest in
+// the smaller height where that holds it, so that at most H1 - 1 padding rows (with one height H0 - 1) are multiplied.
 struct TileCount {
-  int n0, n1, n2;
+  int n0, n1;
 };
-template <int H0, int H1, int H2>
+template <int H0, int H1>
 __device__ __forceinline__ TileCount count_tiles(int rows) {
   const int rest = rows % H0;
-  TileCount c{rows / H0, 0, 0};
-  if (H1 == 0 || rest > H1 + H2) c.n0 += rest > 0;
-  else if (H2 == 0) c.n1 = rest > 0;
-  else { c.n1 = rest > H2; c.n2 = (rest > 0 && rest <= H2) || rest > H1; }
+  TileCount c{rows / H0, 0};
+  if (H1 == 0 || rest > H1) c.n0 += rest > 0;
+  else c.n1 = rest > 0;
   return c;
 }
 
@@ -191,7 +189,7 @@ __device__ __forceinline__ bool list_halved(int incl0, int n1, int nbn, long lon
 // lane (all their offsets in one round trip), counts their tiles, scans the counts over its lanes, and the lane
 // that holds the wanted tile finds its expert.  Offsets are clamped to [0, R], so no list of offsets leads out
 // of the rows.
-template <int H0, int H1, int H2, int PER>
+template <int H0, int H1, int PER>
 __device__ __forceinline__ bool find_row_tile_per(const int32_t* __restrict__ off, int E, int R, int nbn, RowTile& t, int& nb) {
   const int lane = threadIdx.x & 63;
   int end[PER + 1];  // offsets of this lane's experts; past the last expert the groups are empty
@@ -200,13 +198,12 @@ __device__ __forceinline__ bool find_row_tile_per(const int32_t* __restrict__ of
     const int e = min(lane * PER + i, E);
     end[i] = off ? group_end(off, e, R) : (e > 0 ? R : 0);  // without offsets one group holds all rows
   }
-  TileCount n{0, 0, 0};
+  TileCount n{0, 0};
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const TileCount c = count_tiles<H0, H1, H2>(max(end[i + 1] - end[i], 0));
+    const TileCount c = count_tiles<H0, H1>(max(end[i + 1] - end[i], 0));
     n.n0 += c.n0;
     n.n1 += c.n1;
-    n.n2 += c.n2;
   }
   long long j = linear_block() >> 3, item;
   int incl = wave_scan(n.n0, lane), mine = n.n0, cls = 0, half = 0;
@@ -215,21 +212,17 @@ __device__ __forceinline__ bool find_row_tile_per(const int32_t* __restrict__ of
   if (!halved && !list_place((long long)__builtin_amdgcn_readlane(incl, 63) * nbn, j, item)) {
     if (H1 == 0) return false;
     incl = wave_scan(n.n1, lane), mine = n.n1, cls = 1;
-    if (!list_place((long long)__builtin_amdgcn_readlane(incl, 63) * nbn, j, item)) {
-      if (H2 == 0) return false;
-      incl = wave_scan(n.n2, lane), mine = n.n2, cls = 2;
-      if (!list_place((long long)__builtin_amdgcn_readlane(incl, 63) * nbn, j, item)) return false;
-    }
+    if (!list_place((long long)__builtin_amdgcn_readlane(incl, 63) * nbn, j, item)) return false;
   }
   const int place = (int)(item / nbn);  // names the expert: its tiles x nbn items follow each other
   const int src = __builtin_ctzll(__ballot(incl > place));  // place < total: some lane's sum is past it
   // every lane walks its own experts; lane src's answer counts
-  int before = incl - mine, at_i = 0, at_before = before, at_nt = 0, r0 = 0, r1 = 0, full0 = 0, half0 = 0;
+  int before = incl - mine, at_i = 0, at_before = before, at_nt = 0, r0 = 0, r1 = 0, full0 = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const TileCount c = count_tiles<H0, H1, H2>(max(end[i + 1] - end[i], 0));
-    const int nt = cls == 0 ? c.n0 : (cls == 1 ? c.n1 : c.n2);
-    if (i == 0 || before <= place) at_i = i, at_before = before, at_nt = nt, r0 = end[i], r1 = end[i + 1], full0 = c.n0, half0 = c.n1;
+    const TileCount c = count_tiles<H0, H1>(max(end[i + 1] - end[i], 0));
+    const int nt = cls == 0 ? c.n0 : c.n1;
+    if (i == 0 || before <= place) at_i = i, at_before = before, at_nt = nt, r0 = end[i], r1 = end[i + 1], full0 = c.n0;
     before += nt;
   }
   at_i = __builtin_amdgcn_readlane(at_i, src);
@@ -243,10 +236,6 @@ __device__ __forceinline__ bool find_row_tile_per(const int32_t* __restrict__ of
   if (H1 > 0 && cls > 0) {
     first = __builtin_amdgcn_readlane(full0, src) * H0;
     high = H1;
-    if (H2 > 0 && cls == 2) {
-      first += __builtin_amdgcn_readlane(half0, src) * H1;
-      high = H2;
-    }
   }
   if (H1 > 0 && halved) {  // the upper or lower rows of a tile of the highest list
     first += half * H1;
@@ -257,13 +246,13 @@ __device__ __forceinline__ bool find_row_tile_per(const int32_t* __restrict__ of
   return true;
 }
 
-template <int H0, int H1, int H2>
+template <int H0, int H1>
 __device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ off, int E, int R, int nbn, RowTile& t, int& nb) {
-  if (E <= 64) return find_row_tile_per<H0, H1, H2, 1>(off, E, R, nbn, t, nb);
-  if (E <= 128) return find_row_tile_per<H0, H1, H2, 2>(off, E, R, nbn, t, nb);
-  if (E <= 256) return find_row_tile_per<H0, H1, H2, 4>(off, E, R, nbn, t, nb);
-  if (E <= 512) return find_row_tile_per<H0, H1, H2, 8>(off, E, R, nbn, t, nb);
-  return find_row_tile_per<H0, H1, H2, MOE_MAX_EXPERTS / 64>(off, E, R, nbn, t, nb);
+  if (E <= 64) return find_row_tile_per<H0, H1, 1>(off, E, R, nbn, t, nb);
+  if (E <= 128) return find_row_tile_per<H0, H1, 2>(off, E, R, nbn, t, nb);
+  if (E <= 256) return find_row_tile_per<H0, H1, 4>(off, E, R, nbn, t, nb);
+  if (E <= 512) return find_row_tile_per<H0, H1, 8>(off, E, R, nbn, t, nb);
+  return find_row_tile_per<H0, H1, MOE_MAX_EXPERTS / 64>(off, E, R, nbn, t, nb);
 }
 
 __device__ __forceinline__ void store4(void* C, int out, size_t at, const float (&v)[4]) {
@@ -727,13 +716,12 @@ __device__ __forceinline__ void ragged_tile(const RaggedArgs& p, const RowTile& 
   }
 }
 
-template <class T, int MODE, int EPI, class S0, class S1, class S2>
+template <class T, int MODE, int EPI, class S0, class S1>
 __global__ __launch_bounds__(S0::WM * S0::WN * 64) void ragged_gemm_kernel(RaggedArgs p) {
   constexpr int BM = S0::BM, BN = S0::BN;
-  constexpr int kLds = S0::kLds > S1::kLds ? (S0::kLds > S2::kLds ? S0::kLds : S2::kLds) : (S1::kLds > S2::kLds ? S1::kLds : S2::kLds);
+  constexpr int kLds = S0::kLds > S1::kLds ? S0::kLds : S1::kLds;
   constexpr bool I8 = T::kBytes == 1;
   static_assert(S1::BM == 0 || (S1::BN == BN && S1::WM * S1::WN == S0::WM * S0::WN), "one grid and workgroup size");
-  static_assert(S2::BM == 0 || (S2::BN == BN && S2::WM * S2::WN == S0::WM * S0::WN), "one grid and workgroup size");
   __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
   // the row indexes lie in what the last stage later takes, so that the stages may fill the LDS; int8 tiles keep
   // room for the scales where there is any
@@ -779,15 +767,11 @@ __global__ __launch_bounds__(S0::WM * S0::WN * 64) void ragged_gemm_kernel(Ragge
   } else {
     RowTile t;
     int nb;
-    if (!find_row_tile<BM, S1::BM, S2::BM>(p.offsets, p.E, p.R, nbn, t, nb)) return;
+    if (!find_row_tile<BM, S1::BM>(p.offsets, p.E, p.R, nbn, t, nb)) return;
     if (S1::BM == 0 || t.cls == 0) {
       ragged_tile<T, MODE, EPI, S0, kLate>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
     } else if constexpr (S1::BM > 0) {
-      if (S2::BM == 0 || t.cls == 1) {
-        ragged_tile<T, MODE, EPI, S1, kLate>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
-      } else if constexpr (S2::BM > 0) {
-        ragged_tile<T, MODE, EPI, S2, kLate>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
-      }
+      ragged_tile<T, MODE, EPI, S1, kLate>(p, t, nb, 0, smem, sRow, sScaleA, sScaleW);
     }
   }
 }
@@ -803,7 +787,7 @@ static inline bool fills(const RaggedArgs& a, int bm, int nd, int bc) {
 constexpr int kHalvesBytes = 4096;
 
 // Launch of one configuration.
-template <class T, int MODE, int EPI, class S0, class S1 = NoTile, class S2 = NoTile>
+template <class T, int MODE, int EPI, class S0, class S1 = NoTile>
 static hipError_t launch_ragged_cfg(const RaggedArgs& a, hipStream_t s) {
   constexpr int BM = S0::BM, BN = S0::BN;
   const int nd = MODE == kFwd ? (EPI == MOE_EPI_SILU_MUL ? a.N / 2 : a.N) : a.K;
@@ -816,12 +800,12 @@ static hipError_t launch_ragged_cfg(const RaggedArgs& a, hipStream_t s) {
   } else {
     // most row tiles that any groups of R rows give, and up to one more a list and XCD by the shares' rounding
     const long long m = a.offsets ? (a.E < a.R ? a.E : a.R) : 1;
-    const long long tiles = a.R / BM + (S2::BM > 0 ? 2 * m : m);
+    const long long tiles = a.R / BM + m;
     // and, where a tile's time is worth it, as many as a last round cut in halves takes
     const bool halves = S1::BM > 0 && BM >= kHalvedHeight && tiles * nbn <= 8 * 8 * kXcdCus && (MODE == kFwd ? a.K : a.N) * T::kBytes >= kHalvesBytes;
     grid = grid2d(8 * ((tiles * nbn + 7) / 8 + (halves ? 3 + kXcdCus : (S1::BM > 0 ? 3 : 0))));
   }
-  ragged_gemm_kernel<T, MODE, EPI, S0, S1, S2><<<grid, S0::WM * S0::WN * 64, 0, s>>>(a);
+  ragged_gemm_kernel<T, MODE, EPI, S0, S1><<<grid, S0::WM * S0::WN * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
