@@ -821,7 +821,10 @@ static hipError_t launch_ragged_cfg(const RaggedArgs& a, hipStream_t s) {
 //   mean 200: 256 x 256 against 64 x 128: fp16 0.53 against 0.47, int8 0.88 against 0.87;
 //   mean 400: fp16 0.79 against 0.60, int8 1.33 against 1.10.
 // A tile that would leave CUs idle gives way to a smaller one: one group of 77 rows, 1536 columns: 6.4 us with 16-row
-// tiles, 12.3 us with 64.
+// tiles, 12.3 us with 64.  Groups of more than 16 rows on 16-row tiles are several tiles high and few: their weights stay
+// in the L2 for the group's next tile, and four stages hide what two do with eight workgroups a CU.  Two stages past the
+// L2, two stages, four stages, us: int8 200 x 1024 x 2048 13.0, 8.9, 6.0, 400 x 1536 x 2048 14.2, 9.5, 8.3, 8 groups of
+// 50 rows, 1024 x 2048, 13.2, 13.6, 9.2; bf16 4 groups of 50, 1024 x 2048, 22.5, 22.9, 11.0, 8 of 25, 2048 x 512, 8.4, 8.7, 6.9.
 template <class T, int EPI>
 static hipError_t launch_ragged_fwd(const RaggedArgs& a, hipStream_t s) {
   const long long mean = ((long long)a.R + a.E - 1) / a.E;
@@ -832,7 +835,7 @@ static hipError_t launch_ragged_fwd(const RaggedArgs& a, hipStream_t s) {
     return launch_ragged_cfg<T, kFwd, EPI, TileShape<64, 128, 1, 4, 128, 2>>(a, s);
   if (mean > 16 && fills(a, 32, a.N / cols, 128 / cols))
     return launch_ragged_cfg<T, kFwd, EPI, TileShape<32, 128, 1, 4, 128, 2>>(a, s);
-  if (fills(a, 16, a.N / cols, 64 / cols)) {
+  if (mean <= 16 && fills(a, 16, a.N / cols, 64 / cols)) {
     if ((long long)a.K * T::kBytes % 128 == 0) return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 2, 2, true>>(a, s);
     return launch_ragged_cfg<T, kFwd, EPI, TileShape<16, 64, 1, 2, 128, 2>>(a, s);
   }
