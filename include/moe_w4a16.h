@@ -609,13 +609,15 @@ moe_status_t moe_ffn_forward_f8(const uint16_t* x, const float* router_logits, i
  * ascending and within [0, R]; the kernels clamp them to that range.  Rows that no expert owns (past
  * offsets[E]) are not written.  Experts without rows cost nothing.
  * a_row_of, a_row_div: activation row of row r = a_row_of ? a_row_of[r] / a_row_div : r (with a_row_of the
- * sorted_ids of moe_align and a_row_div = k, the token of the row).
+ * sorted_ids of moe_align and a_row_div = k, the token of the row).  Unlike the offsets these indexes are not
+ * checked: for every row that an expert owns, the activation row has to lie within the activations.
  * One expert's weights stay below 4 GiB.
  */
 #define MOE_IN_F16 2
 #define MOE_OUT_F16 5
 #define MOE_RAGGED_MAX_DIM (1 << 20) /* largest N and K */
-#define MOE_I8_MAX_K (1 << 17)       /* sums of K products of int8 codes stay exact in int32 */
+#define MOE_I8_MAX_K (1 << 17)       /* sums of K products of int8 codes in [-127, 127] stay exact in int32 (and with
+                                        -128 too, unless all K products of a sum are -128 * -128 at the largest K) */
 
 /*
  * Rows quantized to int8: s[r] = fp32(max |x[r, :]| / 127), q[r, c] = the integer nearest to x[r, c] / s[r]

@@ -63,8 +63,9 @@ __device__ __forceinline__ u32x2 i8_codes8(const float (&v)[8], float s) {
 }
 
 // One workgroup per row, 8 elements a thread and chunk.  J chunks a thread stay in registers between the
-// maximum and the codes; with J == 0 (longer rows) they are read again.  Bound by the read (4096 x 4096 bf16: 17 us, 3.0
-// TB/s of x and codes), small batches by latency (77 x 2048: 3.3 us).
+// maximum and the codes; with J == 0 (longer rows) they are read again.  Small batches are bound by latency (77 x 2048: 3.3
+// us), large ones by it too: 4096 x 4096 bf16 takes 17 us (3.0 TB/s of x and codes, where a copy reaches 4.9), as a
+// workgroup waits for its one row before it writes and half of its four chunks a thread are empty there.
 template <int IN, int J, int TH>
 __global__ __launch_bounds__(TH) void i8_quant_kernel(const void* __restrict__ x, int rows, int K,
                                                       int8_t* __restrict__ q, float* __restrict__ s) {

@@ -12,11 +12,14 @@
 // contraction axis is contiguous in memory ("rows") is kept as [row][RB bytes]; one whose other axis is
 // contiguous (W in DX, both in DW) as [contraction row][tile columns], and its fragments are read with
 // the transposing LDS load (ds_read_b64_tr_b16: a 16-lane group reads a 4 x 16 block and lane j gets
-// column j).  16-byte chunks are XOR-swizzled so that neither kind of read has bank conflicts.
+// column j).  16-byte chunks are XOR-swizzled so that neither kind of fragment read has bank conflicts (the results'
+// way through LDS has: a third of the LDS cycles of bf16 weight gradients with 25 rows a group, whose results outweigh
+// their contraction; 2-5 % of the others').
 //
-// What bounds it.  Many rows: the matrix units' power and the barrier of a step, one workgroup of 8 waves a CU: fp16
-// 8 experts of 4096 x 14336 over 8192 rows 930-980 us (0.98-1.03 PFLOP/s, units busy 51 % of the cycles), int8 4096 x
-// 28672 x 4096 402 us (2.4 POP/s, 52 %).  Few rows: the weights' bytes, many small workgroups a CU: 64 rows over 128
+// What bounds it.  Many rows: the barrier of a step, one workgroup of 8 waves a CU, and clocks that fall with the matrix
+// units' load (a dense library product of fp16 reaches 1.53 PFLOP/s on this card, of int8 2.15 POP/s): fp16 8 experts
+// of 4096 x 14336 over 8192 rows 930-980 us (0.98-1.03 PFLOP/s, units busy 51 % of the cycles; about 2.5 rounds of tiles
+// where the rows fill 2.0), int8 4096 x 28672 x 4096 402 us (2.4 POP/s, 52 %).  Few rows: the weights' bytes, many small workgroups a CU: 64 rows over 128
 // experts of 1536 x 2048, int8 28 us, bf16 57 us (5.7-5.9 TB/s).
 //
 // Fragments of v_mfma_f32_16x16x32 (16-bit) and v_mfma_i32_16x16x64_i8: lane l supplies 16 bytes, row
@@ -274,7 +277,7 @@ __device__ __forceinline__ void store1(void* C, int out, size_t at, float v) {
 constexpr int kDwIds = 1024;
 
 // Shape of one tile height's work: BM x BN by WM x WN waves, steps of RB bytes, NA stages of the A operand's tile
-// and NB >= NA of the B operand's.  ONCE: most groups are one tile high, so that the B operand is read once.
+// and NB >= NA of the B operand's.  ONCE: for groups that are one tile high on the average, so that the B operand is read once.
 template <int BM_, int BN_, int WM_, int WN_, int RB_, int NA_, int NB_ = NA_, bool ONCE_ = false>
 struct TileShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, RB = RB_, NA = NA_, NB = NB_;

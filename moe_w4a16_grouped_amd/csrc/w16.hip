@@ -10,7 +10,10 @@ namespace moe {
 // Tile choice of the gradients, by the mean rows of a group.  Measured (fp16, weights from HBM): row gradients of 256
 // experts of 1024 x 2048 with 25 rows 195 us with 64 x 256 tiles, 206 us with 32 x 256, 226 us with 32 x 128; 64
 // experts, mean 200: 97 us with 128 x 256 (two workgroups a CU) against 99 us with 256 x 256 and 109 with 64 x 256;
-// mean 400: 143 against 159 and 181; mean 1024 (8 experts of 4096 x 14336): 1085 against 1010.
+// mean 400: 143 against 159 and 181; mean 1024 (8 experts of 4096 x 14336): 1085 against 1010.  Below about 16 rows a
+// group no one shape is best; 64 x 256 against 16 x 128, bf16, mean 7: 64 experts 52.8 against 52.9 us, 256 experts 186
+// against 190, groups of 0 to 60 rows 47 against 52, but 128 experts of 1536 x 2048 156 against 139 and 14 of 2424 x 4528
+// 76 against 57 (32 x 128 tiles, in the same order: 56, 190, 48, 147 and 55 us).
 template <class T>
 static hipError_t launch_dx(const RaggedArgs& a, hipStream_t s) {
   const long long mean = ((long long)a.R + a.E - 1) / a.E;
@@ -23,7 +26,9 @@ static hipError_t launch_dx(const RaggedArgs& a, hipStream_t s) {
 
 // Weight gradients (bf16) of 64 experts of 1024 x 2048, mean 100: 73 us with 256 x 128 tiles (two workgroups a CU), 73
 // with 128 x 128, 81 with 256 x 256; mean 375: 130, 133, 139; 256 experts, mean 25: 231, 230, 258; mean 1024 (8 experts
-// of 4096 x 14336, fp16, 32-bit results): 1239 against 1090 us with 256 x 256.
+// of 4096 x 14336, fp16, 32-bit results): 1239 against 1090 us with 256 x 256.  A few rows a group are all results:
+// 256 x 128 against 128 x 128, mean 4: 256 experts 179 against 183 us, 128 of 1536 x 2048 137 against 140, 14 of 2424 x
+// 4528 80 against 72; with 32-bit results 324 against 318, 245 against 249, 127 against 126.
 //
 // A few output tiles with many rows leave most CUs idle: the rows are then cut into parts, whose sums (fp32, in the
 // workspace) a second launch adds in order.  One group of 8192 rows, 1024 x 2048 weights (128 tiles): 101
