@@ -99,3 +99,36 @@ def test_results_may_be_freed_on_the_current_stream():
     later = moe.moe_silu_mul(G2, stream=other)
     torch.cuda.synchronize()
     assert torch.equal(read, want) and torch.equal(later, moe.moe_silu_mul(G2))
+
+
+@pytest.mark.gpu
+def test_a_given_stream_within_a_captured_graph():
+    """Two streams of one captured graph, with tensors made on both; replayed with other inputs, eager calls between."""
+    x, W = _rand((640, 256), BF16, 1), _rand((2, 512, 256), BF16, 2, 0.06)
+    off = torch.tensor([0, 300, 640], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def both(a, s):
+        here = torch.cuda.current_stream()
+        if s is not None:
+            s.wait_stream(here)
+        G = moe.moe_grouped_gemm_w16(a, None, 1, W, off, 640, stream=s)
+        q = moe.moe_i8_quantize(a)
+        h = moe.moe_silu_mul(G, stream=s)
+        if s is not None:
+            here.wait_stream(s)
+        return [G, *q, h, moe.moe_silu_mul_grad(G, h)]
+
+    live = x.clone()
+    both(live, None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both(live, side)
+    for seed in (3, 4, 3):
+        src = _rand((640, 256), BF16, seed)
+        live.copy_(src)
+        graph.replay()
+        want = both(src, None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), seed
