@@ -3,9 +3,10 @@
 Each function has the name of the C entry point it calls, takes torch tensors on the GPU, passes
 their data pointers and the current HIP stream, and raises ``MoEError`` on a negative status.  With
 ``stream=`` the call runs on that stream, to which the tensors made for it belong; the caller
-sees to it that the tensors given are ready there, and keeps them until it is done.  Every step
-of the layer runs in the HIP kernels of the library; there is no fallback of any kind: if the
-library is not built, loading fails with an error that says how to build it.
+sees to it that the tensors given are ready there, and keeps them until it is done.  No call
+builds an autograd graph: results of tensors that require grad carry none.  Every step of the
+layer runs in the HIP kernels of the library; there is no fallback of any kind: if the library is
+not built, loading fails with an error that says how to build it.
 """
 from __future__ import annotations
 

@@ -19,8 +19,8 @@
 // What bounds it.  Many rows: the barrier of a step, one workgroup of 8 waves a CU, and clocks that fall with the matrix
 // units' load (a dense library product of fp16 reaches 1.53 PFLOP/s on this card, of int8 2.15 POP/s): fp16 8 experts
 // of 4096 x 14336 over 8192 rows 930-980 us (0.98-1.03 PFLOP/s, units busy 51 % of the cycles; about 2.5 rounds of tiles
-// where the rows fill 2.0), int8 4096 x 28672 x 4096 402 us (2.4 POP/s, 52 %).  Few rows: the weights' bytes, many small workgroups a CU: 64 rows over 128
-// experts of 1536 x 2048, int8 28 us, bf16 57 us (5.7-5.9 TB/s).
+// where the rows fill 2.0), int8 4096 x 28672 x 4096 402-412 us (2.3-2.4 POP/s, 52 %).  Few rows: the weights' bytes,
+// many small workgroups a CU: 64 rows over 128 experts of 1536 x 2048, int8 28 us, bf16 57 us (5.7-5.9 TB/s).
 //
 // Fragments of v_mfma_f32_16x16x32 (16-bit) and v_mfma_i32_16x16x64_i8: lane l supplies 16 bytes, row
 // l % 16, contraction bytes [16 (l / 16), +16) of a 64-byte group.  The weight fragment is the first
