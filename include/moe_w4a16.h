@@ -743,6 +743,77 @@ moe_status_t moe_ffn_forward_w16(const uint16_t* x, const float* router_logits, 
                                  int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
                                  void* stream);
 
+/*
+ * ---- Root-mean-square norm in front of the experts -----------------------------------------------------
+ * [ATOM, 8.2: dynamic activation quantization is part of a format's contract.]  For each row of x [T, H]:
+ *   s = x + residual (fp32, rounded to the type; s = x where residual is NULL)
+ *   r = 1 / sqrt(mean(s^2) + eps),  y = s * r * weight (fp32, rounded once)
+ * and, formed in the same pass, 8-bit codes and scales of y for the products that take them:
+ *   MOE_QUANT_I8  one scale a row (moe_gemm_i8, moe_grouped_gemm_i8): scale = max |y| / 127, code = the integer
+ *                 nearest to the real quotient 127 z / max |z|, z = s * weight (which y / scale is), ties to even.
+ *   MOE_QUANT_F8  one scale per row and 128 columns (moe_grouped_gemm_f8): scale = max |y| / 448, code = the E4M3
+ *                 value nearest to the real quotient 448 z / max |z|, ties to the even code.
+ * The codes are those of the unrounded y.  Where a scale is 0 its codes are 0.  A row in which s or z holds an
+ * infinity or a NaN gets scales NaN and codes 0; its y follows the formula (r = 0 beside an infinity).
+ *   dtype      MOE_IN_BF16 or MOE_IN_F16: the type of x, residual, s and y; weight [H] of weight_dtype (dtype or
+ *              MOE_IN_F32).  eps finite and > 0.
+ *   s          [T, H], written where residual is given (it may be x or residual); ignored (NULL) without one.
+ *   y          [T, H] or NULL (only with codes); may be x without a residual, and residual with one.
+ *   q, q_scale codes [T, H] (int8, or E4M3 bytes) and fp32 scales [T] or [T, H / 128]; NULL for MOE_QUANT_NONE.
+ * Shapes: 0 <= T < 2^26; H a positive multiple of 8 (I8: 16, F8: 128) and <= MOE_NORM_MAX_H.
+ * Alignment: q_scale 4 bytes, all other pointers 16.
+ */
+#define MOE_QUANT_NONE 0
+#define MOE_QUANT_I8 1
+#define MOE_QUANT_F8 2
+#define MOE_NORM_MAX_H 16384
+moe_status_t moe_rmsnorm_add(const void* x, const void* residual, int32_t dtype, const void* weight, int32_t weight_dtype,
+                             float eps, int32_t T, int32_t H, void* s, void* y, int32_t quant, void* q, float* q_scale,
+                             void* stream);
+
+/* Workspace bytes of moe_rmsnorm_add_grad (host-only, pure; 0 on invalid sizes, and where T is 0). */
+size_t moe_rmsnorm_add_grad_workspace_bytes(int32_t T, int32_t H);
+
+/*
+ * Gradient of moe_rmsnorm_add: dy [T, H] (gradient of y), the s of the forward pass (x where it had no residual),
+ * ds [T, H] (gradient that reaches s by other paths, such as the residual stream's, or NULL):
+ *   dx = r * (dy * weight - s * r^2 * mean(dy * weight * s)) + ds     [T, H], of x and of the residual alike
+ *   dweight = sum over the rows of dy * s * r                         [H], of dweight_dtype MOE_OUT_BF16, _F16 or _F32
+ * Sums over a row in 64 bits, everything else in fp32, one rounding.  dweight is summed in parts of the rows, which are
+ * added in order (zeros where T is 0).  workspace: at least moe_rmsnorm_add_grad_workspace_bytes(T, H) bytes.
+ * dx may be dy, s or ds.  Types, shapes and alignment as for moe_rmsnorm_add.
+ */
+moe_status_t moe_rmsnorm_add_grad(const void* dy, const void* s, int32_t dtype, const void* weight, int32_t weight_dtype,
+                                  float eps, const void* ds, int32_t T, int32_t H, void* dx, void* dweight,
+                                  int32_t dweight_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- The layer for a few tokens, in two launches --------------------------------------------------------
+ * [ATOM, 8.1.]  What moe_ffn_forward_w16 and moe_ffn_forward_i8 compute in five to seven launches, for decode steps of
+ * at most MOE_FEW_MAX_TOKENS tokens: routing, gate_up and SiLU*mul in one launch, down and the weighted sum in another.
+ *   y[t] = sum_s w[t,s] * W2_e(s) ( silu(W1_e(s) x[t]) * (W3_e(s) x[t]) ),  e(s) = topk_ids[t, s]  (moe_route_topk)
+ *   moe_ffn_few_w16:   w13 bf16 [E, 2I, H], w2 bf16 [E, H, I].
+ *   moe_ffn_few_w8a16: the int8 weights and channel scales of moe_ffn_forward_i8; activations are not quantized (a few
+ *                      tokens are bound by the weights' bytes).
+ * x bf16 [T, H]; router_logits fp32 [T, E], finite; y bf16 [T, H] out, rounded once: h keeps about 16 significant bits
+ * and all sums are fp32.  topk_ids_out int32 [T, k], topk_w_out fp32 [T, k]: optional copies of the routing (NULL = skip).
+ * workspace: at least moe_ffn_few_workspace_bytes(T, H, I, E, k) bytes.  Where T * H passes 65536 the tokens are taken in
+ * groups that stay below it, each with its two launches (and its own reading of the weights).
+ * Shapes: 0 <= T <= MOE_FEW_MAX_TOKENS, 1 <= k <= min(E, MOE_FEW_MAX_K), E <= MOE_MAX_EXPERTS, H and I multiples of
+ * 16, 16 <= H <= 65536, 16 <= I <= MOE_I8_MAX_K.  Alignment: x, weights, y and workspace 16 bytes, the others 4.
+ */
+#define MOE_FEW_MAX_TOKENS 16
+#define MOE_FEW_MAX_K 16
+/* Workspace bytes of both (host-only, pure; 0 on invalid sizes). */
+size_t moe_ffn_few_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k);
+moe_status_t moe_ffn_few_w16(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E,
+                             int32_t k, const uint16_t* w13, const uint16_t* w2, uint16_t* y, int32_t* topk_ids_out,
+                             float* topk_w_out, void* workspace, size_t workspace_bytes, void* stream);
+moe_status_t moe_ffn_few_w8a16(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E,
+                               int32_t k, const int8_t* w13_q, const float* w13_s, const int8_t* w2_q, const float* w2_s,
+                               uint16_t* y, int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

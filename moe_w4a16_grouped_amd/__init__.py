@@ -19,7 +19,10 @@ from ._lib import (MOE_ACT_ROWS, MOE_ACT_TILED, MOE_EPI_NONE, MOE_EPI_SILU_MUL, 
                    moe_i8_quantize, moe_gemm_i8, moe_linear_i8_workspace_bytes, moe_linear_i8, moe_grouped_gemm_i8,
                    moe_ffn_i8_workspace_bytes, moe_ffn_forward_i8, moe_grouped_gemm_w16, moe_grouped_gemm_w16_dx,
                    moe_grouped_gemm_w16_dw, moe_grouped_gemm_w16_dw_workspace_bytes, moe_silu_mul, moe_silu_mul_grad, moe_ffn_w16_workspace_bytes,
-                   moe_ffn_forward_w16, MOE_IN_F16, MOE_OUT_F16)
+                   moe_ffn_forward_w16, MOE_IN_F16, MOE_OUT_F16,
+                   MOE_QUANT_NONE, MOE_QUANT_I8, MOE_QUANT_F8, MOE_FEW_MAX_TOKENS, moe_rmsnorm_add,
+                   moe_rmsnorm_add_grad_workspace_bytes, moe_rmsnorm_add_grad, moe_ffn_few_workspace_bytes, moe_ffn_few_w16,
+                   moe_ffn_few_w8a16)
 
 __all__ = ["MOE_ACT_ROWS", "MOE_ACT_TILED", "MOE_EPI_NONE", "MOE_EPI_SILU_MUL", "MOE_LAYOUT_CANONICAL", "MOE_LAYOUT_PACKED", "MOE_OUT_BF16",
            "MOE_OUT_F32", "MOE_OUT_F16E", "MOE_OUT_H16", "EXPORTED", "LIB_PATH", "MoEError", "load", "moe_align", "moe_align_workspace_bytes",
@@ -35,4 +38,7 @@ __all__ = ["MOE_ACT_ROWS", "MOE_ACT_TILED", "MOE_EPI_NONE", "MOE_EPI_SILU_MUL", 
            "moe_i8_quantize", "moe_gemm_i8", "moe_linear_i8_workspace_bytes", "moe_linear_i8", "moe_grouped_gemm_i8",
            "moe_ffn_i8_workspace_bytes", "moe_ffn_forward_i8", "moe_grouped_gemm_w16", "moe_grouped_gemm_w16_dx",
            "moe_grouped_gemm_w16_dw", "moe_grouped_gemm_w16_dw_workspace_bytes", "moe_silu_mul", "moe_silu_mul_grad", "moe_ffn_w16_workspace_bytes",
-           "moe_ffn_forward_w16", "MOE_IN_F16", "MOE_OUT_F16"]
+           "moe_ffn_forward_w16", "MOE_IN_F16", "MOE_OUT_F16",
+           "MOE_QUANT_NONE", "MOE_QUANT_I8", "MOE_QUANT_F8", "MOE_FEW_MAX_TOKENS", "moe_rmsnorm_add",
+           "moe_rmsnorm_add_grad_workspace_bytes", "moe_rmsnorm_add_grad", "moe_ffn_few_workspace_bytes", "moe_ffn_few_w16",
+           "moe_ffn_few_w8a16"]

@@ -39,6 +39,10 @@ MOE_OUT_F16E = 3
 MOE_OUT_H16 = 4
 MOE_IN_F16 = 2
 MOE_OUT_F16 = 5
+MOE_QUANT_NONE = 0
+MOE_QUANT_I8 = 1
+MOE_QUANT_F8 = 2
+MOE_FEW_MAX_TOKENS = 16
 
 _lib = None
 
@@ -116,6 +120,12 @@ def load() -> ctypes.CDLL:
         "moe_silu_mul_grad": ([P, P, I32, I32, I32, P, P], I32),
         "moe_ffn_w16_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
         "moe_ffn_forward_w16": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P], I32),
+        "moe_rmsnorm_add": ([P, P, I32, P, I32, ctypes.c_float, I32, I32, P, P, I32, P, P, P], I32),
+        "moe_rmsnorm_add_grad_workspace_bytes": ([I32, I32], SZ),
+        "moe_rmsnorm_add_grad": ([P, P, I32, P, I32, ctypes.c_float, P, I32, I32, P, P, I32, P, SZ, P], I32),
+        "moe_ffn_few_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+        "moe_ffn_few_w16": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P], I32),
+        "moe_ffn_few_w8a16": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P], I32),
         "moe_ffn_noalloc_scratch_bytes": ([], SZ),
         "moe_ffn_forward_noalloc": ([P, P, I32, I32, I32, I32, I32, P, P, P, P, I32, P, P, P, P], I32),
     }
@@ -139,7 +149,8 @@ EXPORTED = ("moe_abi_version", "moe_status_string", "moe_last_error", "moe_route
             "moe_grouped_gemm_w4f16", "moe_i8_quantize", "moe_gemm_i8", "moe_linear_i8_workspace_bytes", "moe_linear_i8",
             "moe_grouped_gemm_i8", "moe_ffn_i8_workspace_bytes", "moe_ffn_forward_i8", "moe_grouped_gemm_w16",
             "moe_grouped_gemm_w16_dx", "moe_grouped_gemm_w16_dw_workspace_bytes", "moe_grouped_gemm_w16_dw", "moe_silu_mul", "moe_silu_mul_grad",
-            "moe_ffn_w16_workspace_bytes", "moe_ffn_forward_w16")
+            "moe_ffn_w16_workspace_bytes", "moe_ffn_forward_w16", "moe_rmsnorm_add", "moe_rmsnorm_add_grad_workspace_bytes",
+            "moe_rmsnorm_add_grad", "moe_ffn_few_workspace_bytes", "moe_ffn_few_w16", "moe_ffn_few_w8a16")
 
 
 def _check(status: int):
@@ -695,7 +706,7 @@ _IN = {torch.bfloat16: MOE_IN_BF16, torch.float16: MOE_IN_F16, torch.float32: MO
 _OUT = {torch.bfloat16: MOE_OUT_BF16, torch.float16: MOE_OUT_F16, torch.float32: MOE_OUT_F32}
 _OUT_DTYPE = {v: k for k, v in _OUT.items()}
 _W16 = (torch.bfloat16, torch.float16)
-_I8, _F32, _INT32, _U8 = (torch.int8,), (torch.float32,), (torch.int32,), (torch.uint8,)
+_I8, _F32, _INT32, _U8, _BF16 = (torch.int8,), (torch.float32,), (torch.int32,), (torch.uint8,), (torch.bfloat16,)
 _ACT = tuple(_IN)
 
 
@@ -985,4 +996,113 @@ def moe_ffn_forward_w16(x, router_logits, w13, w2, k: int, y=None, topk_ids_out=
     _call(load().moe_ffn_forward_w16, dev, stream, (y, workspace), x.data_ptr(), router_logits.data_ptr(), T, H, I, E, k,
           w13.data_ptr(), w2.data_ptr(), y.data_ptr(), _ptr(topk_ids_out), _ptr(topk_w_out), workspace.data_ptr(),
           workspace.numel())
+    return y
+
+
+def moe_rmsnorm_add(x, weight, eps: float, residual=None, quant: int = MOE_QUANT_NONE, want_y: bool = True, s=None, y=None,
+                    q=None, q_scale=None, stream=None):
+    """x [T, H] bf16 or fp16, weight [H] of its type or fp32, residual [T, H] or None -> (s, y, q, q_scale): s = x +
+    residual (None without one), y the normalised rows (None where want_y is false and no y is given), q the codes [T, H]
+    (int8, or E4M3 bytes in uint8) and q_scale fp32 [T] or [T, H / 128] (None for MOE_QUANT_NONE)."""
+    T, H = _need(x, _W16, (None, None), "x")
+    dev, dt = x.device, x.dtype
+    _need(weight, (dt, torch.float32), (H,), "weight", dev)
+    if residual is not None:
+        _need(residual, (dt,), (T, H), "residual", dev)
+        s = _out(s, (T, H), _OUT[dt], dev, "s", stream)
+    elif s is not None:
+        raise ValueError("s is the sum with a residual, and none is given")
+    if want_y or y is not None:
+        y = _out(y, (T, H), _OUT[dt], dev, "y", stream)
+    if quant == MOE_QUANT_NONE:
+        if q is not None or q_scale is not None:
+            raise ValueError("q and q_scale belong to a quant of MOE_QUANT_I8 or MOE_QUANT_F8")
+    elif quant in (MOE_QUANT_I8, MOE_QUANT_F8):
+        code = _I8 if quant == MOE_QUANT_I8 else _U8
+        if quant == MOE_QUANT_F8 and H % 128:
+            raise ValueError(f"MOE_QUANT_F8 needs a multiple of 128 columns (got {H})")
+        shape = (T,) if quant == MOE_QUANT_I8 else (T, H // 128)
+        if q is None:
+            q = _empty((T, H), code[0], dev, stream)
+        else:
+            _need(q, code, (T, H), "q", dev)
+        if q_scale is None:
+            q_scale = _empty(shape, torch.float32, dev, stream)
+        else:
+            _need(q_scale, _F32, shape, "q_scale", dev)
+    else:
+        raise ValueError(f"unknown quant {quant}")
+    _call(load().moe_rmsnorm_add, dev, stream, (s, y, q, q_scale), x.data_ptr(), _ptr(residual), _IN[dt], weight.data_ptr(),
+          _IN[weight.dtype], eps, T, H, _ptr(s), _ptr(y), quant, _ptr(q), _ptr(q_scale))
+    return s, y, q, q_scale
+
+
+def moe_rmsnorm_add_grad_workspace_bytes(T: int, H: int) -> int:
+    return int(load().moe_rmsnorm_add_grad_workspace_bytes(T, H))
+
+
+def moe_rmsnorm_add_grad(dy, s, weight, eps: float, ds=None, out_dtype: int = None, dx=None, dweight=None, workspace=None,
+                         stream=None):
+    """Gradient of moe_rmsnorm_add: dy [T, H], s [T, H] (the forward pass's sum, or its x), ds [T, H] or None -> (dx [T, H],
+    of x and of the residual, dweight [H] of out_dtype, by default the weight's type)."""
+    T, H = _need(s, _W16, (None, None), "s")
+    dev, dt = s.device, s.dtype
+    _need(dy, (dt,), (T, H), "dy", dev)
+    _need(weight, (dt, torch.float32), (H,), "weight", dev)
+    if ds is not None:
+        _need(ds, (dt,), (T, H), "ds", dev)
+    out_dtype = _OUT[weight.dtype] if out_dtype is None else out_dtype
+    dx = _out(dx, (T, H), _OUT[dt], dev, "dx", stream)
+    dweight = _out(dweight, (H,), out_dtype, dev, "dweight", stream)
+    lib, size = load(), 0
+    if workspace is not None:
+        size, = _need(workspace, _U8, (None,), "workspace", dev)
+    else:
+        size = lib.moe_rmsnorm_add_grad_workspace_bytes(T, H)
+        if size:
+            workspace = _empty((size,), torch.uint8, dev, stream, keep=False)
+    _call(lib.moe_rmsnorm_add_grad, dev, stream, (dx, dweight, workspace), dy.data_ptr(), s.data_ptr(), _IN[dt],
+          weight.data_ptr(), _IN[weight.dtype], eps, _ptr(ds), T, H, dx.data_ptr(), dweight.data_ptr(), out_dtype,
+          _ptr(workspace), size)
+    return dx, dweight
+
+
+def moe_ffn_few_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
+    return int(load().moe_ffn_few_workspace_bytes(T, H, I, E, k))
+
+
+def moe_ffn_few_w16(x, router_logits, w13, w2, k: int, y=None, topk_ids_out=None, topk_w_out=None, workspace=None,
+                    stream=None):
+    """Whole layer for at most 16 tokens in two launches, bf16 weights (arguments of moe_ffn_forward_w16)."""
+    T, H = _need(x, _BF16, (None, None), "x")
+    dev = x.device
+    E, N13, _ = _need(w13, _BF16, (None, None, H), "w13", dev)
+    I = _halves(N13, "w13")
+    _need(w2, _BF16, (E, H, I), "w2", dev)
+    lib = load()
+    y, workspace = _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
+                             lib.moe_ffn_few_workspace_bytes(T, H, I, E, k), stream)
+    _call(lib.moe_ffn_few_w16, dev, stream, (y, topk_ids_out, topk_w_out, workspace), x.data_ptr(), router_logits.data_ptr(), T,
+          H, I, E, k, w13.data_ptr(), w2.data_ptr(), y.data_ptr(), _ptr(topk_ids_out), _ptr(topk_w_out), workspace.data_ptr(),
+          workspace.numel())
+    return y
+
+
+def moe_ffn_few_w8a16(x, router_logits, w13_q, w13_s, w2_q, w2_s, k: int, y=None, topk_ids_out=None, topk_w_out=None,
+                      workspace=None, stream=None):
+    """Whole layer for at most 16 tokens in two launches, int8 weights with channel scales (arguments of
+    moe_ffn_forward_i8), activations not quantized."""
+    T, H = _need(x, _BF16, (None, None), "x")
+    dev = x.device
+    E, N13, _ = _need(w13_q, _I8, (None, None, H), "w13_q", dev)
+    I = _halves(N13, "w13_q")
+    _need(w13_s, _F32, (E, 2 * I), "w13_s", dev)
+    _need(w2_q, _I8, (E, H, I), "w2_q", dev)
+    _need(w2_s, _F32, (E, H), "w2_s", dev)
+    lib = load()
+    y, workspace = _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
+                             lib.moe_ffn_few_workspace_bytes(T, H, I, E, k), stream)
+    _call(lib.moe_ffn_few_w8a16, dev, stream, (y, topk_ids_out, topk_w_out, workspace), x.data_ptr(), router_logits.data_ptr(),
+          T, H, I, E, k, w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(), y.data_ptr(),
+          _ptr(topk_ids_out), _ptr(topk_w_out), workspace.data_ptr(), workspace.numel())
     return y

@@ -1682,4 +1682,144 @@ moe_status_t moe_ffn_forward_w16(const uint16_t* x, const float* router_logits, 
                         workspace, workspace_bytes, false, "moe_ffn_forward_w16", (hipStream_t)stream);
 }
 
+// Types, sizes and eps shared by the norm and its gradient.
+static moe_status_t check_norm(int32_t dtype, int32_t weight_dtype, float eps, int32_t T, int32_t H, int32_t multiple, const char* who) {
+  if (moe_status_t st = check_w16_dtype(dtype, who)) return st;
+  if (weight_dtype != dtype && weight_dtype != MOE_IN_F32)
+    return fail(MOE_ERR_INVALID_ARG, "%s: weight_dtype %d must be dtype or MOE_IN_F32", who, weight_dtype);
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and > 0", who);
+  if (T < 0 || H < 1) return fail(MOE_ERR_INVALID_ARG, "%s: need T >= 0 and H >= 1", who);
+  if ((int64_t)T >= kMaxRows || H > MOE_NORM_MAX_H || H % multiple != 0)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: T=%d must be < 2^26, H=%d a multiple of %d and <= %d", who, T, H, multiple,
+                MOE_NORM_MAX_H);
+  return MOE_OK;
+}
+
+moe_status_t moe_rmsnorm_add(const void* x, const void* residual, int32_t dtype, const void* weight, int32_t weight_dtype,
+                             float eps, int32_t T, int32_t H, void* s, void* y, int32_t quant, void* q, float* q_scale,
+                             void* stream) {
+  const char* who = "moe_rmsnorm_add";
+  if (quant != MOE_QUANT_NONE && quant != MOE_QUANT_I8 && quant != MOE_QUANT_F8)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown quant %d", who, quant);
+  if (moe_status_t st = check_norm(dtype, weight_dtype, eps, T, H, quant == MOE_QUANT_F8 ? 128 : (quant == MOE_QUANT_I8 ? 16 : 8), who))
+    return st;
+  if (T == 0) return ok();
+  if (!x || !weight || (residual && !s) || (quant == MOE_QUANT_NONE && !y) || (quant != MOE_QUANT_NONE && (!q || !q_scale)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer (s with a residual, y or codes with their scales are required)", who);
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || (residual && !aligned16(s)) || !aligned16(y) ||
+      (quant != MOE_QUANT_NONE && (!aligned16(q) || !aligned4(q_scale))))
+    return fail(MOE_ERR_MISALIGNED, "%s: q_scale needs 4-byte alignment, the other pointers 16-byte", who);
+  const moe::NormArgs a{x, residual, weight, eps, 1.0 / H, T, H, s, y, q, q_scale};
+  return hip_status(moe::launch_rmsnorm(a, dtype == MOE_IN_F16, weight_dtype == MOE_IN_F32, quant, (hipStream_t)stream),
+                    "moe_rmsnorm_add launch");
+}
+
+size_t moe_rmsnorm_add_grad_workspace_bytes(int32_t T, int32_t H) {
+  if (T < 0 || (int64_t)T >= kMaxRows || H < 8 || H % 8 != 0 || H > MOE_NORM_MAX_H) return 0;
+  return (size_t)moe::rmsnorm_grad_parts(T, H) * H * sizeof(float);
+}
+
+moe_status_t moe_rmsnorm_add_grad(const void* dy, const void* s, int32_t dtype, const void* weight, int32_t weight_dtype,
+                                  float eps, const void* ds, int32_t T, int32_t H, void* dx, void* dweight,
+                                  int32_t dweight_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "moe_rmsnorm_add_grad";
+  if (moe_status_t st = check_norm(dtype, weight_dtype, eps, T, H, 8, who)) return st;
+  if (!ragged_out_ok(dweight_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown dweight_dtype %d", who, dweight_dtype);
+  if (!dweight || (T > 0 && (!dy || !s || !weight || !dx || !workspace))) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(dweight) || (T > 0 && (!aligned16(dy) || !aligned16(s) || !aligned16(weight) || !aligned16(ds) || !aligned16(dx) ||
+                                        !aligned16(workspace))))
+    return fail(MOE_ERR_MISALIGNED, "%s: pointers need 16-byte alignment", who);
+  const size_t need = moe_rmsnorm_add_grad_workspace_bytes(T, H);
+  if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu B < required %zu B", who, workspace_bytes, need);
+  const moe::NormGradArgs a{dy, s, weight, ds, eps, 1.0 / H, T, H, dx, static_cast<float*>(workspace), dweight_dtype, dweight};
+  return hip_status(moe::launch_rmsnorm_grad(a, dtype == MOE_IN_F16, weight_dtype == MOE_IN_F32, (hipStream_t)stream),
+                    "moe_rmsnorm_add_grad launch");
+}
+
+// ---- the layer for a few tokens ----------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kFewElems = 65536;  // elements of x that a workgroup's LDS holds
+
+int32_t few_group(int32_t T, int32_t H) { return (int32_t)std::min<int64_t>(T, kFewElems / H); }  // tokens of one pair of launches
+
+bool few_dims_ok(int32_t H, int32_t I) {
+  return H >= 16 && I >= 16 && H % 16 == 0 && I % 16 == 0 && H <= kFewElems && I <= MOE_I8_MAX_K;
+}
+
+struct FewLayout {
+  size_t h, table, ids, w, total;
+};
+
+FewLayout few_layout(int64_t T, int64_t group, int64_t I, int64_t k) {
+  FewLayout L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += up256(bytes);
+    return at;
+  };
+  L.h = take((size_t)(group * k * I) * 4);
+  L.table = take((size_t)(8 + 8 * group * k) * 4);
+  L.ids = take((size_t)(T * k) * 4);
+  L.w = take((size_t)(T * k) * 4);
+  L.total = off;
+  return L;
+}
+
+moe_status_t run_few(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E, int32_t k,
+                     const void* w13, const float* w13_s, const void* w2, const float* w2_s, uint16_t* y,
+                     int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes, bool i8,
+                     const char* who, hipStream_t s) {
+  if (moe_status_t st = check_routing_shape(T, E, k)) return st;
+  if (T > MOE_FEW_MAX_TOKENS || k > MOE_FEW_MAX_K)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: T=%d must not exceed %d, k=%d not %d", who, T, MOE_FEW_MAX_TOKENS, k, MOE_FEW_MAX_K);
+  if (!few_dims_ok(H, I))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H=%d and I=%d must be positive multiples of 16, <= %d and %d", who, H, I,
+                (int)kFewElems, MOE_I8_MAX_K);
+  if (T == 0) return ok();
+  if (!x || !router_logits || !w13 || !w2 || (i8 && (!w13_s || !w2_s)) || !y || !workspace)
+    return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(y) || !aligned16(workspace) || !aligned4(w13_s) ||
+      !aligned4(w2_s) || !aligned4(router_logits) || !aligned4(topk_ids_out) || !aligned4(topk_w_out))
+    return fail(MOE_ERR_MISALIGNED, "%s: x, weights, y and workspace need 16-byte alignment, the others 4-byte", who);
+  const int32_t group = few_group(T, H);
+  const FewLayout L = few_layout(T, group, I, k);
+  if (workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu B < required %zu B", who, workspace_bytes, L.total);
+  char* ws = static_cast<char*>(workspace);
+  int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
+  float* w = topk_w_out ? topk_w_out : reinterpret_cast<float*>(ws + L.w);
+  for (int32_t t = 0; t < T; t += group) {
+    const moe::FewArgs a{x + (size_t)t * H, router_logits + (size_t)t * E, std::min(group, T - t), H, I, E, k, w13, w13_s, w2, w2_s,
+                         reinterpret_cast<uint16_t*>(ws + L.h), reinterpret_cast<int32_t*>(ws + L.table), ids + t * k, w + t * k,
+                         y + (size_t)t * H, 1};
+    const hipError_t e = moe::launch_ffn_few(a, i8, s);
+    if (e != hipSuccess) return hip_status(e, who);
+  }
+  return ok();
+}
+
+}  // namespace
+
+size_t moe_ffn_few_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k) {
+  if (T < 1 || T > MOE_FEW_MAX_TOKENS || !few_dims_ok(H, I) || E < 1 || k < 1 || k > E || k > MOE_FEW_MAX_K || E > MOE_MAX_EXPERTS) return 0;
+  return few_layout(T, few_group(T, H), I, k).total;
+}
+
+moe_status_t moe_ffn_few_w16(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E,
+                             int32_t k, const uint16_t* w13, const uint16_t* w2, uint16_t* y, int32_t* topk_ids_out,
+                             float* topk_w_out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_few(x, router_logits, T, H, I, E, k, w13, nullptr, w2, nullptr, y, topk_ids_out, topk_w_out, workspace,
+                 workspace_bytes, false, "moe_ffn_few_w16", (hipStream_t)stream);
+}
+
+moe_status_t moe_ffn_few_w8a16(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E,
+                               int32_t k, const int8_t* w13_q, const float* w13_s, const int8_t* w2_q, const float* w2_s,
+                               uint16_t* y, int32_t* topk_ids_out, float* topk_w_out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_few(x, router_logits, T, H, I, E, k, w13_q, w13_s, w2_q, w2_s, y, topk_ids_out, topk_w_out, workspace,
+                 workspace_bytes, true, "moe_ffn_few_w8a16", (hipStream_t)stream);
+}
+
 }  // extern "C"

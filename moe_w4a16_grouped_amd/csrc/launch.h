@@ -205,6 +205,54 @@ hipError_t launch_silu_mul(const uint16_t* G, bool f16, long long R, int I, uint
 hipError_t launch_silu_mul_grad(const uint16_t* G, const uint16_t* dh, bool f16, long long R, int I, uint16_t* dG,
                                 hipStream_t stream);
 
+// The layer for at most 16 tokens in two launches (few.hip).
+struct FewArgs {
+  const uint16_t* x;     // bf16 [T, H]
+  const float* logits;   // [T, E]
+  int T, H, I, E, k;
+  const void* w13;       // bf16 or int8 [E, 2I, H]
+  const float* w13_s;    // int8: [E, 2I]
+  const void* w2;        // [E, H, I]
+  const float* w2_s;     // int8: [E, H]
+  uint16_t* h;           // [T * k, I / 8, 16]: 8 values in bf16, then what their rounding left
+  int32_t* table;        // [8 + 8 * T * k]: the number of entries, then the entries
+  int32_t* ids;          // [T, k]
+  float* weight;         // [T, k]
+  uint16_t* y;           // bf16 [T, H]
+  int pieces;
+};
+hipError_t launch_ffn_few(FewArgs a, bool i8, hipStream_t stream);
+
+// Root-mean-square norm (norm.hip): x, residual (NULL: none), s and y (NULL: none) 16-bit [T, H], w [H].
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  const void* w;
+  float eps;
+  double inv_h;   // 1 / H
+  int T, H;
+  void* s;        // x + residual (written where residual is given)
+  void* y;
+  void* q;        // codes [T, H] and their scales [T] or [T, H / 128]
+  float* q_scale;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, bool f16, bool w_f32, int quant, hipStream_t stream);
+struct NormGradArgs {
+  const void* dy;
+  const void* s;
+  const void* w;
+  const void* ds;  // NULL: none
+  float eps;
+  double inv_h;
+  int T, H;
+  void* dx;
+  float* parts;    // [rmsnorm_grad_parts, H]
+  int dw_out;      // MOE_OUT_BF16, MOE_OUT_F16 or MOE_OUT_F32
+  void* dw;
+};
+int rmsnorm_grad_parts(int T, int H);
+hipError_t launch_rmsnorm_grad(const NormGradArgs& a, bool f16, bool w_f32, hipStream_t stream);
+
 hipError_t launch_prepack(const uint8_t* wq, const uint16_t* ws, int E, int N, int K, uint8_t* pq, uint16_t* ps,
                           hipStream_t stream);
 

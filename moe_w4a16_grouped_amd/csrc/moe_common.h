@@ -151,6 +151,36 @@ __device__ __forceinline__ void g2lds16(const void* g, void* lds_wave_base) {
 }
 
 
+// Eight 16-bit values (bf16 or fp16) of 16 bytes as fp32, and back (round to nearest even).
+template <bool F16>
+__device__ __forceinline__ void unpack8(const u32x4& w, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = F16 ? f16_bits_to_f32(w[i] & 0xFFFFu) : bf16_bits_to_f32(w[i] & 0xFFFFu);
+    v[2 * i + 1] = F16 ? f16_bits_to_f32(w[i] >> 16) : bf16_bits_to_f32(w[i] >> 16);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = F16 ? f32_to_f16_bits(v[2 * i]) : f32_to_bf16_bits(v[2 * i]);
+    const uint32_t hi = F16 ? f32_to_f16_bits(v[2 * i + 1]) : f32_to_bf16_bits(v[2 * i + 1]);
+    w[i] = lo | (hi << 16);
+  }
+  return w;
+}
+
+// 16-byte accesses; PAST 1: stores past the L2, PAST 2: loads too.
+template <int PAST>
+__device__ __forceinline__ u32x4 load16(const u32x4* p) { return PAST > 1 ? __builtin_nontemporal_load(p) : *p; }
+template <int PAST>
+__device__ __forceinline__ void store16(const u32x4& v, u32x4* p) {
+  if (PAST > 0) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
 // Output kinds of the NONE epilogue (GemmArgs::out_f32): 0 bf16, 1 fp32, 2 fp16 (kOutF16Exp) with
 // an exponent per row and 8-column segment that is carried in band.  A segment is stored plainly
 // (8 fp16 values, exponent 0) when its largest finite magnitude m is 0 or in [2^-6, 2^15) and it

@@ -95,37 +95,9 @@ hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilog
 // megabytes, which the next launch finds in the L2s.  PAST 2: operands that the 256 MB memory-side cache cannot hold are
 // loaded so too: 8191 x 14336 forward 117 -> 113 us (6.2 TB/s), gradient 202 -> 183 us (6.4 TB/s), but 8191 x 768, whose
 // operands lie in that cache, 6.8 -> 8.3 us.
-template <bool F16>
-__device__ __forceinline__ void unpack8(const u32x4& w, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = F16 ? f16_bits_to_f32(w[i] & 0xFFFFu) : bf16_bits_to_f32(w[i] & 0xFFFFu);
-    v[2 * i + 1] = F16 ? f16_bits_to_f32(w[i] >> 16) : bf16_bits_to_f32(w[i] >> 16);
-  }
-}
-template <bool F16>
-__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
-  u32x4 w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = F16 ? f32_to_f16_bits(v[2 * i]) : f32_to_bf16_bits(v[2 * i]);
-    const uint32_t hi = F16 ? f32_to_f16_bits(v[2 * i + 1]) : f32_to_bf16_bits(v[2 * i + 1]);
-    w[i] = lo | (hi << 16);
-  }
-  return w;
-}
-
 __device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
 constexpr long long kNearBytes = 8ll << 20, kFarBytes = 256ll << 20;
-
-template <int PAST>
-__device__ __forceinline__ u32x4 load16(const u32x4* p) { return PAST > 1 ? __builtin_nontemporal_load(p) : *p; }
-template <int PAST>
-__device__ __forceinline__ void store16(const u32x4& v, u32x4* p) {
-  if (PAST > 0) __builtin_nontemporal_store(v, p);
-  else *p = v;
-}
 
 template <bool F16, bool GRAD, int PAST>
 __global__ __launch_bounds__(256) void silu_mul_kernel(const u32x4* G, const u32x4* dh, long long n, int chunks,
