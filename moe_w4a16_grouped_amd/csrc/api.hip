@@ -1777,6 +1777,8 @@ moe_status_t run_few(const uint16_t* x, const float* router_logits, int32_t T, i
   if (!few_dims_ok(H, I))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H=%d and I=%d must be positive multiples of 16, <= %d and %d", who, H, I,
                 (int)kFewElems, MOE_I8_MAX_K);
+  if (!ragged_ffn_weights_ok(H, I, i8))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: one expert's gate_up weights must stay below 4 GiB", who);
   if (T == 0) return ok();
   if (!x || !router_logits || !w13 || !w2 || (i8 && (!w13_s || !w2_s)) || !y || !workspace)
     return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -1793,7 +1795,7 @@ moe_status_t run_few(const uint16_t* x, const float* router_logits, int32_t T, i
   for (int32_t t = 0; t < T; t += group) {
     const moe::FewArgs a{x + (size_t)t * H, router_logits + (size_t)t * E, std::min(group, T - t), H, I, E, k, w13, w13_s, w2, w2_s,
                          reinterpret_cast<uint16_t*>(ws + L.h), reinterpret_cast<int32_t*>(ws + L.table), ids + t * k, w + t * k,
-                         y + (size_t)t * H, 1};
+                         y + (size_t)t * H};
     const hipError_t e = moe::launch_ffn_few(a, i8, s);
     if (e != hipSuccess) return hip_status(e, who);
   }

@@ -35,192 +35,224 @@ __device__ __forceinline__ bf16x8 i8x8_to_bf16(uint32_t a, uint32_t b) {
   bf16x8 r;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    r[j] = (__bf16)(float)(int8_t)(a >> (8 * j));
-    r[4 + j] = (__bf16)(float)(int8_t)(b >> (8 * j));
+    r[j] = (__bf16)(float)(int)__builtin_amdgcn_sbfe((int)a, 8 * j, 8);
+    r[4 + j] = (__bf16)(float)(int)__builtin_amdgcn_sbfe((int)b, 8 * j, 8);
   }
   return r;
 }
 
-// A lane's 16 bytes of a weight row: PARTS operands of the matrix instruction, 8 elements each; STEP elements of the
-// contraction in all four quarters of the wave.
+// A lane's 16 bytes of a weight row: PARTS operands of the matrix instruction, 8 elements each; LANE elements in all.
 struct FewW16 {
-  static constexpr int PARTS = 1, STEP = 32, BYTES = 2;
+  static constexpr int PARTS = 1, LANE = 8, BYTES = 2;
   static constexpr bool SCALED = false;
   __device__ static __forceinline__ bf16x8 part(const u32x4& w, int) { return __builtin_bit_cast(bf16x8, w); }
 };
 struct FewW8 {
-  static constexpr int PARTS = 2, STEP = 64, BYTES = 1;
+  static constexpr int PARTS = 2, LANE = 16, BYTES = 1;
   static constexpr bool SCALED = true;
   __device__ static __forceinline__ bf16x8 part(const u32x4& w, int i) { return i8x8_to_bf16(w[2 * i], w[2 * i + 1]); }
 };
 
+// 16 bytes at an offset of a buffer; past its end zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t few_buffer(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00027000);
+}
+__device__ __forceinline__ u32x4 few_load(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)offset, 0, 0));
+}
+__device__ __forceinline__ u32x4 few_keep(const u32x4& v, bool in) {
+  return u32x4{in ? v[0] : 0u, in ? v[1] : 0u, in ? v[2] : 0u, in ? v[3] : 0u};
+}
+
 // An expert and at most 8 of its rows (flat slots t * k + s), as the second launch takes them.
 struct FewEntry {
   int32_t expert, rows;
-  int16_t row[8];  // past `rows` the last one again
+  int16_t row[8];
   int32_t pad[2];
 };
 static_assert(sizeof(FewEntry) == 32, "two 16-byte loads");
 
+// The largest value of a wave, on the scalar side (row shifts, then the rows' last lanes broadcast: lane 63 has seen all).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_max_u32(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROWS, 0xF, false));
+}
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));
-  auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = max(a[0], a[1]);
-  auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return max(b[0], b[1]);
+  v = dpp_max_u32<0x111, 0xF>(v);
+  v = dpp_max_u32<0x112, 0xF>(v);
+  v = dpp_max_u32<0x114, 0xF>(v);
+  v = dpp_max_u32<0x118, 0xF>(v);
+  v = dpp_max_u32<0x142, 0xA>(v);
+  v = dpp_max_u32<0x143, 0xC>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// The k largest logits of a token by one wave, one after the other (equal ones by lower id): lane s gets slot s's id and
-// weight.  u: the lane's keys, 0 where there is no expert (and, from here on, where it has been taken).
+// The k largest logits of NT tokens by one wave, one after the other (equal ones by lower id): lane s gets slot s's id and
+// key.  u: the lane's keys, experts lane * NJ + j, 0 where there is none (and, from here on, where it has been taken).  The
+// lowest lane that holds the largest key holds the lowest id of it, so one ballot finds the slot's expert.  Many waves of a
+// compute unit do this at once, so instructions count as well as the chain: a radix select with compaction and ranking, as
+// larger batches use it, is about twice as long.  chosen: lane w's bits of experts 32w .. 32w + 31, of all NT tokens.
 template <int NT, int NJ, int MOST>
-__device__ __forceinline__ void few_route(uint32_t (&u)[MOST][NJ], int k, int (&id)[MOST], float (&weight)[MOST]) {
+__device__ __forceinline__ void few_route(uint32_t (&u)[MOST][NJ], int k, int (&id)[MOST], uint32_t (&key)[MOST], uint32_t& chosen) {
   const int lane = threadIdx.x & 63;
-  float logit[NT];
-#pragma unroll
-  for (int a = 0; a < NT; ++a) id[a] = 0, logit[a] = 0.f;
   for (int s = 0; s < k; ++s) {
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
-      uint32_t m = u[a][0];
+      uint32_t top = u[a][0];
 #pragma unroll
-      for (int j = 1; j < NJ; ++j) m = max(m, u[a][j]);
-      m = __builtin_amdgcn_readfirstlane(wave_max_u32(m));
-      int best = 0;
+      for (int j = 1; j < NJ; ++j) top = max(top, u[a][j]);
+      const uint32_t m = wave_max_u32(top);
+      const int owner = (int)__builtin_ctzll(__ballot(top == m));
+      int at = NJ - 1;
 #pragma unroll
-      for (int j = NJ - 1; j >= 0; --j) {
-        const uint64_t b = __ballot(u[a][j] == m);
-        if (b) best = 64 * j + (int)__builtin_ctzll(b);
-      }
+      for (int j = NJ - 2; j >= 0; --j) at = u[a][j] == m ? j : at;
+      const int best = __builtin_amdgcn_readlane(at, owner);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (lane + 64 * j == best) u[a][j] = 0u;
-      if (lane == s) id[a] = best, logit[a] = from_ordered_bits(m);
+      for (int j = 0; j < NJ; ++j) u[a][j] = lane == owner && best == j ? 0u : u[a][j];
+      const int e = owner * NJ + best;
+      if (MOST > 1 || NT > 1) chosen |= lane == e >> 5 ? 1u << (e & 31) : 0u;
+      id[a] = lane == s ? e : id[a];
+      key[a] = lane == s ? m : key[a];
     }
   }
-#pragma unroll
-  for (int a = 0; a < NT; ++a) {
-    const float top = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(logit[a])));
-    const float p = expf(logit[a] - top);
-    float sum = 0.f;
-    for (int s = 0; s < k; ++s) sum += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p), s));
-    weight[a] = p / sum;
-  }
+}
+
+// Slot weights from the slots' logits (lane s: slot s), added in the order of the slots as moe_route_topk adds them.
+__device__ __forceinline__ float few_weight(float logit, int k) {
+  const float top = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(logit)));
+  const float p = expf(logit - top);
+  float sum = 0.f;
+  for (int s = 0; s < k; ++s) sum += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p), s));
+  return p / sum;
 }
 
 // LDS of the first launch; the tokens stand behind it, 16 bytes apart in the banks.
 struct FewLds {
   f32x4 part[2][kFewWaves][64];
-  u32x4 zero;
-  uint32_t mask[MOE_MAX_EXPERTS / 32];
+  u32x4 zero[2];
+  uint32_t mask[kFewWaves][MOE_MAX_EXPERTS / 32];  // the experts that a wave's tokens chose
   int32_t ids[kFewSlots];
+  uint32_t keys[kFewSlots];
   int32_t list[kFewSlots];                    // the chosen experts, ascending
   int16_t slot[kFewSlots][kFewTokens];        // a chosen expert's slot of each token, or -1
   int32_t more;
 };
 
-template <class W, int NJ>
+// ONE: a single token.
+template <class W, int NJ, bool ONE>
 __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) {
   extern __shared__ u32x4 few_lds[];
   FewLds& s = *reinterpret_cast<FewLds*>(few_lds);
   char* xs = reinterpret_cast<char*>(few_lds) + (sizeof(FewLds) + 15) / 16 * 16;
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int T = p.T, H = p.H, I = p.I, E = p.E, k = p.k, R = T * k;
+  const int T = ONE ? 1 : p.T, H = p.H, I = p.I, E = p.E, k = p.k, R = T * k;
   const bool writer = blockIdx.x == gridDim.x - 1;
   const int xstride = 2 * H + 16;
 
   // the logits of this wave's tokens, then the tokens
-  constexpr int NT = kFewTokens / kFewWaves;
+  constexpr int NT = ONE ? 1 : kFewTokens / kFewWaves;
   uint32_t u[NT][NJ];
 #pragma unroll
   for (int a = 0; a < NT; ++a) {
     const int t = wave + a * kFewWaves;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int e = lane + 64 * j;
+      const int e = lane * NJ + j;
       u[a][j] = t < T && e < E ? max(ordered_bits(p.logits[(size_t)t * E + e]), 1u) : 0u;
     }
   }
-  constexpr int kAhead = 4;
-  const int xn = H / 8, xtotal = T * xn;
+  // a token's row by one wave, or by 2, 4 or 8 where there are fewer tokens: 8 chunks a lane at a time, of two rows 4 each
+  constexpr int kAhead = 8;
+  const int spread = T == 1 ? 3 : (T == 2 ? 2 : (T <= 4 ? 1 : 0)), xn = H / 8;
+  const int xt = wave >> spread, xc = (wave & ((1 << spread) - 1)) * 64 + lane, xstep = 64 << spread;
+  const bool two = !ONE && T > kFewWaves;
+  const u32x4* x = reinterpret_cast<const u32x4*>(p.x);
   u32x4 xr[kAhead];
+  auto fetch = [&](int from) {
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    const int c = tid + i * 64 * kFewWaves;
-    if (c < xtotal) xr[i] = reinterpret_cast<const u32x4*>(p.x)[c];
-  }
-  if (tid < MOE_MAX_EXPERTS / 32) s.mask[tid] = 0u;
-  if (tid == 0) s.zero = u32x4{0u, 0u, 0u, 0u}, s.more = 0;
-  for (int i = tid; i < kFewSlots * kFewTokens / 8; i += 64 * kFewWaves)
-    reinterpret_cast<u32x4*>(s.slot)[i] = u32x4{~0u, ~0u, ~0u, ~0u};
+    for (int i = 0; i < kAhead; ++i) {
+      const int t = xt + (two ? i / 4 * kFewWaves : 0), c = xc + (from + (two ? i % 4 : i)) * xstep;
+      if (t < T && c < xn) xr[i] = x[t * xn + c];
+    }
+  };
+  auto put = [&](int from) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int t = xt + (two ? i / 4 * kFewWaves : 0), c = xc + (from + (two ? i % 4 : i)) * xstep;
+      if (t < T && c < xn) *reinterpret_cast<u32x4*>(xs + t * xstride + c * 16) = xr[i];
+    }
+  };
+  fetch(0);
+  if (tid == 0) s.zero[0] = s.zero[1] = u32x4{0u, 0u, 0u, 0u}, s.more = 0;
+  for (int i = tid; i < R * (kFewTokens / 8); i += 64 * kFewWaves) reinterpret_cast<u32x4*>(s.slot)[i] = u32x4{~0u, ~0u, ~0u, ~0u};
+  int id[NT] = {};
+  uint32_t key[NT] = {}, chosen = 0u;
   if (wave < T) {
-    int id[NT] = {};
-    float weight[NT] = {};
-    if (T <= kFewWaves) few_route<1>(u, k, id, weight);
-    else few_route<NT>(u, k, id, weight);
+    if (!ONE && wave + kFewWaves < T) few_route<NT>(u, k, id, key, chosen);
+    else few_route<1>(u, k, id, key, chosen);
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
-      const int t = wave + a * kFewWaves;
-      if (t < T && lane < k) {
-        s.ids[t * k + lane] = id[a];
-        if (writer) {
-          p.ids[t * k + lane] = id[a];
-          p.weight[t * k + lane] = weight[a];
-        }
-      }
+      const int f = (wave + a * kFewWaves) * k + lane;
+      if (wave + a * kFewWaves < T && lane < k) s.ids[f] = id[a], s.keys[f] = key[a];
     }
   }
-  auto put = [&](int c, const u32x4& v) {
-    const int t = c / xn;
-    *reinterpret_cast<u32x4*>(xs + t * xstride + (c - t * xn) * 16) = v;
-  };
+  if (!ONE && lane < MOE_MAX_EXPERTS / 32) s.mask[wave][lane] = chosen;
+  put(0);
+  for (int from = two ? kAhead / 2 : kAhead; from * xstep < xn; from += two ? kAhead / 2 : kAhead) {
+    fetch(from);
+    put(from);
+  }
+  __syncthreads();
+  int n = k;  // chosen experts
+  if (!ONE) {  // each wave adds up the experts before every word of the mask, and a slot's thread finds its expert's rank
+    uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    const int c = tid + i * 64 * kFewWaves;
-    if (c < xtotal) put(c, xr[i]);
-  }
-  for (int c = tid + kAhead * 64 * kFewWaves; c < xtotal; c += 64 * kFewWaves) put(c, reinterpret_cast<const u32x4*>(p.x)[c]);
-  __syncthreads();
-  if (tid < R) atomicOr(&s.mask[s.ids[tid] >> 5], 1u << (s.ids[tid] & 31));
-  __syncthreads();
-  int n = 0;  // chosen experts
-  {
-    const int e = tid < R ? s.ids[tid] : 0;
-    int rank = 0;
-    for (int w = 0; w < (E + 31) / 32; ++w) {
-      const uint32_t m = s.mask[w];
-      n += __popc(m);
-      rank += __popc(w < (e >> 5) ? m : (w == (e >> 5) ? m & ((1u << (e & 31)) - 1u) : 0u));
+    for (int w = 0; w < kFewWaves; ++w) m |= s.mask[w][lane & (MOE_MAX_EXPERTS / 32 - 1)];
+    if (lane >= MOE_MAX_EXPERTS / 32) m = 0u;
+    int before = __popc(m);
+#pragma unroll
+    for (int d = 1; d < MOE_MAX_EXPERTS / 32; d <<= 1) {
+      const int v = __shfl_up(before, d);
+      if (lane >= d) before += v;
     }
+    n = __builtin_amdgcn_readlane(before, MOE_MAX_EXPERTS / 32 - 1);
+    before -= __popc(m);
+    const int e = s.ids[min(tid, R - 1)];
+    const int rank = __shfl(before, e >> 5) + __popc(__shfl((int)m, e >> 5) & ((1u << (e & 31)) - 1u));
     if (tid < R) {
       s.list[rank] = e;
       s.slot[rank][tid / k] = (int16_t)tid;
     }
+    __syncthreads();
   }
-  n = __builtin_amdgcn_readfirstlane(n);
-  __syncthreads();
+  const int32_t* list = ONE ? s.ids : s.list;
 
-  if (writer) {  // the entries: an expert's first 8 rows at its rank, a second 8 behind the experts
+  if (writer) {  // the routing, and the entries: an expert's first rows at its rank, further ones behind the experts
+    for (int t = wave; t < T; t += kFewWaves) {
+      const int f = t * k + min(lane, k - 1);
+      const float w = few_weight(from_ordered_bits(s.keys[f]), k);
+      if (lane < k) {
+        p.ids[f] = s.ids[f];
+        p.weight[f] = w;
+      }
+    }
     FewEntry* table = reinterpret_cast<FewEntry*>(p.table) + 1;
     if (tid < n) {
       FewEntry* at = table + tid;
       int have = 0;
       for (int t = 0; t < T; ++t) {
-        const int f = s.slot[tid][t];
+        const int f = ONE ? tid : s.slot[tid][t];
         if (f < 0) continue;
-        if (have == 8) {
-          at->expert = s.list[tid];
-          at->rows = 8;
+        if (have == p.entry_rows) {
+          at->expert = list[tid];
+          at->rows = have;
           at = table + n + atomicAdd(&s.more, 1);
           have = 0;
         }
-        for (int j = have; j < 8; ++j) at->row[j] = (int16_t)f;
-        ++have;
+        at->row[have++] = (int16_t)f;
       }
-      at->expert = s.list[tid];
+      at->expert = list[tid];
       at->rows = have;
     }
     __syncthreads();
@@ -228,38 +260,42 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
   }
 
   // this wave's share of the contraction, in chunks of C steps
-  constexpr int C = 4, RING = 2, LANE = W::STEP / 4;
-  const int steps = (H + W::STEP - 1) / W::STEP, share = (steps + kFewWaves - 1) / kFewWaves;
-  const int chunks = (share + C - 1) / C, blocks = I / 8, tasks = n * blocks;
-  const int k0 = wave * share * W::STEP + q * LANE;
-  const int wrow = l16 < 8 ? l16 : I + l16 - 8;
-  const char* xrow = xs + min(l16, T - 1) * xstride;
+  constexpr int C = 4, RING = 2, STEP = 4 * W::LANE;
+  const int steps = (H + STEP - 1) / STEP, share = (steps + kFewWaves - 1) / kFewWaves;
+  const int chunks = (share + C - 1) / C, blocks = I / 8;
+  const int first = wave * share * STEP;                       // of the contraction
+  const int whole = max(0, min(share, (H - first) / STEP)) / C;  // chunks that lie within the share and the row
+  const uint32_t row_bytes = (uint32_t)H * W::BYTES;
+  const uint32_t lane_offset = (uint32_t)(l16 < 8 ? l16 : I + l16 - 8) * row_bytes + (first + q * W::LANE) * W::BYTES;
+  const char* xrow = xs + min(l16, T - 1) * xstride + (first + q * W::LANE) * 2;
   struct Cursor {
-    int task, chunk;
+    int rank, block, chunk;
   };
+  const int rank_step = gridDim.x / blocks, block_step = gridDim.x - rank_step * blocks;
   auto advance = [&](Cursor& c) {
-    if (++c.chunk == chunks) c.chunk = 0, c.task += gridDim.x;
+    if (++c.chunk < chunks) return;
+    c.chunk = 0;
+    c.rank += rank_step;
+    c.block += block_step;
+    if (c.block >= blocks) c.block -= blocks, ++c.rank;
   };
   u32x4 ring[RING][C];
   float sg[RING], su[RING];  // scales of the column that this thread finishes
-  auto valid = [&](int chunk, int i) { return chunk * C + i < share && k0 + (chunk * C + i) * W::STEP < H; };
+  const uint32_t expert_bytes = (uint32_t)(2 * I) * row_bytes;
   auto load = [&](const Cursor& c, int b) {
-    if (c.task >= tasks) return;
-    const int rank = c.task / blocks, block = c.task - rank * blocks;
-    const int e = __builtin_amdgcn_readfirstlane(s.list[rank]);
-    const char* row = static_cast<const char*>(p.w13) + ((size_t)e * (2 * I) + block * 8 + wrow) * (size_t)H * W::BYTES;
+    if (c.rank >= n) return;
+    const int e = __builtin_amdgcn_readfirstlane(list[c.rank]);
+    const auto buffer = few_buffer(static_cast<const char*>(p.w13) + (size_t)e * expert_bytes, expert_bytes);
+    const uint32_t offset = lane_offset + (uint32_t)c.block * 8 * row_bytes + c.chunk * (C * STEP * W::BYTES);
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int at = min(k0 + (c.chunk * C + i) * W::STEP, H - LANE);
-      ring[b][i] = *reinterpret_cast<const u32x4*>(row + (size_t)at * W::BYTES);
-    }
-    if (W::SCALED && tid < 8 * kFewTokens) {
-      const float* sc = p.w13_s + (size_t)e * (2 * I) + block * 8 + (tid & 7);
+    for (int i = 0; i < C; ++i) ring[b][i] = few_load(buffer, offset + i * (STEP * W::BYTES));
+    if (W::SCALED && c.chunk == chunks - 1 && tid < 8 * kFewTokens) {
+      const float* sc = p.w13_s + (size_t)e * (2 * I) + c.block * 8 + (tid & 7);
       sg[b] = sc[0];
       su[b] = sc[I];
     }
   };
-  Cursor use = {(int)blockIdx.x, 0}, ahead = use;
+  Cursor use = {(int)blockIdx.x / blocks, (int)blockIdx.x % blocks, 0}, ahead = use;
 #pragma unroll
   for (int b = 0; b < RING; ++b) {
     load(ahead, b);
@@ -267,202 +303,299 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
   }
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   int turn = 0;
-  while (use.task < tasks) {
+  for (;;) {
 #pragma unroll
     for (int b = 0; b < RING; ++b) {
-      if (use.task < tasks) {
+      if (use.rank >= n) return;
+      const char* xk = xrow + use.chunk * (C * STEP * 2);
+      if (use.chunk < whole) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int h = 0; h < W::PARTS; ++h)
+            acc = mfma16x16x32(W::part(ring[b][i], h), *reinterpret_cast<const bf16x8*>(xk + i * (STEP * 2) + 16 * h), acc);
+      } else {  // weights and tokens past the share or the row count as zeros
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-          const bool in = valid(use.chunk, i);
-          u32x4 w = ring[b][i];
+          const int step = use.chunk * C + i;
+          const bool in = step < share && first + step * STEP + q * W::LANE < H;
+          const u32x4 w = few_keep(ring[b][i], in);
+          const char* xi = in ? xk + i * (STEP * 2) : reinterpret_cast<const char*>(s.zero);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = in ? w[j] : 0u;
-          const char* xk = in ? xrow + (k0 + (use.chunk * C + i) * W::STEP) * 2 : reinterpret_cast<const char*>(&s.zero);
-#pragma unroll
-          for (int h = 0; h < W::PARTS; ++h) {
-            const bf16x8 xv = *reinterpret_cast<const bf16x8*>(in ? xk + 16 * h : xk);
-            acc = mfma16x16x32(W::part(w, h), xv, acc);
-          }
+          for (int h = 0; h < W::PARTS; ++h)
+            acc = mfma16x16x32(W::part(w, h), *reinterpret_cast<const bf16x8*>(xi + 16 * h), acc);
         }
-        const float scale_g = sg[b], scale_u = su[b];
-        load(ahead, b);
-        advance(ahead);
-        if (use.chunk == chunks - 1) {
-          s.part[turn][wave][lane] = acc;
-          acc = f32x4{0.f, 0.f, 0.f, 0.f};
-          __syncthreads();  // one a task: this half of part is written again only past the next task's barrier
-          if (tid < 8 * kFewTokens) {
-            const int c = tid & 7, t = tid >> 3;
-            const int rank = use.task / blocks, block = use.task - rank * blocks;
-            const int f = s.slot[rank][t];
-            float g = 0.f, up = 0.f;
-            const int from = (c >> 2) * 16 + t;
-#pragma unroll
-            for (int w = 0; w < kFewWaves; ++w) {
-              g += reinterpret_cast<const float*>(&s.part[turn][w][from])[c & 3];
-              up += reinterpret_cast<const float*>(&s.part[turn][w][from + 32])[c & 3];
-            }
-            if (W::SCALED) g *= scale_g, up *= scale_u;
-            if (f >= 0) {
-              const float h = silu_f32(g) * up;
-              const uint32_t hi = f32_to_bf16_bits(h);
-              const float left = h - bf16_bits_to_f32(hi);
-              uint16_t* dst = p.h + ((size_t)f * blocks + block) * 16 + c;
-              dst[0] = (uint16_t)hi;
-              dst[8] = fabsf(left) < __builtin_inff() ? f32_to_bf16_bits(left) : (uint16_t)0;
-            }
-          }
-          turn ^= 1;
-        }
-        advance(use);
       }
+      const float scale_g = W::SCALED ? sg[b] : 1.f, scale_u = W::SCALED ? su[b] : 1.f;
+      load(ahead, b);
+      advance(ahead);
+      if (use.chunk == chunks - 1) {
+        s.part[turn][wave][lane] = acc;
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        __syncthreads();  // one a task: this half of part is written again only past the next task's barrier
+        if (tid < 8 * kFewTokens) {
+          const int c = tid & 7, t = tid >> 3;
+          const int f = ONE ? (t == 0 ? use.rank : -1) : s.slot[use.rank][t];
+          float g = 0.f, up = 0.f;
+          const int from = (c >> 2) * 16 + t;
+#pragma unroll
+          for (int w = 0; w < kFewWaves; ++w) {
+            g += reinterpret_cast<const float*>(&s.part[turn][w][from])[c & 3];
+            up += reinterpret_cast<const float*>(&s.part[turn][w][from + 32])[c & 3];
+          }
+          if (W::SCALED) g *= scale_g, up *= scale_u;
+          if (f >= 0) {
+            const float h = silu_f32(g) * up;
+            const uint32_t hi = f32_to_bf16_bits(h);
+            const float left = h - bf16_bits_to_f32(hi);
+            uint16_t* dst = p.h + ((size_t)f * blocks + use.block) * 16 + c;
+            dst[0] = (uint16_t)hi;
+            dst[8] = fabsf(left) < __builtin_inff() ? f32_to_bf16_bits(left) : (uint16_t)0;
+          }
+        }
+        turn ^= 1;
+      }
+      advance(use);
     }
   }
 }
 
-template <class W>
-__global__ __launch_bounds__(64 * kFewWaves) void few_down_kernel(FewArgs p) {
-  __shared__ FewEntry table[kFewSlots];
-  __shared__ __attribute__((aligned(16))) float out[kFewSlots][8];
-  __shared__ float weight[kFewSlots];
+// The second launch: 8 columns of y a workgroup.  A wave takes units, an entry and every pieces-th super-chunk of SUPER elements of
+// the contraction, from a place of its own on (workgroups in step would ask the same few memory channels).  The 8 lanes (four quarters, two halves) of a row of weights read 128 bytes in a row of it; what the halves
+// take apart of the contraction they add at the end.  The entry's rows of h come as whole lines, one load a row and
+// super-chunk, and reach the lanes that need them through the wave's own LDS: as operands straight from memory they would be
+// fetched 4 to 16 times over, which the L1s do not give beside the weights.
+template <class W, int CT, int SUPER, int TOK, int RING, int NW>
+__global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
+  constexpr int kHRow = SUPER * 4 + 16, HB = SUPER / 256;  // a row of h in LDS, and its 1 KB loads
+  extern __shared__ u32x4 few_lds[];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int T = p.T, H = p.H, I = p.I, k = p.k, R = T * k;
-  const int col0 = blockIdx.x * 8;
-  const int n = p.table[0];
+  const int T = p.T, H = p.H, I = p.I, k = p.k, R = T * k, shift = p.pieces_shift;
+  char* stage = reinterpret_cast<char*>(few_lds) + wave * (TOK * kHRow);
+  FewEntry* table = reinterpret_cast<FewEntry*>(reinterpret_cast<char*>(few_lds) + NW * TOK * kHRow);
+  float* weight = reinterpret_cast<float*>(table + R);
+  f32x4* out = reinterpret_cast<f32x4*>(weight + (R + 3) / 4 * 4);  // [pieces][R][2 * CT]: 8 * CT columns
+  const int col0 = blockIdx.x * (8 * CT);
+  const int n = __builtin_amdgcn_readfirstlane(p.table[0]);
   if (tid < 2 * R) reinterpret_cast<u32x4*>(table)[tid] = reinterpret_cast<const u32x4*>(p.table)[2 + tid];
   if (tid < R) weight[tid] = p.weight[tid];
   __syncthreads();
 
-  // units: an entry and a piece of the contraction; a piece is two halves of `share` steps
-  constexpr int C = W::PARTS == 1 ? 4 : 2, RING = 2, LANE = W::STEP / 4;
-  const int pieces = p.pieces, units = n * pieces;
-  const int steps = (I + W::STEP - 1) / W::STEP, share = (steps + 2 * pieces - 1) / (2 * pieces), chunks = (share + C - 1) / C;
-  const int half = l16 >> 3, m = l16 & 7;
+  constexpr int C = SUPER / 8 / W::LANE;  // steps of a super-chunk
+  const int pieces = 1 << shift, units = n << shift;
+  const int supers = (I + SUPER - 1) / SUPER;
+  const bool ragged = I % SUPER != 0;
+  const int m = l16 & 7, eighth = q * 2 + (l16 >> 3);
+  const uint32_t row_bytes = (uint32_t)I * W::BYTES;
+  const uint32_t lane_offset = (uint32_t)m * row_bytes + eighth * 16;
+  const char* hfrag = stage + min(m, TOK - 1) * kHRow + eighth * (W::PARTS * 32);
   struct Cursor {
-    int unit, chunk;
+    int unit, super, left;
+  };
+  const int turn = (blockIdx.x >> 3) % (supers >> shift);
+  auto begin = [&](int unit) {
+    const int piece = unit & (pieces - 1);
+    return Cursor{unit, piece + (turn << shift), (supers - piece + pieces - 1) >> shift};
   };
   auto advance = [&](Cursor& c) {
-    if (++c.chunk == chunks) c.chunk = 0, c.unit += kFewWaves;
+    if (--c.left == 0) {
+      c = begin(c.unit + NW);
+      return;
+    }
+    c.super += pieces;
+    if (c.super >= supers) c.super = c.unit & (pieces - 1);
   };
-  u32x4 ring[RING][C], hv[RING][C][2 * W::PARTS];
-  float sc[RING][4];
-  auto start = [&](const Cursor& c, int piece) { return ((piece * 2 + half) * share + c.chunk * C) * W::STEP + q * LANE; };
+  u32x4 ring[RING][CT][C], hv[RING][TOK][HB];
+  f32x4 sc[RING][CT];
+  const uint32_t expert_bytes = (uint32_t)H * row_bytes;
+  // lane i holds what the wave's i-th unit needs (there are at most 64), so that no unit waits for LDS
+  const FewEntry& own = table[min((wave + NW * lane) >> shift, n - 1)];
+  const int own_expert = own.expert, own_rows = own.rows;
+  uint32_t own_row[(TOK + 1) / 2];
+#pragma unroll
+  for (int j = 0; j < (TOK + 1) / 2; ++j) own_row[j] = reinterpret_cast<const uint32_t*>(own.row)[j];
+  auto row_of = [&](int i, int j) { return (__builtin_amdgcn_readlane(own_row[j >> 1], i) >> (16 * (j & 1))) & 0xFFFFu; };
   auto load = [&](const Cursor& c, int b) {
     if (c.unit >= units) return;
-    const int entry = c.unit / pieces, piece = c.unit - entry * pieces;
-    const int e = __builtin_amdgcn_readfirstlane(table[entry].expert);
-    const char* row = static_cast<const char*>(p.w2) + ((size_t)e * H + col0 + m) * (size_t)I * W::BYTES;
-    const uint16_t* hrow = p.h + (size_t)table[entry].row[m] * I * 2;
-    const int k0 = start(c, piece);
+    const int i = c.unit / NW;
+    const int e = __builtin_amdgcn_readlane(own_expert, i), rows = __builtin_amdgcn_readlane(own_rows, i);
+    const auto buffer = few_buffer(static_cast<const char*>(p.w2) + (size_t)e * expert_bytes, expert_bytes);
+    const uint32_t offset = lane_offset + (uint32_t)col0 * row_bytes + c.super * (SUPER * W::BYTES);
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int at = min(k0 + i * W::STEP, I - LANE);
-      ring[b][i] = *reinterpret_cast<const u32x4*>(row + (size_t)at * W::BYTES);
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int h = 0; h < 2 * W::PARTS; ++h) hv[b][i][h] = *reinterpret_cast<const u32x4*>(hrow + at * 2 + 8 * h);
-    }
-    if (W::SCALED) {
+      for (int i = 0; i < C; ++i) ring[b][ct][i] = few_load(buffer, offset + ct * 8 * row_bytes + i * 128);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sc[b][r] = p.w2_s[(size_t)e * H + col0 + 4 * (q & 1) + r];
+    for (int j = 0; j < TOK; ++j)
+      if (j < rows) {
+        const auto hrow = few_buffer(p.h + (size_t)row_of(i, j) * I * 2, (uint32_t)I * 4);
+#pragma unroll
+        for (int v = 0; v < HB; ++v) hv[b][j][v] = few_load(hrow, lane * 16 + c.super * (SUPER * 4) + v * 1024);
+      }
+    if (W::SCALED && c.left == 1) {
+      const auto scales = few_buffer(p.w2_s + (size_t)e * H, (uint32_t)H * 4);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) sc[b][ct] = __builtin_bit_cast(f32x4, few_load(scales, (col0 + ct * 8 + 4 * (q & 1)) * 4));
     }
   };
-  Cursor use = {wave, 0}, ahead = use;
+  Cursor use = begin(wave), ahead = use;
 #pragma unroll
   for (int b = 0; b < RING; ++b) {
     load(ahead, b);
     advance(ahead);
   }
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  while (use.unit < units) {
+  f32x4 acc[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) acc[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (;;) {
 #pragma unroll
     for (int b = 0; b < RING; ++b) {
-      if (use.unit < units) {
-        const int entry = use.unit / pieces, piece = use.unit - entry * pieces;
-        const int k0 = start(use, piece);
+      if (use.unit >= units) goto summed;
+      const int rows = __builtin_amdgcn_readlane(own_rows, use.unit / NW);
+      const bool last = use.super == supers - 1 && ragged;  // weights past the row count as zeros; h past its end was read so
+      if (last) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-          const bool in = use.chunk * C + i < share && k0 + i * W::STEP < I;
-          u32x4 w = ring[b][i];
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = in ? w[j] : 0u;
+          for (int i = 0; i < C; ++i) ring[b][ct][i] = few_keep(ring[b][ct][i], use.super * SUPER + (i * 8 + eighth) * W::LANE < I);
+      }
 #pragma unroll
-          for (int h = 0; h < W::PARTS; ++h) {
-            const bf16x8 a = W::part(w, h);
+      for (int j = 0; j < TOK; ++j)
+        if (j < rows) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              u32x4 x = hv[b][i][2 * h + v];
+          for (int v = 0; v < HB; ++v) *reinterpret_cast<u32x4*>(stage + j * kHRow + v * 1024 + lane * 16) = hv[b][j][v];
+        }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = in ? x[j] : 0u;
-              acc = mfma16x16x32(a, __builtin_bit_cast(bf16x8, x), acc);
-            }
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int h = 0; h < W::PARTS; ++h) {
+          const char* at = hfrag + i * (W::PARTS * 256) + h * 32;
+          const bf16x8 hi = *reinterpret_cast<const bf16x8*>(at), lo = *reinterpret_cast<const bf16x8*>(at + 16);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const bf16x8 a = W::part(ring[b][ct][i], h);
+            acc[ct] = mfma16x16x32(a, hi, acc[ct]);
+            acc[ct] = mfma16x16x32(a, lo, acc[ct]);
           }
         }
-        float scale[4];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      f32x4 scale[CT];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) scale[r] = W::SCALED ? sc[b][r] : 1.f;
-        load(ahead, b);
-        advance(ahead);
-        if (use.chunk == chunks - 1) {
+      for (int ct = 0; ct < CT; ++ct) scale[ct] = W::SCALED ? sc[b][ct] : f32x4{1.f, 1.f, 1.f, 1.f};
+      load(ahead, b);
+      advance(ahead);
+      if (use.left == 1) {
+        const int f = (use.unit & (pieces - 1)) * R + table[use.unit >> shift].row[l16 & 7];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
           f32x4 o;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            o[r] = acc[r] + __shfl(acc[r], lane + 40);  // rows 8 + of columns 8 +: the other half
-            if (W::SCALED) o[r] *= scale[r];
+            o[r] = acc[ct][r] + __shfl(acc[ct][r], (lane + 40) & 63);  // rows 8 + of columns 8 +: the other half
+            if (W::SCALED) o[r] *= scale[ct][r];
           }
-          if (q < 2 && l16 < 8 && l16 < table[entry].rows)
-            *reinterpret_cast<f32x4*>(&out[piece * R + table[entry].row[l16]][4 * q]) = o;
-          acc = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (q < 2 && l16 < rows) out[(f * CT + ct) * 2 + q] = o;
+          acc[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        advance(use);
       }
+      advance(use);
     }
   }
+summed:
   __syncthreads();
-  if (tid < 8 * T) {
-    const int t = tid >> 3, c = tid & 7;
+  if (tid < 8 * CT * T) {
+    const int t = tid / (8 * CT), c = tid % (8 * CT);
+    const float* o8 = reinterpret_cast<const float*>(out) + c;
     float y = 0.f;
-    for (int s = 0; s < k; ++s) {
-      const int f = t * k + s;
-      float o = out[f][c];
-      for (int i = 1; i < pieces; ++i) o += out[i * R + f][c];
-      y = fmaf(weight[f], o, y);
+    for (int s = 0; s < k; s += 4) {  // four slots' values are asked for at a time; their sum is that of the slots in order
+      float o[4], w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int f = t * k + min(s + j, k - 1);
+        w[j] = weight[f];
+        o[j] = o8[f * (8 * CT)];
+        for (int i = 1; i < pieces; ++i) o[j] += o8[(i * R + f) * (8 * CT)];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (s + j < k) y = fmaf(w[j], o[j], y);
     }
     p.y[(size_t)t * H + col0 + c] = f32_to_bf16_bits(y);
   }
 }
 
-// Pieces of the contraction that a second launch's units are cut into, so that the eight waves of a workgroup have one each
-// even where a single token chose fewer experts.  pieces * T * k <= kFewSlots.
-static int few_pieces(int k) { return k >= kFewWaves ? 1 : (kFewWaves + k - 1) / k; }
+// Pieces (a power of two) of the contraction that a second launch's units are cut into, so that the waves of a workgroup have
+// one each even where a single token chose fewer experts; no more than there are super-chunks.  At most 64 units a wave.
+static int few_pieces_shift(int k, int I, int super, int waves) {
+  const int supers = (I + super - 1) / super;
+  int shift = 0;
+  while ((k << shift) < waves && (2 << shift) <= supers && shift < 3) ++shift;
+  return shift;
+}
 
-template <class W, int NJ>
-static hipError_t launch_few_of(const FewArgs& p, hipStream_t s) {
+template <class W, int NJ, bool ONE>
+static hipError_t launch_few_first(const FewArgs& p, hipStream_t s) {
   const int lds = (int)((sizeof(FewLds) + 15) / 16 * 16) + p.T * (2 * p.H + 16);
-  const int most = std::max(1, std::min(3, (160 << 10) / lds));  // workgroups a CU
-  const int tasks = std::min(p.E, p.T * p.k) * (p.I / 8);
-  const int grid = std::min(tasks, 256 * most);
+  // Workgroups a CU: of one token three, which then have a piece of the largest of its layers each; of more two, as every
+  // workgroup routes all of them (11 tokens, 60 experts top-6, 1040 x 336 int8: 27.3 us with two, 29.6 with three).
+  const int fit = std::max(1, std::min(ONE ? 3 : 2, (160 << 10) / lds));
+  const int grid = std::min(std::min(p.E, p.T * p.k) * (p.I / 8), 256 * fit);
   if (lds > (64 << 10)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(few_gate_up_kernel<W, NJ>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(few_gate_up_kernel<W, NJ, ONE>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  few_gate_up_kernel<W, NJ><<<grid, 64 * kFewWaves, lds, s>>>(p);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  few_down_kernel<W><<<p.H / 8, 64 * kFewWaves, 0, s>>>(p);
+  few_gate_up_kernel<W, NJ, ONE><<<grid, 64 * kFewWaves, lds, s>>>(p);
+  return hipGetLastError();
+}
+
+template <class W, int NJ>
+static hipError_t launch_few_of(const FewArgs& p, hipStream_t s) {
+  return p.T == 1 ? launch_few_first<W, NJ, true>(p, s) : launch_few_first<W, NJ, false>(p, s);
+}
+
+template <class W, int CT, int SUPER, int TOK, int RING, int NW>
+static hipError_t launch_few_second(FewArgs p, hipStream_t s) {
+  p.pieces_shift = few_pieces_shift(p.k, p.I, SUPER, NW);
+  const int R = p.T * p.k, lds = NW * TOK * (SUPER * 4 + 16) + R * 32 + (R + 3) / 4 * 16 + (R << p.pieces_shift) * 32 * CT;
+  const auto kernel = few_down_kernel<W, CT, SUPER, TOK, RING, NW>;
+  if (lds > (64 << 10)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  kernel<<<p.H / (8 * CT), 64 * NW, lds, s>>>(p);
   return hipGetLastError();
 }
 
 template <class W>
-static hipError_t launch_few_w(const FewArgs& p, hipStream_t s) {
-  if (p.E <= 128) return launch_few_of<W, 2>(p, s);
-  if (p.E <= 256) return launch_few_of<W, 4>(p, s);
-  if (p.E <= 512) return launch_few_of<W, 8>(p, s);
-  return launch_few_of<W, 16>(p, s);
+static hipError_t launch_few_w(FewArgs p, hipStream_t s) {
+  // rows of an entry: more where the experts are crowded, so that their weights are read once
+  const bool crowded = p.T * p.k > 2 * p.E;
+  p.entry_rows = p.T == 1 ? 1 : (crowded ? 8 : 4);
+  hipError_t e;
+  if (p.E <= 128) e = launch_few_of<W, 2>(p, s);
+  else if (p.E <= 256) e = launch_few_of<W, 4>(p, s);
+  else if (p.E <= 512) e = launch_few_of<W, 8>(p, s);
+  else e = launch_few_of<W, 16>(p, s);
+  if (e != hipSuccess) return e;
+  if (p.T == 1) return launch_few_second<W, 1, 256, 1, 3, 8>(p, s);
+  if (crowded) {
+    // 16 columns a workgroup halve the traffic of h, but want enough workgroups (16 tokens, 8 experts of 4096 x 14336: 167 us
+    // against 190; 2048 columns: 44 us against 30)
+    if (p.H >= 4096) return launch_few_second<W, 2, 256, 8, 2, 8>(p, s);
+    return launch_few_second<W, 1, 256, 8, 2, 8>(p, s);
+  }
+  // int8 units are half as long in bytes and convert their weights: twice the waves (16 tokens, 256 experts top-8, 2048 x 512:
+  // 24 us against 26; bf16, 8 tokens, 128 experts, 2048 x 768: 32 us against 31, so not there)
+  if (W::SCALED) return launch_few_second<W, 1, 256, 4, 2, 16>(p, s);
+  return launch_few_second<W, 1, 256, 4, 3, 8>(p, s);
 }
 
-hipError_t launch_ffn_few(FewArgs p, bool i8, hipStream_t stream) {
-  p.pieces = few_pieces(p.k);
+hipError_t launch_ffn_few(const FewArgs& p, bool i8, hipStream_t stream) {
   return i8 ? launch_few_w<FewW8>(p, stream) : launch_few_w<FewW16>(p, stream);
 }
 

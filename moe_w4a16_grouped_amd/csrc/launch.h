@@ -219,9 +219,10 @@ struct FewArgs {
   int32_t* ids;          // [T, k]
   float* weight;         // [T, k]
   uint16_t* y;           // bf16 [T, H]
-  int pieces;
+  int entry_rows = 0;    // an entry's rows at most, and log2 of the pieces of an entry: set by the launch
+  int pieces_shift = 0;
 };
-hipError_t launch_ffn_few(FewArgs a, bool i8, hipStream_t stream);
+hipError_t launch_ffn_few(const FewArgs& a, bool i8, hipStream_t stream);
 
 // Root-mean-square norm (norm.hip): x, residual (NULL: none), s and y (NULL: none) 16-bit [T, H], w [H].
 struct NormArgs {
