@@ -999,6 +999,14 @@ def moe_ffn_forward_w16(x, router_logits, w13, w2, k: int, y=None, topk_ids_out=
     return y
 
 
+def _made_like(made, x, dtype, name, stream):
+    """The caller's tensor of x's shape, checked, or a new one."""
+    if made is not None:
+        _need(made, (dtype,), tuple(x.shape), name, x.device)
+        return made
+    return torch.empty_like(x, dtype=dtype) if stream is None else _empty(x.shape, dtype, x.device, stream)
+
+
 def moe_rmsnorm_add(x, weight, eps: float, residual=None, quant: int = MOE_QUANT_NONE, want_y: bool = True, s=None, y=None,
                     q=None, q_scale=None, stream=None):
     """x [T, H] bf16 or fp16, weight [H] of its type or fp32, residual [T, H] or None -> (s, y, q, q_scale): s = x +
@@ -1009,27 +1017,19 @@ def moe_rmsnorm_add(x, weight, eps: float, residual=None, quant: int = MOE_QUANT
     _need(weight, (dt, torch.float32), (H,), "weight", dev)
     if residual is not None:
         _need(residual, (dt,), (T, H), "residual", dev)
-        s = _out(s, (T, H), _OUT[dt], dev, "s", stream)
+        s = _made_like(s, x, dt, "s", stream)
     elif s is not None:
         raise ValueError("s is the sum with a residual, and none is given")
     if want_y or y is not None:
-        y = _out(y, (T, H), _OUT[dt], dev, "y", stream)
+        y = _made_like(y, x, dt, "y", stream)
     if quant == MOE_QUANT_NONE:
         if q is not None or q_scale is not None:
             raise ValueError("q and q_scale belong to a quant of MOE_QUANT_I8 or MOE_QUANT_F8")
-    elif quant in (MOE_QUANT_I8, MOE_QUANT_F8):
-        code = _I8 if quant == MOE_QUANT_I8 else _U8
+    elif quant == MOE_QUANT_I8 or quant == MOE_QUANT_F8:
         if quant == MOE_QUANT_F8 and H % 128:
             raise ValueError(f"MOE_QUANT_F8 needs a multiple of 128 columns (got {H})")
-        shape = (T,) if quant == MOE_QUANT_I8 else (T, H // 128)
-        if q is None:
-            q = _empty((T, H), code[0], dev, stream)
-        else:
-            _need(q, code, (T, H), "q", dev)
-        if q_scale is None:
-            q_scale = _empty(shape, torch.float32, dev, stream)
-        else:
-            _need(q_scale, _F32, shape, "q_scale", dev)
+        q = _made_like(q, x, torch.int8 if quant == MOE_QUANT_I8 else torch.uint8, "q", stream)
+        q_scale = _out(q_scale, (T,) if quant == MOE_QUANT_I8 else (T, H // 128), MOE_OUT_F32, dev, "q_scale", stream)
     else:
         raise ValueError(f"unknown quant {quant}")
     _call(load().moe_rmsnorm_add, dev, stream, (s, y, q, q_scale), x.data_ptr(), _ptr(residual), _IN[dt], weight.data_ptr(),
@@ -1052,7 +1052,7 @@ def moe_rmsnorm_add_grad(dy, s, weight, eps: float, ds=None, out_dtype: int = No
     if ds is not None:
         _need(ds, (dt,), (T, H), "ds", dev)
     out_dtype = _OUT[weight.dtype] if out_dtype is None else out_dtype
-    dx = _out(dx, (T, H), _OUT[dt], dev, "dx", stream)
+    dx = _made_like(dx, s, dt, "dx", stream)
     dweight = _out(dweight, (H,), out_dtype, dev, "dweight", stream)
     lib, size = load(), 0
     if workspace is not None:

@@ -20,9 +20,9 @@
 // beside the weights', and y is then rounded once.  Sums are fp32.
 #include <algorithm>
 
-#include "../../include/moe_w4a16.h"
 #include "launch.h"
 #include "moe_common.h"
+#include "moe_w4a16.h"
 #include "topk.h"
 
 namespace moe {

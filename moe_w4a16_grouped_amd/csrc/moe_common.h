@@ -172,7 +172,8 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return w;
 }
 
-// 16-byte accesses; PAST 1: stores past the L2, PAST 2: loads too.
+// 16-byte accesses; PAST 1: stores past the L2, PAST 2: loads too.  The memory-side cache holds kFarBytes.
+constexpr long long kFarBytes = 256ll << 20;
 template <int PAST>
 __device__ __forceinline__ u32x4 load16(const u32x4* p) { return PAST > 1 ? __builtin_nontemporal_load(p) : *p; }
 template <int PAST>

@@ -10,12 +10,13 @@
 //     scale = max |z| r / top, rounded to fp32 once
 // The codes do not depend on r, nor on the order in which anything is added: z is exact in 64 bits (at most 24 + 11
 // significant bits), and of a quotient next to a border between two codes the exact products top z and border max |z|
-// are compared.  Squares are added in 64 bits, which no 16-bit value overflows.  The 64-bit operations stand beside about
-// 7 bytes of traffic an element and hide behind it.
+// are compared.  Squares are added by fours in fp32 and the rest in 64 bits; rows that leave
+// the middle of fp32's range go through 64 bits altogether, which no 16-bit value overflows.
+#include <algorithm>
+
 #include "launch.h"
 #include "moe_common.h"
-
-#include "../../include/moe_w4a16.h"
+#include "moe_w4a16.h"
 
 namespace moe {
 
@@ -61,6 +62,36 @@ __device__ __forceinline__ double wave_f64(double v, F f) {
   v = swap_f64<false>(v, f);
   return swap_f64<true>(v, f);
 }
+// f over values that repeat every N lanes (4, 8 or 16): what the waves of a workgroup left, one lane each.
+template <int N, class F>
+__device__ __forceinline__ double first_lanes_f64(double v, F f) {
+  v = f(v, dpp_f64<0xB1>(v));
+  v = f(v, dpp_f64<0x4E>(v));
+  if (N > 4) v = f(v, dpp_f64<0x141>(v));
+  return N > 8 ? f(v, dpp_f64<0x140>(v)) : v;
+}
+template <int N>
+__device__ __forceinline__ uint32_t first_lanes_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));
+  if (N > 4) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));
+  return N > 8 ? max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true)) : v;
+}
+
+// The largest value of each row of 16 lanes, and of the wave.
+__device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = row16_max_u32(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
 struct AddF64 {
   __device__ __forceinline__ double operator()(double a, double b) const { return a + b; }
 };
@@ -81,7 +112,7 @@ __device__ __forceinline__ double recip_f64(double v) {
 
 // The code of z where the largest magnitude is zmax, inv = 127 / zmax to 2^-45: a quotient that rounds to a border in
 // fp32 may lie on either side of it; all others lie on fp32's side.
-__device__ __forceinline__ int norm_code_i8(double z, double zmax, double inv) {
+__device__ __forceinline__ float norm_code_i8(double z, double zmax, double inv) {
   const float v = (float)(z * inv);
   float n = rintf(v);
   if (__builtin_expect(fabsf(v - n) == 0.5f, 0)) {
@@ -89,7 +120,7 @@ __device__ __forceinline__ int norm_code_i8(double z, double zmax, double inv) {
     if (d > 0.0) n = v + 0.5f;
     if (d < 0.0) n = v - 0.5f;
   }
-  return (int)fminf(fmaxf(n, -127.f), 127.f);  // (a NaN, of a row that gets codes 0 anyway, becomes a number)
+  return fminf(fmaxf(n, -127.f), 127.f);  // (a NaN, of a row that gets codes 0 anyway, becomes a number)
 }
 
 // fp32 whose E4M3 rounding (nearest, ties to even) is that of the real quotient 448 z / zmax, inv = 448 / zmax to 2^-45.
@@ -125,16 +156,22 @@ __device__ __forceinline__ void weight8(const u32x4 (&raw)[WF32 ? 2 : 1], float 
   }
 }
 
+template <int PAST>
+__device__ __forceinline__ void store8(const u32x2& v, u32x2* p) {
+  if (PAST > 0) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
 constexpr int kQuantNone = MOE_QUANT_NONE, kQuantI8 = MOE_QUANT_I8, kQuantF8 = MOE_QUANT_F8;
 
 // s of chunk c (8 columns) of a row: x, or x + residual rounded to the type.
-template <bool F16>
+template <bool F16, int PAST>
 __device__ __forceinline__ u32x4 sum8(const NormArgs& p, size_t at) {
-  u32x4 v = static_cast<const u32x4*>(p.x)[at];
+  u32x4 v = load16<PAST>(static_cast<const u32x4*>(p.x) + at);
   if (p.residual) {
     float a[8], b[8];
     unpack8<F16>(v, a);
-    unpack8<F16>(static_cast<const u32x4*>(p.residual)[at], b);
+    unpack8<F16>(load16<PAST>(static_cast<const u32x4*>(p.residual) + at), b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] += b[j];
     v = pack8<F16>(a);
@@ -142,34 +179,101 @@ __device__ __forceinline__ u32x4 sum8(const NormArgs& p, size_t at) {
   return v;
 }
 
-// A chunk's part of the row's sums.
-struct NormSums {
-  double ss;    // sum of s^2
-  double zmax;  // max |z| (int8)
-  double bad;   // 0, or NaN where z holds an infinity or a NaN
-};
+// Four squares added in fp32 (at most three roundings); all that these sums meet is added in 64 bits.
+__device__ __forceinline__ float square4(const float* s) { return fmaf(s[3], s[3], fmaf(s[2], s[2], fmaf(s[1], s[1], s[0] * s[0]))); }
+
+// A chunk's part of what a row's threads add up: the sum of s^2, and max |z|: with 16-bit weights as the bits of a float,
+// which order like the values with infinities and NaN above all; with fp32 weights, whose products with s fp32 does not
+// hold, as a double too.
 template <bool F16, bool WF32, int QUANT>
-__device__ __forceinline__ double norm_gather(const u32x4& sv, const u32x4 (&wv)[WF32 ? 2 : 1], NormSums& n) {
+__device__ __forceinline__ void norm_gather(const u32x4& sv, const u32x4 (&wv)[WF32 ? 2 : 1], double& ss, uint32_t& zbits, double& zmax) {
   float s[8], w[8];
   unpack8<F16>(sv, s);
   if (QUANT != kQuantNone) weight8<F16, WF32>(wv, w);
-  double m = 0.0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    n.ss = fma((double)s[j], (double)s[j], n.ss);
     if (QUANT != kQuantNone) {
-      const double z = (double)s[j] * (double)w[j];
-      m = fmax(m, fabs(z));
-      n.bad = fma(z, 0.0, n.bad);
+      zbits = max(zbits, __float_as_uint(s[j] * w[j]) & 0x7FFFFFFFu);
+      if (WF32) zmax = fmax(zmax, fabs((double)s[j] * (double)w[j]));
     }
   }
-  return m;
+  ss += (double)square4(s) + (double)square4(s + 4);
+}
+
+// The same in 64 bits throughout, for rows whose squares or products leave the middle of fp32's range.  Returns whether z
+// holds an infinity or a NaN.
+template <bool F16, bool WF32, int QUANT>
+__device__ __forceinline__ bool norm_gather_f64(const u32x4& sv, const u32x4 (&wv)[WF32 ? 2 : 1], double& ss, double& zmax) {
+  float s[8], w[8];
+  unpack8<F16>(sv, s);
+  weight8<F16, WF32>(wv, w);
+  double bad = 0.0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double z = (double)s[j] * (double)w[j];
+    ss = fma((double)s[j], (double)s[j], ss);
+    if (QUANT != kQuantNone) zmax = fmax(zmax, fabs(z));
+    bad = fma(z, 0.0, bad);
+  }
+  return QUANT != kQuantNone && !(bad == 0.0);
+}
+
+// Eight codes of z = s w where the largest magnitude is zmax; some false: codes 0.  fast: zmax lies in the middle of fp32's
+// range; then the quotients are formed in fp32 (z, the reciprocal and the products round: off by less than 2^-22), and only
+// those next to a border are looked at in 64 bits.
+template <int QUANT>
+__device__ __forceinline__ u32x2 norm_codes8(const float (&s)[8], const float (&w)[8], double zmax, bool some, bool fast) {
+  constexpr float kTop = QUANT == kQuantI8 ? 127.f : 448.f;
+  float v[8];
+  bool close = !fast;
+  if (fast) {
+    const float f = kTop * __builtin_amdgcn_rcpf((float)zmax);
+    float far = 0.f;
+    uint32_t near = ~0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = s[j] * w[j] * f;
+      if (QUANT == kQuantI8) {
+        const float n = rintf(v[j]);
+        far = fmaxf(far, fabsf(v[j] - n));
+        v[j] = n;
+      } else {  // borders have five significant bits; below 2^-6 they are those of the value plus 2^-6
+        const float a = fabsf(v[j]), b = a < 0x1p-6f ? a + 0x1p-6f : a;
+        near = min(near, (__float_as_uint(b) - 0x7FFF8u) & 0xFFFFFu);
+      }
+    }
+    close = QUANT == kQuantI8 ? far > 0.49995f : near <= 16u;
+  }
+  if (__builtin_expect(close, 0)) {
+    const double inv = (double)kTop * recip_f64(zmax);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double z = (double)s[j] * (double)w[j];
+      v[j] = QUANT == kQuantI8 ? norm_code_i8(z, zmax, inv) : norm_quotient_f8(z, zmax, inv);
+    }
+  }
+  u32x2 c = {0u, 0u};
+  if constexpr (QUANT == kQuantI8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = __builtin_amdgcn_perm((uint32_t)(int)v[4 * i + 1], (uint32_t)(int)v[4 * i], 0x0C0C0400u);
+      const uint32_t hi = __builtin_amdgcn_perm((uint32_t)(int)v[4 * i + 3], (uint32_t)(int)v[4 * i + 2], 0x04000C0Cu);
+      c[i] = lo | hi;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+      c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], b, true);
+    }
+  }
+  return some ? c : u32x2{0u, 0u};
 }
 
 // A chunk's outputs.
-template <bool F16, bool WF32, int QUANT>
+template <bool F16, bool WF32, int QUANT, int PAST>
 __device__ __forceinline__ void norm_store(const NormArgs& p, const u32x4& sv, const u32x4 (&wv)[WF32 ? 2 : 1], float r,
-                                           double zmax, double inv, size_t at) {
+                                           double zmax, bool some, bool fast, size_t at) {
   float s[8], w[8];
   unpack8<F16>(sv, s);
   weight8<F16, WF32>(wv, w);
@@ -177,120 +281,129 @@ __device__ __forceinline__ void norm_store(const NormArgs& p, const u32x4& sv, c
     float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = s[j] * r * w[j];
-    static_cast<u32x4*>(p.y)[at] = pack8<F16>(y);
+    store16<PAST>(pack8<F16>(y), static_cast<u32x4*>(p.y) + at);
   }
-  if constexpr (QUANT == kQuantI8) {
-    u32x2 c = {0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      c[j >> 2] |= (uint32_t)(norm_code_i8((double)s[j] * (double)w[j], zmax, inv) & 0xFF) << (8 * (j & 3));
-    static_cast<u32x2*>(p.q)[at] = inv > 0.0 ? c : u32x2{0u, 0u};
-  }
-  if constexpr (QUANT == kQuantF8) {
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = norm_quotient_f8((double)s[j] * (double)w[j], zmax, inv);
-    u32x2 c;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
-      c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], b, true);
-    }
-    static_cast<u32x2*>(p.q)[at] = inv > 0.0 ? c : u32x2{0u, 0u};
-  }
-}
-
-// The scale of codes whose largest magnitude is zmax, and what z is multiplied by: 0 (codes 0) where the scale is 0 or NaN.
-__device__ __forceinline__ float norm_scale(double zmax, double r, double top, bool bad, double& inv) {
-  const float scale = bad ? __uint_as_float(0x7FC00000u) : (float)(zmax * r * (1.0 / top));
-  inv = scale > 0.0f ? top * recip_f64(zmax) : 0.0;
-  return scale;
+  if constexpr (QUANT != kQuantNone) store8<PAST>(norm_codes8<QUANT>(s, w, zmax, some, fast), static_cast<u32x2*>(p.q) + at);
 }
 
 // TH threads a row (64: a wave, four rows a workgroup), NC chunks of 8 columns a thread, held between the sums and the
 // outputs.
-template <bool F16, bool WF32, int QUANT, int TH, int NC>
+template <bool F16, bool WF32, int QUANT, int TH, int NC, int PAST>
 __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p) {
   constexpr int kRows = TH < 256 ? 256 / TH : 1, kWaves = TH / 64;
   static_assert(TH >= 256 || TH == 64, "whole waves, or one, a row");
-  __shared__ double part_ss[kWaves], part_z[kWaves];
-  __shared__ int part_bad[kWaves];
+  __shared__ double part_ss[2][kWaves], part_z[2][kWaves];
+  __shared__ uint32_t part_bits[2][kWaves];
   const int t = threadIdx.x % TH, wave = t >> 6, lane = t & 63;
   const long long row = linear_block() * kRows + threadIdx.x / TH;
   if (row >= p.T) return;  // of all threads of a row, and of a workgroup that meets at a barrier
   const int nc = p.H / 8;
   const size_t base = (size_t)row * nc;
   u32x4 sv[NC], wv[NC][WF32 ? 2 : 1];
-  double blk[NC];
-  NormSums n = {0.0, 0.0, 0.0};
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = t + j * TH;
     if (c < nc) {
-      sv[j] = sum8<F16>(p, base + c);
+      sv[j] = sum8<F16, PAST>(p, base + c);
       load_weight8<WF32>(p.w, c, wv[j]);
     }
   }
+  // the row's sums over its threads; bits: the largest of what the threads say, 0x7F800000 and above for infinities and NaN
+  auto meet = [&](int turn, double& ss, double& zmax, uint32_t& bits) {
+    ss = wave_f64(ss, AddF64{});
+    if (QUANT == kQuantI8 && (WF32 || turn)) zmax = wave_f64(zmax, MaxF64{});
+    if (QUANT != kQuantNone) bits = wave_max_u32(bits);
+    if constexpr (TH > 64) {
+      if (lane == 0) {
+        part_ss[turn][wave] = ss;
+        if (QUANT == kQuantI8 && (WF32 || turn)) part_z[turn][wave] = zmax;
+        if (QUANT != kQuantNone) part_bits[turn][wave] = bits;
+      }
+      __syncthreads();
+      const int k = lane & (kWaves - 1);
+      ss = first_lanes_f64<kWaves>(part_ss[turn][k], AddF64{});
+      if (QUANT == kQuantI8 && (WF32 || turn)) zmax = first_lanes_f64<kWaves>(part_z[turn][k], MaxF64{});
+      if (QUANT != kQuantNone) bits = first_lanes_max<kWaves>(part_bits[turn][k]);
+    }
+  };
+  double ss = 0.0;
+  uint32_t bits = 0u;
+  double zmax = 0.0, blk[NC];
+  uint32_t blk_bits[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = t + j * TH;
     blk[j] = 0.0;
+    blk_bits[j] = 0u;
     if (c < nc) {
-      if (p.residual) static_cast<u32x4*>(p.s)[base + c] = sv[j];
-      blk[j] = norm_gather<F16, WF32, QUANT>(sv[j], wv[j], n);
+      if (p.residual) store16<PAST>(sv[j], static_cast<u32x4*>(p.s) + base + c);
+      norm_gather<F16, WF32, QUANT>(sv[j], wv[j], ss, blk_bits[j], blk[j]);
     }
-    if (QUANT == kQuantI8) n.zmax = fmax(n.zmax, blk[j]);
+    bits = max(bits, blk_bits[j]);
+    if (WF32) zmax = fmax(zmax, blk[j]);
   }
-  n.ss = wave_f64(n.ss, AddF64{});
-  if (QUANT == kQuantI8) n.zmax = wave_f64(n.zmax, MaxF64{});
-  bool bad = QUANT != kQuantNone && __ballot(!(n.bad == 0.0)) != 0ull;
-  if constexpr (TH > 64) {
-    if (lane == 0) {
-      part_ss[wave] = n.ss;
-      if (QUANT == kQuantI8) part_z[wave] = n.zmax;
-      if (QUANT != kQuantNone) part_bad[wave] = bad;
-    }
-    __syncthreads();
-    n.ss = 0.0;
+  meet(0, ss, zmax, bits);
+  // rows whose squares fp32 cannot add, or whose products or their quotients it cannot hold: once more in 64 bits (rows of
+  // zeros too: they may be products that fp32 let vanish)
+  bool fast = ss < 1e36 && (ss > 1e-25 || p.eps > 1e-15f);
+  if (QUANT != kQuantNone) fast = fast && bits >= 0x21800000u && bits < 0x7B800000u;  // 2^-60 and 2^120
+  if (QUANT == kQuantI8 && !WF32) zmax = (double)__uint_as_float(bits);
+  bool bad = false;
+  if (!fast) {
+    ss = zmax = 0.0;
+    bits = 0u;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-      n.ss += part_ss[k];
-      if (QUANT == kQuantI8) n.zmax = fmax(n.zmax, part_z[k]);
-      if (QUANT != kQuantNone) bad |= part_bad[k] != 0;
+    for (int j = 0; j < NC; ++j) {
+      blk[j] = 0.0;
+      if (t + j * TH < nc && norm_gather_f64<F16, WF32, QUANT>(sv[j], wv[j], ss, blk[j])) bits = 0x7F800000u;
+      zmax = fmax(zmax, blk[j]);
     }
+    meet(1, ss, zmax, bits);
+    bad = bits >= 0x7F800000u || !(ss < __builtin_inf());
   }
-  bad |= !(n.ss < __builtin_inf());
-  const double rd = rsqrt_f64(fma(n.ss, p.inv_h, (double)p.eps));
+  const double rd = rsqrt_f64(fma(ss, p.inv_h, (double)p.eps));
   const float r = (float)rd;
-  double inv = 0.0;
+  // scales by r / top, rounded once; where one is 0 or NaN its codes are 0
+  const double rtop = rd * (QUANT == kQuantI8 ? 1.0 / 127.0 : 1.0 / 448.0);
+  auto scale_of = [&](double m) { return bad ? __uint_as_float(0x7FC00000u) : (float)(m * rtop); };
+  float scale = 0.f;
   if constexpr (QUANT == kQuantI8) {
-    const float scale = norm_scale(n.zmax, rd, 127.0, bad, inv);
+    scale = scale_of(zmax);
     if (t == 0) p.q_scale[row] = scale;
   }
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = t + j * TH;
     if (c < nc) {
-      double zmax = n.zmax;
+      bool quick = fast;
       if constexpr (QUANT == kQuantF8) {  // the 16 lanes of a block of 128 columns are within H together
-        zmax = row16_f64(blk[j], MaxF64{});
-        const float scale = norm_scale(zmax, rd, 448.0, bad, inv);
+        if (!WF32 && fast) zmax = (double)__uint_as_float(row16_max_u32(blk_bits[j]));
+        else zmax = row16_f64(blk[j], MaxF64{});
+        scale = scale_of(zmax);
         if ((lane & 15) == 0) p.q_scale[(size_t)row * (nc / 16) + c / 16] = scale;
+        quick = fast && zmax >= 0x1p-60;  // a block may be far smaller than its row
       }
-      norm_store<F16, WF32, QUANT>(p, sv[j], wv[j], r, zmax, inv, base + c);
+      norm_store<F16, WF32, QUANT, PAST>(p, sv[j], wv[j], r, zmax, scale > 0.f, quick, base + c);
     }
   }
 }
 
+template <bool F16, bool WF32, int QUANT, int PAST>
+static hipError_t launch_norm_past(const NormArgs& p, hipStream_t s) {
+  const dim3 grid = grid2d(p.T), grid4 = grid2d(((long long)p.T + 3) / 4);
+  if (p.H <= 512) rmsnorm_kernel<F16, WF32, QUANT, 64, 1, PAST><<<grid4, 256, 0, s>>>(p);
+  else if (p.H <= 2048) rmsnorm_kernel<F16, WF32, QUANT, 256, 1, PAST><<<grid, 256, 0, s>>>(p);
+  else if (p.H <= 4096) rmsnorm_kernel<F16, WF32, QUANT, 256, 2, PAST><<<grid, 256, 0, s>>>(p);
+  else if (p.H <= 8192 && QUANT == kQuantNone) rmsnorm_kernel<F16, WF32, QUANT, 1024, 1, PAST><<<grid, 1024, 0, s>>>(p);
+  else if (p.H <= 8192) rmsnorm_kernel<F16, WF32, QUANT, 512, 2, PAST><<<grid, 512, 0, s>>>(p);
+  else rmsnorm_kernel<F16, WF32, QUANT, 1024, 2, PAST><<<grid, 1024, 0, s>>>(p);
+  return hipGetLastError();
+}
+
 template <bool F16, bool WF32, int QUANT>
 static hipError_t launch_norm_of(const NormArgs& p, hipStream_t s) {
-  const dim3 grid = grid2d(p.T), grid4 = grid2d(((long long)p.T + 3) / 4);
-  if (p.H <= 512) rmsnorm_kernel<F16, WF32, QUANT, 64, 1><<<grid4, 256, 0, s>>>(p);
-  else if (p.H <= 2048) rmsnorm_kernel<F16, WF32, QUANT, 256, 1><<<grid, 256, 0, s>>>(p);
-  else if (p.H <= 4096) rmsnorm_kernel<F16, WF32, QUANT, 256, 2><<<grid, 256, 0, s>>>(p);
-  else if (p.H <= 8192) rmsnorm_kernel<F16, WF32, QUANT, 1024, 1><<<grid, 1024, 0, s>>>(p);
-  else rmsnorm_kernel<F16, WF32, QUANT, 1024, 2><<<grid, 1024, 0, s>>>(p);
-  return hipGetLastError();
+  const long long bytes = (long long)p.T * p.H * (2 + (p.residual ? 4 : 0) + (p.y ? 2 : 0) + (QUANT != kQuantNone ? 1 : 0));
+  return bytes < kFarBytes ? launch_norm_past<F16, WF32, QUANT, 1>(p, s) : launch_norm_past<F16, WF32, QUANT, 0>(p, s);
 }
 
 template <bool F16, bool WF32>
@@ -311,12 +424,13 @@ hipError_t launch_rmsnorm(const NormArgs& p, bool f16, bool w_f32, int quant, hi
 // r is formed again from s, which has to be read anyway.  A workgroup takes every nwg-th row, a thread the same columns of
 // each, so that the weight's gradient stays in its registers; the next row is asked for before the current one's sums
 // meet.  The workgroups' sums of rows go to the workspace and are added in the order of the workgroups.
+// TH threads a row (64: a wave, four rows a workgroup, whose sums meet in LDS before they are written).
 template <bool F16, bool WF32, int TH, int NC>
-__global__ __launch_bounds__(TH) void rmsnorm_grad_kernel(NormGradArgs p) {
-  constexpr int kWaves = TH / 64;
+__global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormGradArgs p) {
+  constexpr int kWaves = TH / 64, kRows = TH < 256 ? 256 / TH : 1;
   __shared__ double part[2][kWaves][2];
-  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-  const int nc = p.H / 8, nwg = gridDim.x;
+  const int t = threadIdx.x % TH, sub = threadIdx.x / TH, wave = t >> 6, lane = t & 63;
+  const int nc = p.H / 8, step = gridDim.x * kRows;
   u32x4 wv[NC][WF32 ? 2 : 1], sv[NC], gv[NC], av[NC];
   float dw[NC][8];
 #pragma unroll
@@ -339,8 +453,9 @@ __global__ __launch_bounds__(TH) void rmsnorm_grad_kernel(NormGradArgs p) {
     }
   };
   int turn = 0;
-  load(blockIdx.x);
-  for (long long row = blockIdx.x; row < p.T; row += nwg, turn ^= 1) {
+  const long long first = (long long)blockIdx.x * kRows + sub;
+  if (first < p.T) load(first);
+  for (long long row = first; row < p.T; row += step, turn ^= 1) {
     double ss = 0.0, gs = 0.0;
     u32x4 s8[NC], g8[NC], a8[NC];
 #pragma unroll
@@ -349,7 +464,7 @@ __global__ __launch_bounds__(TH) void rmsnorm_grad_kernel(NormGradArgs p) {
       g8[j] = gv[j];
       a8[j] = av[j];
     }
-    if (row + nwg < p.T) load(row + nwg);
+    if (row + step < p.T) load(row + step);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       if (t + j * TH < nc) {
@@ -402,6 +517,23 @@ __global__ __launch_bounds__(TH) void rmsnorm_grad_kernel(NormGradArgs p) {
       }
     }
   }
+  if constexpr (kRows > 1) {
+    __shared__ float more[kRows - 1][TH * NC * 8];
+    static_assert(NC == 1, "a thread's sums stand 16 bytes apart from its neighbour's");
+    f32x4* mine = reinterpret_cast<f32x4*>(more[sub > 0 ? sub - 1 : 0]);
+    if (sub > 0) {
+      mine[t] = f32x4{dw[0][0], dw[0][1], dw[0][2], dw[0][3]};
+      mine[TH + t] = f32x4{dw[0][4], dw[0][5], dw[0][6], dw[0][7]};
+    }
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int r = 0; r < kRows - 1; ++r) {
+      const f32x4* other = reinterpret_cast<const f32x4*>(more[r]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dw[0][i] += other[(i >> 2) * TH + t][i & 3];
+    }
+  }
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = t + j * TH;
@@ -413,43 +545,57 @@ __global__ __launch_bounds__(TH) void rmsnorm_grad_kernel(NormGradArgs p) {
   }
 }
 
-// dw = the sum of n rows of parts [n, H]: 16 columns a workgroup, the rows dealt to 16 threads a column in turn, whose
-// sums (64 bits) are added in order.
-__global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* __restrict__ parts, int n, int H, int out, void* __restrict__ dw) {
-  __shared__ double sums[16][17];
-  const int l = threadIdx.x & 15, g = threadIdx.x >> 4, c = blockIdx.x * 16 + l;
-  double a = 0.0;
-  if (c < H)
-    for (int i = g; i < n; i += 16) a += (double)parts[(size_t)i * H + c];
-  sums[g][l] = a;
-  __syncthreads();
-  if (g != 0 || c >= H) return;
+// dw = the sum of n rows of parts [n, H]: 32 columns a workgroup, the rows dealt to 128 groups of 8 threads, four columns a
+// thread, whose sums (64 bits) are added in order.
+__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restrict__ parts, int n, int H, int out, void* __restrict__ dw) {
+  __shared__ double sums[128][33];
+  const int l = threadIdx.x & 7, g = threadIdx.x >> 3, c = blockIdx.x * 32 + 4 * l;
+  double a[4] = {0.0, 0.0, 0.0, 0.0};
+  if (c < H) {
+#pragma unroll 4
+    for (int i = g; i < n; i += 128) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(parts + (size_t)i * H + c);
 #pragma unroll
-  for (int i = 1; i < 16; ++i) a += sums[i][l];
-  const float v = (float)a;
-  if (out == MOE_OUT_F32) static_cast<float*>(dw)[c] = v;
-  else static_cast<uint16_t*>(dw)[c] = out == MOE_OUT_F16 ? f32_to_f16_bits(v) : f32_to_bf16_bits(v);
+      for (int j = 0; j < 4; ++j) a[j] += (double)v[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sums[g][4 * l + j] = a[j];
+  __syncthreads();
+  // 32 threads a column take four sums each, then one thread their sums
+  const int col = threadIdx.x >> 5, k = threadIdx.x & 31;
+  double v = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v += sums[4 * k + i][col];
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  const int at = blockIdx.x * 32 + col;
+  if (k != 0 || at >= H) return;
+  const float r = (float)v;
+  if (out == MOE_OUT_F32) static_cast<float*>(dw)[at] = r;
+  else static_cast<uint16_t*>(dw)[at] = out == MOE_OUT_F16 ? f32_to_f16_bits(r) : f32_to_bf16_bits(r);
 }
 
-// Threads a row of the gradient's workgroups, and the workgroups: 4096 waves at most, which hold the card's memory busy.
-static int grad_threads(int H) { return H <= 512 ? 64 : (H <= 2048 ? 256 : (H <= 8192 ? 512 : 1024)); }
+// Threads a row of the gradient's workgroups, and the workgroups: as many as the card holds at once, so that few parts are left
+// to add.
+static int grad_threads(int H) { return H <= 512 ? 64 : (H <= 2048 ? 256 : (H <= 4096 ? 512 : 1024)); }
 
 int rmsnorm_grad_parts(int T, int H) {
-  const int most = 262144 / grad_threads(H);
-  return T < most ? T : most;
+  const int th = grad_threads(H), rows = th < 256 ? 256 / th : 1, most = 1024 / std::max(1, th / 256);
+  return std::min((T + rows - 1) / rows, most);
 }
 
 template <bool F16, bool WF32>
 static hipError_t launch_norm_grad_of(const NormGradArgs& p, hipStream_t s) {
   const int n = rmsnorm_grad_parts(p.T, p.H);
   if (p.T == 0) {
-  } else if (p.H <= 512) rmsnorm_grad_kernel<F16, WF32, 64, 1><<<n, 64, 0, s>>>(p);
+  } else if (p.H <= 512) rmsnorm_grad_kernel<F16, WF32, 64, 1><<<n, 256, 0, s>>>(p);
   else if (p.H <= 2048) rmsnorm_grad_kernel<F16, WF32, 256, 1><<<n, 256, 0, s>>>(p);
   else if (p.H <= 4096) rmsnorm_grad_kernel<F16, WF32, 512, 1><<<n, 512, 0, s>>>(p);
-  else if (p.H <= 8192) rmsnorm_grad_kernel<F16, WF32, 512, 2><<<n, 512, 0, s>>>(p);
+  else if (p.H <= 8192) rmsnorm_grad_kernel<F16, WF32, 1024, 1><<<n, 1024, 0, s>>>(p);
   else rmsnorm_grad_kernel<F16, WF32, 1024, 2><<<n, 1024, 0, s>>>(p);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  rmsnorm_dw_kernel<<<(p.H + 15) / 16, 256, 0, s>>>(p.parts, n, p.H, p.dw_out, p.dw);
+  rmsnorm_dw_kernel<<<(p.H + 31) / 32, 1024, 0, s>>>(p.parts, n, p.H, p.dw_out, p.dw);
   return hipGetLastError();
 }
 

@@ -97,7 +97,7 @@ hipError_t launch_ragged_w16(const RaggedArgs& a, int mode, bool f16, int epilog
 // operands lie in that cache, 6.8 -> 8.3 us.
 __device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-constexpr long long kNearBytes = 8ll << 20, kFarBytes = 256ll << 20;
+constexpr long long kNearBytes = 8ll << 20;
 
 template <bool F16, bool GRAD, int PAST>
 __global__ __launch_bounds__(256) void silu_mul_kernel(const u32x4* G, const u32x4* dh, long long n, int chunks,

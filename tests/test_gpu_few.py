@@ -223,7 +223,7 @@ def test_decode_step():
     assert torch.equal(s2, total)
     v = total.double()
     want = v * torch.rsqrt((v * v).mean(dim=1, keepdim=True) + 1e-6) * weight.double()
-    ru.assert_close(y2, want, 3.1 * U * want.abs())
+    ru.assert_close(y2, want, 4.6 * U * want.abs())  # (see test_gpu_norm)
     assert bool(((q2.double() * scale2.double()[:, None] - want).abs() <= scale2.double()[:, None] * 0.5001).all())
 
 

@@ -1,9 +1,10 @@
 """The root-mean-square norm with the residual's addition, its 8-bit outputs and its gradient, against plain forms in 64
 bits, at the sizes and values where they can go wrong.
 
-Bounds.  y = (s * r) * w in fp32: r is off by 2^-24 (its 64-bit value rounded), the two products by 2^-24 each, so 3.1 * 2^-24 in
-all, then half a step of the type.  A scale is the 64-bit value rounded once (the 64-bit part is off by less than 2^-44).  Codes
-are those of the real quotient: equal."""
+Bounds.  Squares (exact in fp32, of 16-bit values) are added by fours in fp32, three roundings of 2^-24 of positive sums, and
+those sums in 64 bits: the mean is off by 3 * 2^-24, its inverse root by half of that.  y = (s * r) * w in fp32: r 1.5 * 2^-24 and
+2^-24 for its own rounding, the two products 2^-24 each: 4.6 * 2^-24 in all, then half a step of the type.  A scale is a
+64-bit product with that root, rounded once: 2.6 * 2^-24.  Codes are those of the real quotient: equal."""
 import pytest
 import torch
 
@@ -57,7 +58,7 @@ def _check(x, r, w, eps, quant, want_y, got):
     else:
         assert torch.equal(got[0], s)
     if want_y:
-        ru.assert_close(got[1], y, 3.1 * U * y.abs(), "y")
+        ru.assert_close(got[1], y, 4.6 * U * y.abs(), "y")
     else:
         assert got[1] is None
     if quant == NONE:
@@ -66,7 +67,7 @@ def _check(x, r, w, eps, quant, want_y, got):
     if quant == I8:
         scale = scale[:, 0]
     assert got[3].shape == scale.shape
-    assert bool(((got[3].double() - scale).abs() <= scale * U * 1.001 + 2.0 ** -149).all())
+    assert bool(((got[3].double() - scale).abs() <= scale * U * 2.6 + 2.0 ** -149).all())
     q = got[2].double() if quant == I8 else got[2].view(torch.float8_e4m3fn).double()
     assert torch.equal(q, codes)
 
@@ -183,7 +184,7 @@ def test_no_rows_and_many():
     x = torch.randint(0, 9, ((1 << 21) + 3, 8), device="cuda", dtype=torch.int32).to(BF16)  # more workgroups than one grid dimension takes
     got = moe.moe_rmsnorm_add(x, w[:8], 1e-6)[1]
     y = _reference(x, None, w[:8], 1e-6, NONE)[1]
-    ru.assert_close(got, y, 3.1 * U * y.abs())
+    ru.assert_close(got, y, 4.6 * U * y.abs())
 
 
 def test_rows_past_four_gib():
