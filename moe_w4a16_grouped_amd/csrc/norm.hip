@@ -190,13 +190,15 @@ __device__ __forceinline__ void norm_gather(const u32x4& sv, const u32x4 (&wv)[W
   float s[8], w[8];
   unpack8<F16>(sv, s);
   if (QUANT != kQuantNone) weight8<F16, WF32>(wv, w);
+  float zabs = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (QUANT != kQuantNone) {
-      zbits = max(zbits, __float_as_uint(s[j] * w[j]) & 0x7FFFFFFFu);
+      zabs = __builtin_elementwise_maximum(zabs, fabsf(s[j] * w[j]));  // (a NaN stays)
       if (WF32) zmax = fmax(zmax, fabs((double)s[j] * (double)w[j]));
     }
   }
+  zbits = __float_as_uint(zabs);
   ss += (double)square4(s) + (double)square4(s + 4);
 }
 
@@ -219,52 +221,65 @@ __device__ __forceinline__ bool norm_gather_f64(const u32x4& sv, const u32x4 (&w
 }
 
 // Eight codes of z = s w where the largest magnitude is zmax; some false: codes 0.  fast: zmax lies in the middle of fp32's
-// range; then the quotients are formed in fp32 (z, the reciprocal and the products round: off by less than 2^-22), and only
-// those next to a border are looked at in 64 bits.
+// range, and zv holds z in fp32.  Then the codes are formed from two quotients a little below and above the true one (z, the
+// reciprocal and the factor are off by less than 2^-21.7); where both give the same code, that is it, and only where some
+// element's do not, within 2^-21 of a border, are the eight formed in 64 bits.
 template <int QUANT>
-__device__ __forceinline__ u32x2 norm_codes8(const float (&s)[8], const float (&w)[8], double zmax, bool some, bool fast) {
+__device__ __forceinline__ u32x2 norm_codes8(const float (&s)[8], const float (&w)[8], const float (&zv)[8], double zmax, bool some,
+                                             bool fast) {
   constexpr float kTop = QUANT == kQuantI8 ? 127.f : 448.f;
-  float v[8];
+  u32x2 c = {0u, 0u};
   bool close = !fast;
   if (fast) {
     const float f = kTop * __builtin_amdgcn_rcpf((float)zmax);
-    float far = 0.f;
-    uint32_t near = ~0u;
+    const float below = f * (1.0f - 0x1p-21f), above = f * (1.0f + 0x1p-21f);
+    uint32_t differ = 0u;
+    if constexpr (QUANT == kQuantI8) {
+      constexpr float kInt = 0x1.8p23f;  // a sum with it is an integer, rounded to nearest even, in the low bits
+      uint32_t n[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = s[j] * w[j] * f;
-      if (QUANT == kQuantI8) {
-        const float n = rintf(v[j]);
-        far = fmaxf(far, fabsf(v[j] - n));
-        v[j] = n;
-      } else {  // borders have five significant bits; below 2^-6 they are those of the value plus 2^-6
-        const float a = fabsf(v[j]), b = a < 0x1p-6f ? a + 0x1p-6f : a;
-        near = min(near, (__float_as_uint(b) - 0x7FFF8u) & 0xFFFFFu);
+      for (int j = 0; j < 8; ++j) {
+        n[j] = __float_as_uint(fmaf(zv[j], below, kInt));
+        differ |= n[j] ^ __float_as_uint(fmaf(zv[j], above, kInt));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __builtin_amdgcn_perm(n[4 * i + 1], n[4 * i], 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(n[4 * i + 3], n[4 * i + 2], 0x04000C0Cu);
+        c[i] = lo | hi;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float* z = zv + 4 * i;
+        int a = __builtin_amdgcn_cvt_pk_fp8_f32(z[0] * below, z[1] * below, 0, false);
+        a = __builtin_amdgcn_cvt_pk_fp8_f32(z[2] * below, z[3] * below, a, true);
+        int b = __builtin_amdgcn_cvt_pk_fp8_f32(z[0] * above, z[1] * above, 0, false);
+        b = __builtin_amdgcn_cvt_pk_fp8_f32(z[2] * above, z[3] * above, b, true);
+        c[i] = (uint32_t)a;
+        differ |= (uint32_t)(a ^ b);
       }
     }
-    close = QUANT == kQuantI8 ? far > 0.49995f : near <= 16u;
+    close = differ != 0u;
   }
   if (__builtin_expect(close, 0)) {
     const double inv = (double)kTop * recip_f64(zmax);
+    float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const double z = (double)s[j] * (double)w[j];
       v[j] = QUANT == kQuantI8 ? norm_code_i8(z, zmax, inv) : norm_quotient_f8(z, zmax, inv);
     }
-  }
-  u32x2 c = {0u, 0u};
-  if constexpr (QUANT == kQuantI8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t lo = __builtin_amdgcn_perm((uint32_t)(int)v[4 * i + 1], (uint32_t)(int)v[4 * i], 0x0C0C0400u);
-      const uint32_t hi = __builtin_amdgcn_perm((uint32_t)(int)v[4 * i + 3], (uint32_t)(int)v[4 * i + 2], 0x04000C0Cu);
-      c[i] = lo | hi;
-    }
-  } else {
+      if constexpr (QUANT == kQuantI8) {
+        c[i] = 0u;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
-      c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], b, true);
+        for (int j = 0; j < 4; ++j) c[i] |= ((uint32_t)(int)v[4 * i + j] & 0xFFu) << (8 * j);
+      } else {
+        const int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+        c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], b, true);
+      }
     }
   }
   return some ? c : u32x2{0u, 0u};
@@ -273,17 +288,19 @@ __device__ __forceinline__ u32x2 norm_codes8(const float (&s)[8], const float (&
 // A chunk's outputs.
 template <bool F16, bool WF32, int QUANT, int PAST>
 __device__ __forceinline__ void norm_store(const NormArgs& p, const u32x4& sv, const u32x4 (&wv)[WF32 ? 2 : 1], float r,
-                                           double zmax, bool some, bool fast, size_t at) {
+                                           double zmax, bool some, bool fast, bool quick, size_t at) {
   float s[8], w[8];
   unpack8<F16>(sv, s);
   weight8<F16, WF32>(wv, w);
-  if (p.y) {
-    float y[8];
+  float z[8], y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = s[j] * r * w[j];
+  for (int j = 0; j < 8; ++j) z[j] = s[j] * w[j];
+  if (p.y) {  // z r, or, where z may pass fp32, s r w
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = QUANT != kQuantNone && fast ? z[j] * r : s[j] * r * w[j];
     store16<PAST>(pack8<F16>(y), static_cast<u32x4*>(p.y) + at);
   }
-  if constexpr (QUANT != kQuantNone) store8<PAST>(norm_codes8<QUANT>(s, w, zmax, some, fast), static_cast<u32x2*>(p.q) + at);
+  if constexpr (QUANT != kQuantNone) store8<PAST>(norm_codes8<QUANT>(s, w, z, zmax, some, quick), static_cast<u32x2*>(p.q) + at);
 }
 
 // TH threads a row (64: a wave, four rows a workgroup), NC chunks of 8 columns a thread, held between the sums and the
@@ -383,7 +400,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
         if ((lane & 15) == 0) p.q_scale[(size_t)row * (nc / 16) + c / 16] = scale;
         quick = fast && zmax >= 0x1p-60;  // a block may be far smaller than its row
       }
-      norm_store<F16, WF32, QUANT, PAST>(p, sv[j], wv[j], r, zmax, scale > 0.f, quick, base + c);
+      norm_store<F16, WF32, QUANT, PAST>(p, sv[j], wv[j], r, zmax, scale > 0.f, fast, quick, base + c);
     }
   }
 }
