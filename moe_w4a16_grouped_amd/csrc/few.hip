@@ -360,14 +360,19 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
   }
 }
 
-// The second launch: 8 columns of y a workgroup.  A wave takes units, an entry and every pieces-th super-chunk of SUPER elements of
-// the contraction, from a place of its own on (workgroups in step would ask the same few memory channels).  The 8 lanes (four quarters, two halves) of a row of weights read 128 bytes in a row of it; what the halves
-// take apart of the contraction they add at the end.  The entry's rows of h come as whole lines, one load a row and
-// super-chunk, and reach the lanes that need them through the wave's own LDS: as operands straight from memory they would be
-// fetched 4 to 16 times over, which the L1s do not give beside the weights.
-template <class W, int CT, int SUPER, int TOK, int RING, int NW>
+// The second launch: COLS (4, 8 or 16) columns of y a workgroup.  A wave takes units, an entry and every pieces-th super-chunk of
+// SUPER elements of the contraction, from a place of its own on (workgroups in step would ask the same few memory channels).
+// The instruction's 16 rows are 8 columns as two halves of the contraction, or 4 as four quarters (more workgroups where H
+// is small); the 8 or 16 lanes of a row of weights read 128 or 256 bytes in a row of it, and what they take apart of the
+// contraction is added at the end.  The entry's rows of h come as whole lines, one load a row and 256 elements, and reach
+// the lanes that need them through the wave's own LDS: as operands straight from memory they would be fetched 4 to 16
+// times over, which the L1s do not give beside the weights.
+template <class W, int COLS, int SUPER, int TOK, int RING, int NW>
 __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   constexpr int kHRow = SUPER * 4 + 16, HB = SUPER / 256;  // a row of h in LDS, and its 1 KB loads
+  constexpr int MR = COLS == 4 ? 4 : 8, CT = COLS / MR, SPLIT = 16 / MR;  // columns of an instruction, instructions, parts
+  constexpr int LINE = 4 * SPLIT;                                        // lanes of a row of weights
+  static_assert(TOK <= MR, "a column of the instruction for each row and part");
   extern __shared__ u32x4 few_lds[];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -375,21 +380,21 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   char* stage = reinterpret_cast<char*>(few_lds) + wave * (TOK * kHRow);
   FewEntry* table = reinterpret_cast<FewEntry*>(reinterpret_cast<char*>(few_lds) + NW * TOK * kHRow);
   float* weight = reinterpret_cast<float*>(table + R);
-  f32x4* out = reinterpret_cast<f32x4*>(weight + (R + 3) / 4 * 4);  // [pieces][R][2 * CT]: 8 * CT columns
-  const int col0 = blockIdx.x * (8 * CT);
+  f32x4* out = reinterpret_cast<f32x4*>(weight + (R + 3) / 4 * 4);  // [pieces][R][COLS / 4]
+  const int col0 = blockIdx.x * COLS;
   const int n = __builtin_amdgcn_readfirstlane(p.table[0]);
   if (tid < 2 * R) reinterpret_cast<u32x4*>(table)[tid] = reinterpret_cast<const u32x4*>(p.table)[2 + tid];
   if (tid < R) weight[tid] = p.weight[tid];
   __syncthreads();
 
-  constexpr int C = SUPER / 8 / W::LANE;  // steps of a super-chunk
+  constexpr int C = SUPER / LINE / W::LANE;  // steps of a super-chunk
   const int pieces = 1 << shift, units = n << shift;
   const int supers = (I + SUPER - 1) / SUPER;
   const bool ragged = I % SUPER != 0;
-  const int m = l16 & 7, eighth = q * 2 + (l16 >> 3);
+  const int m = l16 & (MR - 1), in_line = q * SPLIT + l16 / MR;
   const uint32_t row_bytes = (uint32_t)I * W::BYTES;
-  const uint32_t lane_offset = (uint32_t)m * row_bytes + eighth * 16;
-  const char* hfrag = stage + min(m, TOK - 1) * kHRow + eighth * (W::PARTS * 32);
+  const uint32_t lane_offset = (uint32_t)m * row_bytes + in_line * 16;
+  const char* hfrag = stage + min(m, TOK - 1) * kHRow + in_line * (W::PARTS * 32);
   struct Cursor {
     int unit, super, left;
   };
@@ -425,7 +430,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < C; ++i) ring[b][ct][i] = few_load(buffer, offset + ct * 8 * row_bytes + i * 128);
+      for (int i = 0; i < C; ++i) ring[b][ct][i] = few_load(buffer, offset + ct * MR * row_bytes + i * (LINE * 16));
 #pragma unroll
     for (int j = 0; j < TOK; ++j)
       if (j < rows) {
@@ -436,7 +441,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
     if (W::SCALED && c.left == 1) {
       const auto scales = few_buffer(p.w2_s + (size_t)e * H, (uint32_t)H * 4);
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) sc[b][ct] = __builtin_bit_cast(f32x4, few_load(scales, (col0 + ct * 8 + 4 * (q & 1)) * 4));
+      for (int ct = 0; ct < CT; ++ct) sc[b][ct] = __builtin_bit_cast(f32x4, few_load(scales, (col0 + ct * MR + (MR == 8 ? 4 * (q & 1) : 0)) * 4));
     }
   };
   Cursor use = begin(wave), ahead = use;
@@ -458,7 +463,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-          for (int i = 0; i < C; ++i) ring[b][ct][i] = few_keep(ring[b][ct][i], use.super * SUPER + (i * 8 + eighth) * W::LANE < I);
+          for (int i = 0; i < C; ++i) ring[b][ct][i] = few_keep(ring[b][ct][i], use.super * SUPER + (i * LINE + in_line) * W::LANE < I);
       }
 #pragma unroll
       for (int j = 0; j < TOK; ++j)
@@ -472,7 +477,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
       for (int i = 0; i < C; ++i)
 #pragma unroll
         for (int h = 0; h < W::PARTS; ++h) {
-          const char* at = hfrag + i * (W::PARTS * 256) + h * 32;
+          const char* at = hfrag + i * (LINE * W::PARTS * 32) + h * 32;
           const bf16x8 hi = *reinterpret_cast<const bf16x8*>(at), lo = *reinterpret_cast<const bf16x8*>(at + 16);
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {
@@ -489,16 +494,19 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
       load(ahead, b);
       advance(ahead);
       if (use.left == 1) {
-        const int f = (use.unit & (pieces - 1)) * R + table[use.unit >> shift].row[l16 & 7];
+        const int f = (use.unit & (pieces - 1)) * R + table[use.unit >> shift].row[m];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           f32x4 o;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            o[r] = acc[ct][r] + __shfl(acc[ct][r], (lane + 40) & 63);  // rows 8 + of columns 8 +: the other half
+            // part n's results stand in rows and columns MR * n + : 20 or 40 lanes further each
+            o[r] = acc[ct][r];
+#pragma unroll
+            for (int n = 1; n < SPLIT; ++n) o[r] += __shfl(acc[ct][r], (lane + n * (MR == 8 ? 40 : 20)) & 63);
             if (W::SCALED) o[r] *= scale[ct][r];
           }
-          if (q < 2 && l16 < rows) out[(f * CT + ct) * 2 + q] = o;
+          if (q < MR / 4 && l16 < rows) out[(f * CT + ct) * (MR / 4) + q] = o;
           acc[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
       }
@@ -507,8 +515,8 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   }
 summed:
   __syncthreads();
-  if (tid < 8 * CT * T) {
-    const int t = tid / (8 * CT), c = tid % (8 * CT);
+  if (tid < COLS * T) {
+    const int t = tid / COLS, c = tid % COLS;
     const float* o8 = reinterpret_cast<const float*>(out) + c;
     float y = 0.f;
     for (int s = 0; s < k; s += 4) {  // four slots' values are asked for at a time; their sum is that of the slots in order
@@ -517,8 +525,8 @@ summed:
       for (int j = 0; j < 4; ++j) {
         const int f = t * k + min(s + j, k - 1);
         w[j] = weight[f];
-        o[j] = o8[f * (8 * CT)];
-        for (int i = 1; i < pieces; ++i) o[j] += o8[(i * R + f) * (8 * CT)];
+        o[j] = o8[f * COLS];
+        for (int i = 1; i < pieces; ++i) o[j] += o8[(i * R + f) * COLS];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -558,16 +566,16 @@ static hipError_t launch_few_of(const FewArgs& p, hipStream_t s) {
   return p.T == 1 ? launch_few_first<W, NJ, true>(p, s) : launch_few_first<W, NJ, false>(p, s);
 }
 
-template <class W, int CT, int SUPER, int TOK, int RING, int NW>
+template <class W, int COLS, int SUPER, int TOK, int RING, int NW>
 static hipError_t launch_few_second(FewArgs p, hipStream_t s) {
   p.pieces_shift = few_pieces_shift(p.k, p.I, SUPER, NW);
-  const int R = p.T * p.k, lds = NW * TOK * (SUPER * 4 + 16) + R * 32 + (R + 3) / 4 * 16 + (R << p.pieces_shift) * 32 * CT;
-  const auto kernel = few_down_kernel<W, CT, SUPER, TOK, RING, NW>;
+  const int R = p.T * p.k, lds = NW * TOK * (SUPER * 4 + 16) + R * 32 + (R + 3) / 4 * 16 + (R << p.pieces_shift) * 4 * COLS;
+  const auto kernel = few_down_kernel<W, COLS, SUPER, TOK, RING, NW>;
   if (lds > (64 << 10)) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  kernel<<<p.H / (8 * CT), 64 * NW, lds, s>>>(p);
+  kernel<<<p.H / COLS, 64 * NW, lds, s>>>(p);
   return hipGetLastError();
 }
 
@@ -582,17 +590,24 @@ static hipError_t launch_few_w(FewArgs p, hipStream_t s) {
   else if (p.E <= 512) e = launch_few_of<W, 8>(p, s);
   else e = launch_few_of<W, 16>(p, s);
   if (e != hipSuccess) return e;
-  if (p.T == 1) return launch_few_second<W, 1, 256, 1, 3, 8>(p, s);
+  // 4 columns a workgroup where 8 would leave half the CUs idle and the contraction fills super-chunks of 512 (8 tokens, 64
+  // experts top-6, 1024 x 512, bf16: 10.4 us against 13.5; 12 tokens, 1536 x 1536: 47 against 37; int8 1040 x 336: 11.7 against 10.1)
+  const bool narrow = p.H <= 1280 && p.I >= 512;
+  if (p.T == 1) {
+    if (narrow) return launch_few_second<W, 4, 512, 1, 2, 8>(p, s);
+    return launch_few_second<W, 8, 256, 1, 3, 8>(p, s);
+  }
   if (crowded) {
     // 16 columns a workgroup halve the traffic of h, but want enough workgroups (16 tokens, 8 experts of 4096 x 14336: 167 us
     // against 190; 2048 columns: 44 us against 30)
-    if (p.H >= 4096) return launch_few_second<W, 2, 256, 8, 2, 8>(p, s);
-    return launch_few_second<W, 1, 256, 8, 2, 8>(p, s);
+    if (p.H >= 4096) return launch_few_second<W, 16, 256, 8, 2, 8>(p, s);
+    return launch_few_second<W, 8, 256, 8, 2, 8>(p, s);
   }
+  if (narrow) return launch_few_second<W, 4, 512, 4, 2, 8>(p, s);
   // int8 units are half as long in bytes and convert their weights: twice the waves (16 tokens, 256 experts top-8, 2048 x 512:
   // 24 us against 26; bf16, 8 tokens, 128 experts, 2048 x 768: 32 us against 31, so not there)
-  if (W::SCALED) return launch_few_second<W, 1, 256, 4, 2, 16>(p, s);
-  return launch_few_second<W, 1, 256, 4, 3, 8>(p, s);
+  if (W::SCALED) return launch_few_second<W, 8, 256, 4, 2, 16>(p, s);
+  return launch_few_second<W, 8, 256, 4, 3, 8>(p, s);
 }
 
 hipError_t launch_ffn_few(const FewArgs& p, bool i8, hipStream_t stream) {
