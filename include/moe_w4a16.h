@@ -779,7 +779,7 @@ size_t moe_rmsnorm_add_grad_workspace_bytes(int32_t T, int32_t H);
  * ds [T, H] (gradient that reaches s by other paths, such as the residual stream's, or NULL):
  *   dx = r * (dy * weight - s * r^2 * mean(dy * weight * s)) + ds     [T, H], of x and of the residual alike
  *   dweight = sum over the rows of dy * s * r                         [H], of dweight_dtype MOE_OUT_BF16, _F16 or _F32
- * Sums over a row in 64 bits, everything else in fp32, one rounding.  dweight is summed in parts of the rows, which are
+ * Sums over a row in 64 bits, everything else in fp32 (dy * weight within its range), one rounding.  dweight is summed in parts of the rows, which are
  * added in order (zeros where T is 0).  workspace: at least moe_rmsnorm_add_grad_workspace_bytes(T, H) bytes.
  * dx may be dy, s or ds.  Types, shapes and alignment as for moe_rmsnorm_add.
  */
@@ -800,7 +800,8 @@ moe_status_t moe_rmsnorm_add_grad(const void* dy, const void* s, int32_t dtype, 
  * workspace: at least moe_ffn_few_workspace_bytes(T, H, I, E, k) bytes.  Where T * H passes 65536 the tokens are taken in
  * groups that stay below it, each with its two launches (and its own reading of the weights).
  * Shapes: 0 <= T <= MOE_FEW_MAX_TOKENS, 1 <= k <= min(E, MOE_FEW_MAX_K), E <= MOE_MAX_EXPERTS, H and I multiples of
- * 16, 16 <= H <= 65536, 16 <= I <= MOE_I8_MAX_K.  Alignment: x, weights, y and workspace 16 bytes, the others 4.
+ * 16, 16 <= H <= 65536, 16 <= I <= MOE_I8_MAX_K, one expert's gate_up weights below 4 GiB.  Alignment: x, weights, y and
+ * workspace 16 bytes, the others 4.
  */
 #define MOE_FEW_MAX_TOKENS 16
 #define MOE_FEW_MAX_K 16

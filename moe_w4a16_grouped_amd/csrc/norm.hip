@@ -394,11 +394,19 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
     if (c < nc) {
       bool quick = fast;
       if constexpr (QUANT == kQuantF8) {  // the 16 lanes of a block of 128 columns are within H together
-        if (!WF32 && fast) zmax = (double)__uint_as_float(row16_max_u32(blk_bits[j]));
-        else zmax = row16_f64(blk[j], MaxF64{});
+        if (!WF32 && fast) {
+          zmax = (double)__uint_as_float(row16_max_u32(blk_bits[j]));
+          if (zmax < 0x1p-60) {  // a block may be far smaller than its row, down to products that fp32 does not hold
+            double unused = 0.0, m = 0.0;
+            norm_gather_f64<F16, WF32, QUANT>(sv[j], wv[j], unused, m);
+            zmax = row16_f64(m, MaxF64{});
+          }
+        } else {
+          zmax = row16_f64(blk[j], MaxF64{});
+        }
         scale = scale_of(zmax);
         if ((lane & 15) == 0) p.q_scale[(size_t)row * (nc / 16) + c / 16] = scale;
-        quick = fast && zmax >= 0x1p-60;  // a block may be far smaller than its row
+        quick = fast && zmax >= 0x1p-60;
       }
       norm_store<F16, WF32, QUANT, PAST>(p, sv[j], wv[j], r, zmax, scale > 0.f, fast, quick, base + c);
     }
@@ -445,6 +453,7 @@ hipError_t launch_rmsnorm(const NormArgs& p, bool f16, bool w_f32, int quant, hi
 template <bool F16, bool WF32, int TH, int NC>
 __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormGradArgs p) {
   constexpr int kWaves = TH / 64, kRows = TH < 256 ? 256 / TH : 1;
+  constexpr bool kAhead = NC == 1;  // with two chunks a thread a second row would not fit the registers of 1024 threads
   __shared__ double part[2][kWaves][2];
   const int t = threadIdx.x % TH, sub = threadIdx.x / TH, wave = t >> 6, lane = t & 63;
   const int nc = p.H / 8, step = gridDim.x * kRows;
@@ -471,17 +480,18 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormG
   };
   int turn = 0;
   const long long first = (long long)blockIdx.x * kRows + sub;
-  if (first < p.T) load(first);
+  if (kAhead && first < p.T) load(first);
   for (long long row = first; row < p.T; row += step, turn ^= 1) {
     double ss = 0.0, gs = 0.0;
     u32x4 s8[NC], g8[NC], a8[NC];
+    if (!kAhead) load(row);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       s8[j] = sv[j];
       g8[j] = gv[j];
       a8[j] = av[j];
     }
-    if (row + step < p.T) load(row + step);
+    if (kAhead && row + step < p.T) load(row + step);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       if (t + j * TH < nc) {

@@ -47,8 +47,9 @@ def _reference(x, r, w, eps, quant):
     top = 127.0 if quant == I8 else 448.0
     most = z.abs().amax(dim=2, keepdim=True)
     quotient = torch.where(most > 0, z * top / torch.where(most > 0, most, 1.0), 0.0)
-    codes = torch.round(quotient) if quant == I8 else _e4m3(quotient)
-    return s, y, codes.view(x.shape), (most * rstd[:, :, None] / top).squeeze(2)
+    scale = most * rstd[:, :, None] / top
+    codes = torch.where(scale.float() > 0, torch.round(quotient) if quant == I8 else _e4m3(quotient), 0.0)
+    return s, y, codes.view(x.shape), scale.squeeze(2)
 
 
 def _check(x, r, w, eps, quant, want_y, got):
@@ -140,6 +141,23 @@ def test_far_magnitudes(quant, value):
     _check(x, None, w, 1e-6, quant, True, got)
     tiny = (_rand((4, 256), F32, 5) * 2.0 ** -120).to(BF16)  # r = 2^60 with an eps as small
     _check(tiny, None, w, 2.0 ** -120, quant, True, moe.moe_rmsnorm_add(tiny, w, 2.0 ** -120, quant=quant))
+
+
+@pytest.mark.parametrize("w_dtype", [BF16, F32])
+@pytest.mark.parametrize("quant", [I8, F8])
+def test_blocks_of_far_magnitudes_in_one_row(quant, w_dtype):
+    """Blocks whose products vanish in fp32, or nearly, beside ordinary ones; blocks and rows of zeros."""
+    H = 1024
+    x = _rand((5, H), F32, 3)
+    scale = torch.tensor([1.0, 2.0 ** -40, 2.0 ** -100, 2.0 ** -120, 0.0, 2.0 ** 30, 2.0 ** -62, 1e-3], device="cuda").repeat_interleave(128)
+    x[:3] *= scale
+    x[2] *= 2.0 ** -20
+    x[3] = 0
+    w = _weight(H, F32, 4)
+    w[256:512] *= 2.0 ** -35
+    x, w = x.to(BF16), w.to(w_dtype)
+    for eps in (1e-6, 1e-30):
+        _check(x, None, w, eps, quant, True, moe.moe_rmsnorm_add(x, w, eps, quant=quant))
 
 
 @pytest.mark.parametrize("quant", [I8, F8])
