@@ -19,6 +19,7 @@
 // h stays in two bf16 parts (value, and what its rounding left), for about 16 significant bits: the traffic of h is small
 // beside the weights', and y is then rounded once.  Sums are fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "moe_common.h"
@@ -126,6 +127,13 @@ __device__ __forceinline__ float few_weight(float logit, int k) {
   return p / sum;
 }
 
+// h as two bf16: itself, and (upper half) what that leaves; nothing beside an infinity.
+__device__ __forceinline__ uint32_t few_parts(float h) {
+  const uint32_t hi = f32_to_bf16_bits(h);
+  const float left = h - bf16_bits_to_f32(hi);
+  return hi | (fabsf(left) < __builtin_inff() ? (uint32_t)f32_to_bf16_bits(left) << 16 : 0u);
+}
+
 // LDS of the first launch; the tokens stand behind it, 16 bytes apart in the banks.
 struct FewLds {
   f32x4 part[2][kFewWaves][64];
@@ -138,8 +146,8 @@ struct FewLds {
   int32_t more;
 };
 
-// ONE: a single token.
-template <class W, int NJ, bool ONE>
+// ONE: a single token.  ALONE: a task is a wave's own, the whole contraction of it, rather than a workgroup's.
+template <class W, int NJ, bool ONE, bool ALONE>
 __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) {
   extern __shared__ u32x4 few_lds[];
   FewLds& s = *reinterpret_cast<FewLds*>(few_lds);
@@ -261,9 +269,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
 
   // this wave's share of the contraction, in chunks of C steps
   constexpr int C = 4, RING = 2, STEP = 4 * W::LANE;
-  const int steps = (H + STEP - 1) / STEP, share = (steps + kFewWaves - 1) / kFewWaves;
+  const int steps = (H + STEP - 1) / STEP, share = ALONE ? steps : (steps + kFewWaves - 1) / kFewWaves;
   const int chunks = (share + C - 1) / C, blocks = I / 8;
-  const int first = wave * share * STEP;                       // of the contraction
+  const int first = ALONE ? 0 : wave * share * STEP;             // of the contraction
   const int whole = max(0, min(share, (H - first) / STEP)) / C;  // chunks that lie within the share and the row
   const uint32_t row_bytes = (uint32_t)H * W::BYTES;
   const uint32_t lane_offset = (uint32_t)(l16 < 8 ? l16 : I + l16 - 8) * row_bytes + (first + q * W::LANE) * W::BYTES;
@@ -271,7 +279,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
   struct Cursor {
     int rank, block, chunk;
   };
-  const int rank_step = gridDim.x / blocks, block_step = gridDim.x - rank_step * blocks;
+  const int workers = ALONE ? gridDim.x * kFewWaves : gridDim.x, worker = ALONE ? blockIdx.x * kFewWaves + wave : blockIdx.x;
+  const int rank_step = workers / blocks, block_step = workers - rank_step * blocks;
   auto advance = [&](Cursor& c) {
     if (++c.chunk < chunks) return;
     c.chunk = 0;
@@ -280,7 +289,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
     if (c.block >= blocks) c.block -= blocks, ++c.rank;
   };
   u32x4 ring[RING][C];
-  float sg[RING], su[RING];  // scales of the column that this thread finishes
+  using Scales = std::conditional_t<ALONE, f32x4, float>;
+  Scales sg[RING], su[RING];  // of the column that this thread finishes, or its four
   const uint32_t expert_bytes = (uint32_t)(2 * I) * row_bytes;
   auto load = [&](const Cursor& c, int b) {
     if (c.rank >= n) return;
@@ -289,13 +299,18 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
     const uint32_t offset = lane_offset + (uint32_t)c.block * 8 * row_bytes + c.chunk * (C * STEP * W::BYTES);
 #pragma unroll
     for (int i = 0; i < C; ++i) ring[b][i] = few_load(buffer, offset + i * (STEP * W::BYTES));
-    if (W::SCALED && c.chunk == chunks - 1 && tid < 8 * kFewTokens) {
+    if constexpr (W::SCALED && ALONE) if (c.chunk == chunks - 1) {
+      const auto scales = few_buffer(p.w13_s + (size_t)e * (2 * I), (uint32_t)I * 8);
+      sg[b] = __builtin_bit_cast(Scales, few_load(scales, (c.block * 8 + 4 * (q & 1)) * 4));
+      su[b] = __builtin_bit_cast(Scales, few_load(scales, (I + c.block * 8 + 4 * (q & 1)) * 4));
+    }
+    if constexpr (W::SCALED && !ALONE) if (c.chunk == chunks - 1 && tid < 8 * kFewTokens) {
       const float* sc = p.w13_s + (size_t)e * (2 * I) + c.block * 8 + (tid & 7);
       sg[b] = sc[0];
       su[b] = sc[I];
     }
   };
-  Cursor use = {(int)blockIdx.x / blocks, (int)blockIdx.x % blocks, 0}, ahead = use;
+  Cursor use = {worker / blocks, worker % blocks, 0}, ahead = use;
 #pragma unroll
   for (int b = 0; b < RING; ++b) {
     load(ahead, b);
@@ -326,10 +341,35 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
             acc = mfma16x16x32(W::part(w, h), *reinterpret_cast<const bf16x8*>(xi + 16 * h), acc);
         }
       }
-      const float scale_g = W::SCALED ? sg[b] : 1.f, scale_u = W::SCALED ? su[b] : 1.f;
+      const Scales scale_g = sg[b], scale_u = su[b];
       load(ahead, b);
       advance(ahead);
-      if (use.chunk == chunks - 1) {
+      if constexpr (ALONE) if (use.chunk == chunks - 1) {
+        // gate rows are in the lower half of the wave, the up rows of the same columns and tokens 32 lanes on
+        float h[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const auto gu = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[r]), __float_as_uint(acc[r]), false, false);
+          float g = __uint_as_float(gu[0]), up = __uint_as_float(gu[1]);
+          if (W::SCALED) g *= scale_g[r], up *= scale_u[r];
+          h[r] = silu_f32(g) * up;
+        }
+        const int f = ONE ? (l16 == 0 ? use.rank : -1) : s.slot[use.rank][l16];
+        if (lane < 32 && f >= 0) {
+          u32x2 hi, lo;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t a = few_parts(h[2 * r]), b = few_parts(h[2 * r + 1]);
+            hi[r] = (a & 0xFFFFu) | (b << 16);
+            lo[r] = (a >> 16) | (b & 0xFFFF0000u);
+          }
+          u32x2* dst = reinterpret_cast<u32x2*>(p.h + ((size_t)f * blocks + use.block) * 16 + 4 * q);
+          dst[0] = hi;
+          dst[2] = lo;
+        }
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      if constexpr (!ALONE) if (use.chunk == chunks - 1) {
         s.part[turn][wave][lane] = acc;
         acc = f32x4{0.f, 0.f, 0.f, 0.f};
         __syncthreads();  // one a task: this half of part is written again only past the next task's barrier
@@ -345,12 +385,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
           }
           if (W::SCALED) g *= scale_g, up *= scale_u;
           if (f >= 0) {
-            const float h = silu_f32(g) * up;
-            const uint32_t hi = f32_to_bf16_bits(h);
-            const float left = h - bf16_bits_to_f32(hi);
+            const uint32_t parts = few_parts(silu_f32(g) * up);
             uint16_t* dst = p.h + ((size_t)f * blocks + use.block) * 16 + c;
-            dst[0] = (uint16_t)hi;
-            dst[8] = fabsf(left) < __builtin_inff() ? f32_to_bf16_bits(left) : (uint16_t)0;
+            dst[0] = (uint16_t)parts;
+            dst[8] = (uint16_t)(parts >> 16);
           }
         }
         turn ^= 1;
@@ -545,25 +583,32 @@ static int few_pieces_shift(int k, int I, int super, int waves) {
   return shift;
 }
 
-template <class W, int NJ, bool ONE>
+template <class W, int NJ, bool ONE, bool ALONE>
 static hipError_t launch_few_first(const FewArgs& p, hipStream_t s) {
   const int lds = (int)((sizeof(FewLds) + 15) / 16 * 16) + p.T * (2 * p.H + 16);
   // Workgroups a CU: of one token three, which then have a piece of the largest of its layers each; of more two, as every
   // workgroup routes all of them (11 tokens, 60 experts top-6, 1040 x 336 int8: 27.3 us with two, 29.6 with three).
   const int fit = std::max(1, std::min(ONE ? 3 : 2, (160 << 10) / lds));
-  const int grid = std::min(std::min(p.E, p.T * p.k) * (p.I / 8), 256 * fit);
+  const int tasks = std::min(p.E, p.T * p.k) * (p.I / 8);
+  const int grid = std::min(ALONE ? (tasks + kFewWaves - 1) / kFewWaves : tasks, 256 * fit);
+  const auto kernel = few_gate_up_kernel<W, NJ, ONE, ALONE>;
   if (lds > (64 << 10)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(few_gate_up_kernel<W, NJ, ONE>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  few_gate_up_kernel<W, NJ, ONE><<<grid, 64 * kFewWaves, lds, s>>>(p);
+  kernel<<<grid, 64 * kFewWaves, lds, s>>>(p);
   return hipGetLastError();
 }
 
 template <class W, int NJ>
 static hipError_t launch_few_of(const FewArgs& p, hipStream_t s) {
-  return p.T == 1 ? launch_few_first<W, NJ, true>(p, s) : launch_few_first<W, NJ, false>(p, s);
+  // Short rows of weights: a wave a task, without the barrier and the meeting that a task of a workgroup ends with (12 tokens, 64
+  // experts top-4, 256 x 7168: bf16 54 us against 127, int8 128 x 7168 29 against 135; int8 1536 x 1040 21.4 against 22.5,
+  // bf16 1536 x 1040 36 against 33).  One token has too few tasks for that beyond H 512 (512 x 1536 int8: 7.2 us against 10.6,
+  // 1024 x 512: 10.2 against 7.7).
+  const bool alone = p.T == 1 ? p.H <= 512 : p.H * W::BYTES <= 1536;
+  if (alone) return p.T == 1 ? launch_few_first<W, NJ, true, true>(p, s) : launch_few_first<W, NJ, false, true>(p, s);
+  return p.T == 1 ? launch_few_first<W, NJ, true, false>(p, s) : launch_few_first<W, NJ, false, false>(p, s);
 }
 
 template <class W, int COLS, int SUPER, int TOK, int RING, int NW>
