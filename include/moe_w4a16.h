@@ -795,8 +795,9 @@ moe_status_t moe_rmsnorm_add_grad(const void* dy, const void* s, int32_t dtype, 
  *   moe_ffn_few_w16:   w13 bf16 [E, 2I, H], w2 bf16 [E, H, I].
  *   moe_ffn_few_w8a16: the int8 weights and channel scales of moe_ffn_forward_i8; activations are not quantized (a few
  *                      tokens are bound by the weights' bytes).
- * x bf16 [T, H]; router_logits fp32 [T, E], finite; y bf16 [T, H] out, rounded once: h keeps about 16 significant bits
- * and all sums are fp32.  topk_ids_out int32 [T, k], topk_w_out fp32 [T, k]: optional copies of the routing (NULL = skip).
+ * x bf16 [T, H]; router_logits fp32 [T, E], finite or (an expert that is closed) -infinity, in each token at least one
+ * finite; a slot whose weight is 0 adds nothing, whatever its expert holds.  y bf16 [T, H] out, rounded once: h keeps about
+ * 16 significant bits and all sums are fp32.  topk_ids_out int32 [T, k], topk_w_out fp32 [T, k]: optional copies of the routing (NULL = skip).
  * workspace: at least moe_ffn_few_workspace_bytes(T, H, I, E, k) bytes.  Where T * H passes 65536 the tokens are taken in
  * groups that stay below it, each with its two launches (and its own reading of the weights).
  * Shapes: 0 <= T <= MOE_FEW_MAX_TOKENS, 1 <= k <= min(E, MOE_FEW_MAX_K), E <= MOE_MAX_EXPERTS, H and I multiples of

@@ -568,7 +568,7 @@ summed:
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (s + j < k) y = fmaf(w[j], o[j], y);
+        if (s + j < k && w[j] != 0.f) y = fmaf(w[j], o[j], y);  // a closed expert may hold anything
     }
     p.y[(size_t)t * H + col0 + c] = f32_to_bf16_bits(y);
   }

@@ -113,7 +113,7 @@ def test_crowded_and_tied(int8):
 @pytest.mark.parametrize("int8", [False, True], ids=["w16", "w8a16"])
 @pytest.mark.parametrize("lowest", [-3.4028234663852886e38, float("-inf")])
 def test_masked_experts(int8, lowest):
-    """Experts that a mask closes get the weight 0 where fewer than k are left open, and never reach y by a NaN."""
+    """Experts that a mask closes get the weight 0 where fewer than k are left open, and never reach y, whatever they hold."""
     T, E, k, H, I = 6, 16, 4, 128, 64
     logits = _rand((T, E), F32, 1)
     logits[:, 2:] = lowest
@@ -122,6 +122,11 @@ def test_masked_experts(int8, lowest):
     y = L.run(topk_w_out=w)
     assert not bool(w[:, 2:].any())
     L.check(y)
+    if int8:
+        L.w13_s[2:], L.w2_s[2:] = float("nan"), float("inf")
+    else:
+        L.w13[2:], L.w2[2:] = float("nan"), float("inf")
+    assert torch.equal(L.run(), y)
 
 
 def test_values_without_end_stay_with_their_token():
