@@ -779,8 +779,9 @@ size_t moe_rmsnorm_add_grad_workspace_bytes(int32_t T, int32_t H);
  * ds [T, H] (gradient that reaches s by other paths, such as the residual stream's, or NULL):
  *   dx = r * (dy * weight - s * r^2 * mean(dy * weight * s)) + ds     [T, H], of x and of the residual alike
  *   dweight = sum over the rows of dy * s * r                         [H], of dweight_dtype MOE_OUT_BF16, _F16 or _F32
- * Sums over a row in 64 bits, everything else in fp32 (dy * weight within its range), one rounding.  dweight is summed in parts of the rows, which are
- * added in order (zeros where T is 0).  workspace: at least moe_rmsnorm_add_grad_workspace_bytes(T, H) bytes.
+ * Sums over a row in 64 bits, everything else in fp32 (dy * weight within its range), one rounding.  dweight is summed
+ * in parts of the rows, which are added in order (zeros where T is 0).  workspace: at least
+ * moe_rmsnorm_add_grad_workspace_bytes(T, H) bytes.
  * dx may be dy, s or ds.  Types, shapes and alignment as for moe_rmsnorm_add.
  */
 moe_status_t moe_rmsnorm_add_grad(const void* dy, const void* s, int32_t dtype, const void* weight, int32_t weight_dtype,
@@ -797,16 +798,17 @@ moe_status_t moe_rmsnorm_add_grad(const void* dy, const void* s, int32_t dtype, 
  *                      tokens are bound by the weights' bytes).
  * x bf16 [T, H]; router_logits fp32 [T, E], finite or (an expert that is closed) -infinity, in each token at least one
  * finite; a slot whose weight is 0 adds nothing, whatever its expert holds.  y bf16 [T, H] out, rounded once: h keeps about
- * 16 significant bits and all sums are fp32.  topk_ids_out int32 [T, k], topk_w_out fp32 [T, k]: optional copies of the routing (NULL = skip).
- * workspace: at least moe_ffn_few_workspace_bytes(T, H, I, E, k) bytes.  Where T * H passes 65536 the tokens are taken in
- * groups that stay below it, each with its two launches (and its own reading of the weights).
+ * 16 significant bits and all sums are fp32.  topk_ids_out int32 [T, k], topk_w_out fp32 [T, k]: optional copies of the
+ * routing (NULL = skip).  workspace: at least moe_ffn_few_workspace_bytes(T, H, I, E, k) bytes, of one call at a time.
+ * Where T * H passes 65536 the tokens are taken in groups that do not, each with its two launches (and its own reading
+ * of the weights).
  * Shapes: 0 <= T <= MOE_FEW_MAX_TOKENS, 1 <= k <= min(E, MOE_FEW_MAX_K), E <= MOE_MAX_EXPERTS, H and I multiples of
  * 16, 16 <= H <= 65536, 16 <= I <= MOE_I8_MAX_K, one expert's gate_up weights below 4 GiB.  Alignment: x, weights, y and
  * workspace 16 bytes, the others 4.
  */
 #define MOE_FEW_MAX_TOKENS 16
 #define MOE_FEW_MAX_K 16
-/* Workspace bytes of both (host-only, pure; 0 on invalid sizes). */
+/* Workspace bytes of both (host-only, pure; 0 on sizes that both refuse, and where T is 0). */
 size_t moe_ffn_few_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k);
 moe_status_t moe_ffn_few_w16(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E,
                              int32_t k, const uint16_t* w13, const uint16_t* w2, uint16_t* y, int32_t* topk_ids_out,

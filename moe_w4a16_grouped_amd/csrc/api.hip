@@ -1805,7 +1805,9 @@ moe_status_t run_few(const uint16_t* x, const float* router_logits, int32_t T, i
 }  // namespace
 
 size_t moe_ffn_few_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k) {
-  if (T < 1 || T > MOE_FEW_MAX_TOKENS || !few_dims_ok(H, I) || E < 1 || k < 1 || k > E || k > MOE_FEW_MAX_K || E > MOE_MAX_EXPERTS) return 0;
+  if (T < 1 || T > MOE_FEW_MAX_TOKENS || !few_dims_ok(H, I) || !ragged_ffn_weights_ok(H, I, true) || E < 1 || k < 1 || k > E ||
+      k > MOE_FEW_MAX_K || E > MOE_MAX_EXPERTS)
+    return 0;
   return few_layout(T, few_group(T, H), I, k).total;
 }
 

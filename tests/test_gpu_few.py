@@ -202,6 +202,66 @@ def test_stream_and_graph(int8):
         assert torch.equal(out, L.run())
 
 
+@pytest.mark.parametrize("int8", [False, True], ids=["w16", "w8a16"])
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 16, 4, 512, 1024), (1, 300, 16, 528, 1040), (1, 9, 2, 32, 4112), (2, 40, 7, 1280, 544), (16, 5, 3, 4112, 48),
+                                       (15, 31, 1, 768, 528), (4, 1024, 3, 144, 16)])
+def test_mixes_of_the_rules(T, E, k, H, I, int8):
+    """Short rows and narrow outputs, single tokens, crowded experts, in the mixes that SHAPES leaves out."""
+    L = Layer(T, E, k, H, I, int8, seed=T * E)
+    L.check(L.run())
+
+
+def test_scales_on_four_bytes():
+    """Scales need four bytes of alignment only."""
+    for T, E, k, H, I in ((12, 20, 4, 256, 112), (1, 20, 4, 2048, 64), (1, 20, 4, 256, 640)):
+        L = Layer(T, E, k, H, I, True, seed=3)
+        y = L.run()
+        for name in ("w13_s", "w2_s"):
+            t = getattr(L, name)
+            moved = torch.full((t.numel() + 4,), float("nan"), device="cuda")
+            moved[1:-3] = t.view(-1)
+            setattr(L, name, moved[1:-3].view(t.shape))
+        assert torch.equal(L.run(), y)
+
+
+@pytest.mark.parametrize("int8", [False, True], ids=["w16", "w8a16"])
+def test_two_graphs_of_one_workspace(int8):
+    """A token group a launch, captured: 5 tokens of 16384 columns are groups of 4 and 1.  Two graphs share a workspace."""
+    layers = [Layer(5, 6, 2, 16384, 64, int8, seed=1), Layer(16, 30, 5, 512, 272, int8, seed=2)]
+    size = max(moe.moe_ffn_few_workspace_bytes(*L.x.shape, L.w2.shape[2], L.logits.shape[1], L.k) for L in layers)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    for L in layers:
+        L.check(L.run(workspace=ws))
+    graphs, outs = [], []
+    for L in layers:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(L.run(workspace=ws))
+    for seed in range(4):
+        for L in layers:
+            L.x.copy_(_rand(tuple(L.x.shape), BF16, 50 + seed))
+            L.logits.copy_(_rand(tuple(L.logits.shape), F32, 60 + seed))
+        for i in (0, 1, 1, 0):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for L, out in zip(layers, outs):
+            assert torch.equal(out, L.run())
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each."""
+    layers = [Layer(16, 64, 6, 1024, 512, False, seed=1), Layer(9, 40, 4, 2048, 256, True, seed=2)]
+    want = [L.run() for L in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[L.run(stream=s) for L, s in zip(layers, streams)] for _ in range(8)]
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for pair in got:
+        assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+
+
 def test_close_to_the_layers_of_any_size():
     """The layer that these launches stand in for rounds h to bf16 (2^-8 of it, half a step), and y the same."""
     for int8 in (False, True):

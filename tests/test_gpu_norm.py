@@ -323,6 +323,27 @@ def test_norm_on_a_stream_and_in_a_graph():
             assert torch.equal(a, b)
 
 
+def test_two_gradients_of_one_workspace_in_graphs():
+    sizes = ((70, 2048), (301, 264))
+    ws = torch.full((max(moe.moe_rmsnorm_add_grad_workspace_bytes(*z) for z in sizes),), 0xFF, dtype=torch.uint8, device="cuda")
+    args, graphs, outs = [], [], []
+    for i, (T, H) in enumerate(sizes):
+        args.append((_rand((T, H), BF16, i), _rand((T, H), BF16, 9 + i), _weight(H, F32, 3)))
+        _check_grad(*args[-1], 1e-6, None, moe.moe_rmsnorm_add_grad(*args[-1], 1e-6, workspace=ws))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(moe.moe_rmsnorm_add_grad(*args[-1], 1e-6, workspace=ws))
+    for seed in range(4):
+        for dy, _, _ in args:
+            dy.copy_(_rand(tuple(dy.shape), BF16, 70 + seed))
+        for i in (0, 1, 1, 0):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for a, out in zip(args, outs):
+            want = moe.moe_rmsnorm_add_grad(*a, 1e-6)
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
 def test_codes_feed_the_products():
     """norm -> int8 codes -> moe_gemm_i8, and norm -> products by expert -> their gradients -> the norm's gradient."""
     T, H, N, E = 24, 512, 96, 3

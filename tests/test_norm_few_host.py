@@ -73,6 +73,12 @@ def test_workspace_sizes():
     assert few(4, 2048, 768, 64, 17) == few(4, 65552, 768, 8, 2) == few(4, 2048, 768, 1025, 8) == 0
 
 
+def test_few_workspace_where_one_expert_passes_four_gib():
+    few = moe.moe_ffn_few_workspace_bytes
+    assert few(1, 65536, 16384, 2, 1) > 0  # 2 GiB of int8 gate_up weights; bf16 ones are refused by the call
+    assert few(1, 65536, 32768, 2, 1) == 0  # 4 GiB of int8 ones: refused by both
+
+
 def test_python_refuses_before_the_library():
     x, w = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros(64, dtype=torch.bfloat16)
     for call in (lambda: moe.moe_rmsnorm_add(x, w, 1e-6), lambda: moe.moe_rmsnorm_add_grad(x, x, w, 1e-6),
