@@ -1748,10 +1748,10 @@ bool few_dims_ok(int32_t H, int32_t I) {
 }
 
 struct FewLayout {
-  size_t h, table, ids, w, total;
+  size_t h, table, ids, w, parts, total;
 };
 
-FewLayout few_layout(int64_t T, int64_t group, int64_t I, int64_t k) {
+FewLayout few_layout(int64_t T, int64_t group, int64_t H, int64_t I, int64_t k) {
   FewLayout L;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -1763,6 +1763,7 @@ FewLayout few_layout(int64_t T, int64_t group, int64_t I, int64_t k) {
   L.table = take((size_t)(8 + 8 * group * k) * 4);
   L.ids = take((size_t)(T * k) * 4);
   L.w = take((size_t)(T * k) * 4);
+  L.parts = take(H <= moe::kFewGroupsH ? (size_t)(moe::kFewGroups * group * H) * 4 : 0);
   L.total = off;
   return L;
 }
@@ -1786,7 +1787,7 @@ moe_status_t run_few(const uint16_t* x, const float* router_logits, int32_t T, i
       !aligned4(w2_s) || !aligned4(router_logits) || !aligned4(topk_ids_out) || !aligned4(topk_w_out))
     return fail(MOE_ERR_MISALIGNED, "%s: x, weights, y and workspace need 16-byte alignment, the others 4-byte", who);
   const int32_t group = few_group(T, H);
-  const FewLayout L = few_layout(T, group, I, k);
+  const FewLayout L = few_layout(T, group, H, I, k);
   if (workspace_bytes < L.total)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu B < required %zu B", who, workspace_bytes, L.total);
   char* ws = static_cast<char*>(workspace);
@@ -1795,7 +1796,7 @@ moe_status_t run_few(const uint16_t* x, const float* router_logits, int32_t T, i
   for (int32_t t = 0; t < T; t += group) {
     const moe::FewArgs a{x + (size_t)t * H, router_logits + (size_t)t * E, std::min(group, T - t), H, I, E, k, w13, w13_s, w2, w2_s,
                          reinterpret_cast<uint16_t*>(ws + L.h), reinterpret_cast<int32_t*>(ws + L.table), ids + t * k, w + t * k,
-                         y + (size_t)t * H};
+                         y + (size_t)t * H, reinterpret_cast<float*>(ws + L.parts)};
     const hipError_t e = moe::launch_ffn_few(a, i8, s);
     if (e != hipSuccess) return hip_status(e, who);
   }
@@ -1808,7 +1809,7 @@ size_t moe_ffn_few_workspace_bytes(int32_t T, int32_t H, int32_t I, int32_t E, i
   if (T < 1 || T > MOE_FEW_MAX_TOKENS || !few_dims_ok(H, I) || !ragged_ffn_weights_ok(H, I, true) || E < 1 || k < 1 || k > E ||
       k > MOE_FEW_MAX_K || E > MOE_MAX_EXPERTS)
     return 0;
-  return few_layout(T, few_group(T, H), I, k).total;
+  return few_layout(T, few_group(T, H), H, I, k).total;
 }
 
 moe_status_t moe_ffn_few_w16(const uint16_t* x, const float* router_logits, int32_t T, int32_t H, int32_t I, int32_t E,

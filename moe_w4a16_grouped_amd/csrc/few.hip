@@ -419,10 +419,12 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   FewEntry* table = reinterpret_cast<FewEntry*>(reinterpret_cast<char*>(few_lds) + NW * TOK * kHRow);
   float* weight = reinterpret_cast<float*>(table + R);
   f32x4* out = reinterpret_cast<f32x4*>(weight + (R + 3) / 4 * 4);  // [pieces][R][COLS / 4]
-  const int col0 = blockIdx.x * COLS;
+  const int groups = p.groups, group = blockIdx.y, col0 = blockIdx.x * COLS;
   const int n = __builtin_amdgcn_readfirstlane(p.table[0]);
   if (tid < 2 * R) reinterpret_cast<u32x4*>(table)[tid] = reinterpret_cast<const u32x4*>(p.table)[2 + tid];
   if (tid < R) weight[tid] = p.weight[tid];
+  if (groups > 1)  // what other groups add counts as zero here
+    for (int i = tid; i < (R << shift) * (COLS / 4); i += 64 * NW) out[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
 
   constexpr int C = SUPER / LINE / W::LANE;  // steps of a super-chunk
@@ -434,16 +436,16 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   const uint32_t lane_offset = (uint32_t)m * row_bytes + in_line * 16;
   const char* hfrag = stage + min(m, TOK - 1) * kHRow + in_line * (W::PARTS * 32);
   struct Cursor {
-    int unit, super, left;
+    int i, unit, super, left;
   };
-  const int turn = (blockIdx.x >> 3) % (supers >> shift);
-  auto begin = [&](int unit) {
+  const int turn = (blockIdx.x >> 3) % (supers >> shift), worker = wave + NW * group, workers = NW * groups;
+  auto begin = [&](int i, int unit) {
     const int piece = unit & (pieces - 1);
-    return Cursor{unit, piece + (turn << shift), (supers - piece + pieces - 1) >> shift};
+    return Cursor{i, unit, piece + (turn << shift), (supers - piece + pieces - 1) >> shift};
   };
   auto advance = [&](Cursor& c) {
     if (--c.left == 0) {
-      c = begin(c.unit + NW);
+      c = begin(c.i + 1, c.unit + workers);
       return;
     }
     c.super += pieces;
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   f32x4 sc[RING][CT];
   const uint32_t expert_bytes = (uint32_t)H * row_bytes;
   // lane i holds what the wave's i-th unit needs (there are at most 64), so that no unit waits for LDS
-  const FewEntry& own = table[min((wave + NW * lane) >> shift, n - 1)];
+  const FewEntry& own = table[min((worker + workers * lane) >> shift, n - 1)];
   const int own_expert = own.expert, own_rows = own.rows;
   uint32_t own_row[(TOK + 1) / 2];
 #pragma unroll
@@ -461,8 +463,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   auto row_of = [&](int i, int j) { return (__builtin_amdgcn_readlane(own_row[j >> 1], i) >> (16 * (j & 1))) & 0xFFFFu; };
   auto load = [&](const Cursor& c, int b) {
     if (c.unit >= units) return;
-    const int i = c.unit / NW;
-    const int e = __builtin_amdgcn_readlane(own_expert, i), rows = __builtin_amdgcn_readlane(own_rows, i);
+    const int e = __builtin_amdgcn_readlane(own_expert, c.i), rows = __builtin_amdgcn_readlane(own_rows, c.i);
     const auto buffer = few_buffer(static_cast<const char*>(p.w2) + (size_t)e * expert_bytes, expert_bytes);
     const uint32_t offset = lane_offset + (uint32_t)col0 * row_bytes + c.super * (SUPER * W::BYTES);
 #pragma unroll
@@ -472,7 +473,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
 #pragma unroll
     for (int j = 0; j < TOK; ++j)
       if (j < rows) {
-        const auto hrow = few_buffer(p.h + (size_t)row_of(i, j) * I * 2, (uint32_t)I * 4);
+        const auto hrow = few_buffer(p.h + (size_t)row_of(c.i, j) * I * 2, (uint32_t)I * 4);
 #pragma unroll
         for (int v = 0; v < HB; ++v) hv[b][j][v] = few_load(hrow, lane * 16 + c.super * (SUPER * 4) + v * 1024);
       }
@@ -482,7 +483,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
       for (int ct = 0; ct < CT; ++ct) sc[b][ct] = __builtin_bit_cast(f32x4, few_load(scales, (col0 + ct * MR + (MR == 8 ? 4 * (q & 1) : 0)) * 4));
     }
   };
-  Cursor use = begin(wave), ahead = use;
+  Cursor use = begin(0, worker), ahead = use;
 #pragma unroll
   for (int b = 0; b < RING; ++b) {
     load(ahead, b);
@@ -495,7 +496,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
 #pragma unroll
     for (int b = 0; b < RING; ++b) {
       if (use.unit >= units) goto summed;
-      const int rows = __builtin_amdgcn_readlane(own_rows, use.unit / NW);
+      const int rows = __builtin_amdgcn_readlane(own_rows, use.i);
       const bool last = use.super == supers - 1 && ragged;  // weights past the row count as zeros; h past its end was read so
       if (last) {
 #pragma unroll
@@ -553,10 +554,11 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   }
 summed:
   __syncthreads();
-  if (tid < COLS * T) {
-    const int t = tid / COLS, c = tid % COLS;
+  const int t = tid / COLS, c = tid % COLS;
+  const bool mine = tid < COLS * T;
+  float y = 0.f;
+  if (mine) {
     const float* o8 = reinterpret_cast<const float*>(out) + c;
-    float y = 0.f;
     for (int s = 0; s < k; s += 4) {  // four slots' values are asked for at a time; their sum is that of the slots in order
       float o[4], w[4];
 #pragma unroll
@@ -570,17 +572,37 @@ summed:
       for (int j = 0; j < 4; ++j)
         if (s + j < k && w[j] != 0.f) y = fmaf(w[j], o[j], y);  // a closed expert may hold anything
     }
-    p.y[(size_t)t * H + col0 + c] = f32_to_bf16_bits(y);
   }
+  if (!mine) return;
+  const size_t at = (size_t)t * H + col0 + c;
+  if (groups > 1) p.parts[(size_t)group * T * H + at] = y;
+  else p.y[at] = f32_to_bf16_bits(y);
 }
 
-// Pieces (a power of two) of the contraction that a second launch's units are cut into, so that the waves of a workgroup have
-// one each even where a single token chose fewer experts; no more than there are super-chunks.  At most 64 units a wave.
-static int few_pieces_shift(int k, int I, int super, int waves) {
-  const int supers = (I + super - 1) / super;
-  int shift = 0;
-  while ((k << shift) < waves && (2 << shift) <= supers && shift < 3) ++shift;
-  return shift;
+// y from the parts of the second launch's groups, in their order.
+__global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__ parts, int groups, int n, uint16_t* __restrict__ y) {
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int g = 0; g < groups; g += 4) {
+    f32x4 a[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const f32x4*>(parts + (size_t)min(g + j, groups - 1) * n + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (g + j < groups) v += a[j];
+  }
+  const u32x2 o = {f32_to_bf16_bits(v[0]) | (uint32_t)f32_to_bf16_bits(v[1]) << 16, f32_to_bf16_bits(v[2]) | (uint32_t)f32_to_bf16_bits(v[3]) << 16};
+  *reinterpret_cast<u32x2*>(y + i) = o;
+}
+
+// Entries that the second launch has to expect: of one token exactly its k, of more the distinct experts of even routing, or
+// what the entries' rows make of all slots.
+static double few_entries(const FewArgs& p) {
+  if (p.T == 1) return p.k;
+  double spared = 1.0;
+  for (int t = 0; t < p.T; ++t) spared *= 1.0 - (double)p.k / p.E;
+  return std::max(p.E * (1.0 - spared), (double)(p.T * p.k) / p.entry_rows);
 }
 
 template <class W, int NJ, bool ONE, bool ALONE>
@@ -613,14 +635,29 @@ static hipError_t launch_few_of(const FewArgs& p, hipStream_t s) {
 
 template <class W, int COLS, int SUPER, int TOK, int RING, int NW>
 static hipError_t launch_few_second(FewArgs p, hipStream_t s) {
-  p.pieces_shift = few_pieces_shift(p.k, p.I, SUPER, NW);
-  const int R = p.T * p.k, lds = NW * TOK * (SUPER * 4 + 16) + R * 32 + (R + 3) / 4 * 16 + (R << p.pieces_shift) * 4 * COLS;
+  const int R = p.T * p.k, supers = (p.I + SUPER - 1) / SUPER, columns = p.H / COLS;
+  const double entries = few_entries(p);
+  // Groups of workgroups that share the units of the same columns where there are few columns and many units: a wave's super-chunk
+  // takes about 0.9 us, the third launch that adds the groups' parts 4.5 (11 tokens, 118 experts top-8, int8 224 x 13712: 201 us
+  // down in one group, 62 in eight; 10 tokens, 46 experts top-9, bf16 592 x 5280: 89 and 73).
+  if (p.H <= kFewGroupsH && entries * supers > 16.0 * NW) p.groups = std::max(1, std::min(kFewGroups, 640 / columns));
+  // Pieces (a power of two) of the contraction that units are cut into, no more than there are super-chunks: one token's entries,
+  // all alike, until every wave has a unit; of more tokens until there are about 32, so that the waves end together (9 tokens, 10
+  // experts top-8, int8 1760 x 4672: 50 us uncut, 42 in quarters).  At most 64 units a wave.
+  const double want = p.T == 1 ? NW * p.groups : 30;
+  while (entries * (1 << p.pieces_shift) < want && (2 << p.pieces_shift) <= supers && (R << p.pieces_shift) < 64 * NW) ++p.pieces_shift;
+  const int lds = NW * TOK * (SUPER * 4 + 16) + R * 32 + (R + 3) / 4 * 16 + (R << p.pieces_shift) * 4 * COLS;
   const auto kernel = few_down_kernel<W, COLS, SUPER, TOK, RING, NW>;
   if (lds > (64 << 10)) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  kernel<<<p.H / COLS, 64 * NW, lds, s>>>(p);
+  kernel<<<dim3(columns, p.groups), 64 * NW, lds, s>>>(p);
+  if (p.groups > 1) {
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const int n = p.T * p.H;
+    few_join_kernel<<<(n / 4 + 255) / 256, 256, 0, s>>>(p.parts, p.groups, n, p.y);
+  }
   return hipGetLastError();
 }
 
@@ -651,6 +688,8 @@ static hipError_t launch_few_w(FewArgs p, hipStream_t s) {
   if (narrow) return launch_few_second<W, 4, 512, 4, 2, 8>(p, s);
   // int8 units are half as long in bytes and convert their weights: twice the waves (16 tokens, 256 experts top-8, 2048 x 512:
   // 24 us against 26; bf16, 8 tokens, 128 experts, 2048 x 768: 32 us against 31, so not there)
+  // and from 4096 columns on 16 columns (4 tokens, 256 experts top-8, 7168 x 2048: 85 us against 91; bf16 5120 x 1040: 82 against 68)
+  if (W::SCALED && p.H >= 4096) return launch_few_second<W, 16, 256, 4, 2, 8>(p, s);
   if (W::SCALED) return launch_few_second<W, 8, 256, 4, 2, 16>(p, s);
   return launch_few_second<W, 8, 256, 4, 3, 8>(p, s);
 }

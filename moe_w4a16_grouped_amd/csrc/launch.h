@@ -206,6 +206,7 @@ hipError_t launch_silu_mul_grad(const uint16_t* G, const uint16_t* dh, bool f16,
                                 hipStream_t stream);
 
 // The layer for at most 16 tokens in two launches (few.hip).
+constexpr int kFewGroups = 8, kFewGroupsH = 1024;  // groups of the second launch at most, and the H up to which there are any
 struct FewArgs {
   const uint16_t* x;     // bf16 [T, H]
   const float* logits;   // [T, E]
@@ -219,8 +220,9 @@ struct FewArgs {
   int32_t* ids;          // [T, k]
   float* weight;         // [T, k]
   uint16_t* y;           // bf16 [T, H]
-  int entry_rows = 0;    // an entry's rows at most, and log2 of the pieces of an entry: set by the launch
-  int pieces_shift = 0;
+  float* parts;          // [groups, T, H], where the second launch's workgroups share their columns in groups
+  // set by the launch: an entry's rows at most, log2 of the pieces of an entry, groups of the second launch
+  int entry_rows = 0, pieces_shift = 0, groups = 1;
 };
 hipError_t launch_ffn_few(const FewArgs& a, bool i8, hipStream_t stream);
 

@@ -211,6 +211,22 @@ def test_mixes_of_the_rules(T, E, k, H, I, int8):
     L.check(L.run())
 
 
+@pytest.mark.parametrize("int8", [False, True], ids=["w16", "w8a16"])
+@pytest.mark.parametrize("T,E,k,H,I", [(11, 60, 8, 224, 2064), (1, 20, 10, 240, 10256), (14, 4, 4, 160, 5024), (16, 64, 16, 1024, 1552), (2, 150, 16, 16, 8208)])
+def test_groups_of_the_second_launch(T, E, k, H, I, int8):
+    """Few columns and a long contraction: workgroups share the columns' units, and a third launch adds their parts."""
+    L = Layer(T, E, k, H, I, int8, seed=T + k)
+    ws = torch.full((moe.moe_ffn_few_workspace_bytes(T, H, I, E, k),), 0xFF, dtype=torch.uint8, device="cuda")
+    y = L.run(workspace=ws)
+    L.check(y)
+    assert torch.equal(L.run(workspace=ws), y)
+    L.logits[:, 0] = float("-inf")  # a closed expert holds anything (where E is k it is chosen, with weight 0: 0 * NaN in the reference)
+    y = L.run()
+    L.check(y)
+    L.w2.view(torch.uint8 if int8 else torch.int16)[0] = 0x7F if int8 else 0x7FC0
+    assert torch.equal(L.run(), y)
+
+
 def test_scales_on_four_bytes():
     """Scales need four bytes of alignment only."""
     for T, E, k, H, I in ((12, 20, 4, 256, 112), (1, 20, 4, 2048, 64), (1, 20, 4, 256, 640)):
