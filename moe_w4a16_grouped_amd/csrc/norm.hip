@@ -415,8 +415,13 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
 
 template <bool F16, bool WF32, int QUANT, int PAST>
 static hipError_t launch_norm_past(const NormArgs& p, hipStream_t s) {
+  // Threads a row so that few are idle and few barriers join them.  Up to 512 columns a wave holds a row; up to 1024 two waves'
+  // worth, where there are rows enough for all CUs (4985 x 768 to int8 7.1 us, a workgroup a row 9.6; 4096 x 1024 to FP8 9.6 and
+  // 11.1; of 16 to 64 rows 3.3 to 3.8 and 2.9 to 3.2).  Beyond that a workgroup a row: four chunks a wave are slower (801 x 2048
+  // 5.4 us against 4.5, 4096 x 2048 9.4 against 7.7), and so are 512 threads up to 4096 columns (4096 x 2048 to FP8 17.7 against 15.1).
   const dim3 grid = grid2d(p.T), grid4 = grid2d(((long long)p.T + 3) / 4);
-  if (p.H <= 512) rmsnorm_kernel<F16, WF32, QUANT, 64, 1, PAST><<<grid4, 256, 0, s>>>(p);
+  if (p.H > 512 && p.H <= 1024 && p.T >= 2048) rmsnorm_kernel<F16, WF32, QUANT, 64, 2, PAST><<<grid4, 256, 0, s>>>(p);
+  else if (p.H <= 512) rmsnorm_kernel<F16, WF32, QUANT, 64, 1, PAST><<<grid4, 256, 0, s>>>(p);
   else if (p.H <= 2048) rmsnorm_kernel<F16, WF32, QUANT, 256, 1, PAST><<<grid, 256, 0, s>>>(p);
   else if (p.H <= 4096) rmsnorm_kernel<F16, WF32, QUANT, 256, 2, PAST><<<grid, 256, 0, s>>>(p);
   else if (p.H <= 8192 && QUANT == kQuantNone) rmsnorm_kernel<F16, WF32, QUANT, 1024, 1, PAST><<<grid, 1024, 0, s>>>(p);

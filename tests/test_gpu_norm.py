@@ -89,6 +89,18 @@ def test_norm(T, H, x_dtype, w_dtype, quant, want_y):
         _check(x, residual, w, 1e-5, quant, want_y, got)
 
 
+@pytest.mark.parametrize("H,quant", [(520, NONE), (528, I8), (768, I8), (640, F8), (1024, F8), (1024, NONE)])
+def test_many_short_rows(H, quant):
+    """Rows enough that a wave takes each, of ordinary and of far magnitudes."""
+    T = 2050
+    x, r, w = _rand((T, H), BF16, 1), _rand((T, H), BF16, 2), _weight(H, BF16, 3)
+    for at, f in ((0, 1e30), (5, 1e-36), (1027, 1e20), (T - 1, 0.0)):
+        x[at] *= f
+        r[at] *= f
+    for residual in (None, r):
+        _check(x, residual, w, 1e-5, quant, True, moe.moe_rmsnorm_add(x, w, 1e-5, residual=residual, quant=quant))
+
+
 def test_int8_ties():
     """Quotients on and next to a half: the largest product is 127 * 2^6, so that 127 z / max is z / 64, and weights in fp32
     move a product by its last bit to either side."""
