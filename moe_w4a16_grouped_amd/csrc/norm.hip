@@ -156,22 +156,16 @@ __device__ __forceinline__ void weight8(const u32x4 (&raw)[WF32 ? 2 : 1], float 
   }
 }
 
-template <int PAST>
-__device__ __forceinline__ void store8(const u32x2& v, u32x2* p) {
-  if (PAST > 0) __builtin_nontemporal_store(v, p);
-  else *p = v;
-}
-
 constexpr int kQuantNone = MOE_QUANT_NONE, kQuantI8 = MOE_QUANT_I8, kQuantF8 = MOE_QUANT_F8;
 
 // s of chunk c (8 columns) of a row: x, or x + residual rounded to the type.
-template <bool F16, int PAST>
+template <bool F16>
 __device__ __forceinline__ u32x4 sum8(const NormArgs& p, size_t at) {
-  u32x4 v = load16<PAST>(static_cast<const u32x4*>(p.x) + at);
+  u32x4 v = static_cast<const u32x4*>(p.x)[at];
   if (p.residual) {
     float a[8], b[8];
     unpack8<F16>(v, a);
-    unpack8<F16>(load16<PAST>(static_cast<const u32x4*>(p.residual) + at), b);
+    unpack8<F16>(static_cast<const u32x4*>(p.residual)[at], b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] += b[j];
     v = pack8<F16>(a);
@@ -285,8 +279,9 @@ __device__ __forceinline__ u32x2 norm_codes8(const float (&s)[8], const float (&
   return some ? c : u32x2{0u, 0u};
 }
 
-// A chunk's outputs.
-template <bool F16, bool WF32, int QUANT, int PAST>
+// A chunk's outputs.  All stores of this kernel go past the L2, which they would only clear of rows to be read (5000 x 4096 to FP8
+// 32.2 us against 35.5, 4096 x 2048 15.2 against 16.8, 8191 x 4096 55.9 against 57.6, 801 x 2048 4.5 both ways).
+template <bool F16, bool WF32, int QUANT>
 __device__ __forceinline__ void norm_store(const NormArgs& p, const u32x4& sv, const u32x4 (&wv)[WF32 ? 2 : 1], float r,
                                            double zmax, bool some, bool fast, bool quick, size_t at) {
   float s[8], w[8];
@@ -298,14 +293,14 @@ __device__ __forceinline__ void norm_store(const NormArgs& p, const u32x4& sv, c
   if (p.y) {  // z r, or, where z may pass fp32, s r w
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = QUANT != kQuantNone && fast ? z[j] * r : s[j] * r * w[j];
-    store16<PAST>(pack8<F16>(y), static_cast<u32x4*>(p.y) + at);
+    store16<1>(pack8<F16>(y), static_cast<u32x4*>(p.y) + at);
   }
-  if constexpr (QUANT != kQuantNone) store8<PAST>(norm_codes8<QUANT>(s, w, z, zmax, some, quick), static_cast<u32x2*>(p.q) + at);
+  if constexpr (QUANT != kQuantNone) __builtin_nontemporal_store(norm_codes8<QUANT>(s, w, z, zmax, some, quick), static_cast<u32x2*>(p.q) + at);
 }
 
 // TH threads a row (64: a wave, four rows a workgroup), NC chunks of 8 columns a thread, held between the sums and the
 // outputs.
-template <bool F16, bool WF32, int QUANT, int TH, int NC, int PAST>
+template <bool F16, bool WF32, int QUANT, int TH, int NC>
 __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p) {
   constexpr int kRows = TH < 256 ? 256 / TH : 1, kWaves = TH / 64;
   static_assert(TH >= 256 || TH == 64, "whole waves, or one, a row");
@@ -321,7 +316,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
   for (int j = 0; j < NC; ++j) {
     const int c = t + j * TH;
     if (c < nc) {
-      sv[j] = sum8<F16, PAST>(p, base + c);
+      sv[j] = sum8<F16>(p, base + c);
       load_weight8<WF32>(p.w, c, wv[j]);
     }
   }
@@ -353,7 +348,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
     blk[j] = 0.0;
     blk_bits[j] = 0u;
     if (c < nc) {
-      if (p.residual) store16<PAST>(sv[j], static_cast<u32x4*>(p.s) + base + c);
+      if (p.residual) store16<1>(sv[j], static_cast<u32x4*>(p.s) + base + c);
       norm_gather<F16, WF32, QUANT>(sv[j], wv[j], ss, blk_bits[j], blk[j]);
     }
     bits = max(bits, blk_bits[j]);
@@ -408,32 +403,26 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
         if ((lane & 15) == 0) p.q_scale[(size_t)row * (nc / 16) + c / 16] = scale;
         quick = fast && zmax >= 0x1p-60;
       }
-      norm_store<F16, WF32, QUANT, PAST>(p, sv[j], wv[j], r, zmax, scale > 0.f, fast, quick, base + c);
+      norm_store<F16, WF32, QUANT>(p, sv[j], wv[j], r, zmax, scale > 0.f, fast, quick, base + c);
     }
   }
 }
 
-template <bool F16, bool WF32, int QUANT, int PAST>
-static hipError_t launch_norm_past(const NormArgs& p, hipStream_t s) {
+template <bool F16, bool WF32, int QUANT>
+static hipError_t launch_norm_of(const NormArgs& p, hipStream_t s) {
   // Threads a row so that few are idle and few barriers join them.  Up to 512 columns a wave holds a row; up to 1024 two waves'
   // worth, where there are rows enough for all CUs (4985 x 768 to int8 7.1 us, a workgroup a row 9.6; 4096 x 1024 to FP8 9.6 and
   // 11.1; of 16 to 64 rows 3.3 to 3.8 and 2.9 to 3.2).  Beyond that a workgroup a row: four chunks a wave are slower (801 x 2048
-  // 5.4 us against 4.5, 4096 x 2048 9.4 against 7.7), and so are 512 threads up to 4096 columns (4096 x 2048 to FP8 17.7 against 15.1).
+  // 5.4 us against 4.5, 4096 x 2048 9.4 against 7.7), and so are 512 threads up to 4096 columns (4096 x 2048 to FP8 17.7 against
+  // 15.1) and 1024 up to 8192 (2000 x 8192 to FP8 29.2 against 24.7).
   const dim3 grid = grid2d(p.T), grid4 = grid2d(((long long)p.T + 3) / 4);
-  if (p.H > 512 && p.H <= 1024 && p.T >= 2048) rmsnorm_kernel<F16, WF32, QUANT, 64, 2, PAST><<<grid4, 256, 0, s>>>(p);
-  else if (p.H <= 512) rmsnorm_kernel<F16, WF32, QUANT, 64, 1, PAST><<<grid4, 256, 0, s>>>(p);
-  else if (p.H <= 2048) rmsnorm_kernel<F16, WF32, QUANT, 256, 1, PAST><<<grid, 256, 0, s>>>(p);
-  else if (p.H <= 4096) rmsnorm_kernel<F16, WF32, QUANT, 256, 2, PAST><<<grid, 256, 0, s>>>(p);
-  else if (p.H <= 8192 && QUANT == kQuantNone) rmsnorm_kernel<F16, WF32, QUANT, 1024, 1, PAST><<<grid, 1024, 0, s>>>(p);
-  else if (p.H <= 8192) rmsnorm_kernel<F16, WF32, QUANT, 512, 2, PAST><<<grid, 512, 0, s>>>(p);
-  else rmsnorm_kernel<F16, WF32, QUANT, 1024, 2, PAST><<<grid, 1024, 0, s>>>(p);
+  if (p.H > 512 && p.H <= 1024 && p.T >= 2048) rmsnorm_kernel<F16, WF32, QUANT, 64, 2><<<grid4, 256, 0, s>>>(p);
+  else if (p.H <= 512) rmsnorm_kernel<F16, WF32, QUANT, 64, 1><<<grid4, 256, 0, s>>>(p);
+  else if (p.H <= 2048) rmsnorm_kernel<F16, WF32, QUANT, 256, 1><<<grid, 256, 0, s>>>(p);
+  else if (p.H <= 4096) rmsnorm_kernel<F16, WF32, QUANT, 256, 2><<<grid, 256, 0, s>>>(p);
+  else if (p.H <= 8192) rmsnorm_kernel<F16, WF32, QUANT, 512, 2><<<grid, 512, 0, s>>>(p);
+  else rmsnorm_kernel<F16, WF32, QUANT, 1024, 2><<<grid, 1024, 0, s>>>(p);
   return hipGetLastError();
-}
-
-template <bool F16, bool WF32, int QUANT>
-static hipError_t launch_norm_of(const NormArgs& p, hipStream_t s) {
-  const long long bytes = (long long)p.T * p.H * (2 + (p.residual ? 4 : 0) + (p.y ? 2 : 0) + (QUANT != kQuantNone ? 1 : 0));
-  return bytes < kFarBytes ? launch_norm_past<F16, WF32, QUANT, 1>(p, s) : launch_norm_past<F16, WF32, QUANT, 0>(p, s);
 }
 
 template <bool F16, bool WF32>
@@ -545,7 +534,8 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormG
           if (p.ds) o[i] += a[i];
           dw[j][i] = fmaf(d[i], xhat, dw[j][i]);
         }
-        static_cast<u32x4*>(p.dx)[base + c] = pack8<F16>(o);
+        // past the L2 (8191 x 4096 48.5 us against 51.3, 8192 x 2048 28.6 both ways)
+        store16<1>(pack8<F16>(o), static_cast<u32x4*>(p.dx) + base + c);
       }
     }
   }
@@ -608,8 +598,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restric
   else static_cast<uint16_t*>(dw)[at] = out == MOE_OUT_F16 ? f32_to_f16_bits(r) : f32_to_bf16_bits(r);
 }
 
-// Threads a row of the gradient's workgroups, and the workgroups: as many as the card holds at once, so that few parts are left
-// to add.
+// Threads a row of the gradient's workgroups: one chunk of 8 columns each (8192 x 512: a wave a row 10.1 us, 256 threads 13.0; 8192 x
+// 2048: 256 threads 27.5, 512 27.9, 1024 34.4; 8191 x 4096: 512 threads 50.6, 256 of two chunks 55.7, 1024 57.1; 4096 x 8192: 1024
+// threads 51.1, 512 of two chunks 54.2).  Workgroups: as many as the card holds at once, so that few parts are left to add.
 static int grad_threads(int H) { return H <= 512 ? 64 : (H <= 2048 ? 256 : (H <= 4096 ? 512 : 1024)); }
 
 int rmsnorm_grad_parts(int T, int H) {
