@@ -800,7 +800,8 @@ moe_status_t moe_rmsnorm_add_grad(const void* dy, const void* s, int32_t dtype, 
  * finite; a slot whose weight is 0 adds nothing, whatever its expert holds.  y bf16 [T, H] out, rounded once: h keeps about
  * 16 significant bits and all sums are fp32.  topk_ids_out int32 [T, k], topk_w_out fp32 [T, k]: optional copies of the
  * routing (NULL = skip).  workspace: at least moe_ffn_few_workspace_bytes(T, H, I, E, k) bytes, of one call at a time.
- * Where T * H passes 65536 the tokens are taken in groups that do not, each with its two launches (and its own reading
+ * (Where H <= 1024 and the experts' contraction is long, a third, small launch adds what workgroups share.)
+ * Where T * H passes 65536 the tokens are taken in groups that do not, each with its own launches (and its own reading
  * of the weights).
  * Shapes: 0 <= T <= MOE_FEW_MAX_TOKENS, 1 <= k <= min(E, MOE_FEW_MAX_K), E <= MOE_MAX_EXPERTS, H and I multiples of
  * 16, 16 <= H <= 65536, 16 <= I <= MOE_I8_MAX_K, one expert's gate_up weights below 4 GiB.  Alignment: x, weights, y and

@@ -12,6 +12,11 @@
 // significant bits), and of a quotient next to a border between two codes the exact products top z and border max |z|
 // are compared.  Squares are added by fours in fp32 and the rest in 64 bits; rows that leave
 // the middle of fp32's range go through 64 bits altogether, which no 16-bit value overflows.
+//
+// Bound by memory: a row is read once, held in registers between its sums and its outputs, and s, y, codes and scales are
+// written from there.  8191 x 4096 with a residual to FP8 55 us (302 MB, 5.5 TB/s; 50 % of the issue slots are the vector
+// unit's, and a large addition of two tensors runs at 6.3 TB/s); 801 x 2048 to int8 4.3 us, one row 2.2 us (from Python 8.9 and
+// 11 us: the call's checks, outputs and launch).  The gradient of 8191 x 4096 with ds 48.5 + 4 us (268 MB, 5.5 TB/s).
 #include <algorithm>
 
 #include "launch.h"
@@ -295,7 +300,8 @@ __device__ __forceinline__ void norm_store(const NormArgs& p, const u32x4& sv, c
     for (int j = 0; j < 8; ++j) y[j] = QUANT != kQuantNone && fast ? z[j] * r : s[j] * r * w[j];
     store16<1>(pack8<F16>(y), static_cast<u32x4*>(p.y) + at);
   }
-  if constexpr (QUANT != kQuantNone) __builtin_nontemporal_store(norm_codes8<QUANT>(s, w, z, zmax, some, quick), static_cast<u32x2*>(p.q) + at);
+  if constexpr (QUANT != kQuantNone)
+    __builtin_nontemporal_store(norm_codes8<QUANT>(s, w, z, zmax, some, quick), static_cast<u32x2*>(p.q) + at);
 }
 
 // TH threads a row (64: a wave, four rows a workgroup), NC chunks of 8 columns a thread, held between the sums and the
