@@ -169,12 +169,13 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _empty(shape, dtype, dev, stream=None, keep=True):
+def _empty(shape, dtype, dev, stream=None, keep=True, like=None):
     """Memory that a wrapper makes for its call belongs to the stream of the call: a block that the current stream's
     allocator gives may still be in use by work queued there, which another stream does not wait for.  keep: the caller
-    gets the tensor, and may use and free it on the current stream too (once that waits for the given one)."""
+    gets the tensor, and may use and free it on the current stream too (once that waits for the given one).  like: a
+    tensor of the shape and device, from which torch makes another faster."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else torch.empty_like(like, dtype=dtype)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=dev)
     if keep:
@@ -1004,7 +1005,7 @@ def _made_like(made, x, dtype, name, stream):
     if made is not None:
         _need(made, (dtype,), tuple(x.shape), name, x.device)
         return made
-    return torch.empty_like(x, dtype=dtype) if stream is None else _empty(x.shape, dtype, x.device, stream)
+    return _empty(x.shape, dtype, x.device, stream, like=x)
 
 
 def moe_rmsnorm_add(x, weight, eps: float, residual=None, quant: int = MOE_QUANT_NONE, want_y: bool = True, s=None, y=None,
