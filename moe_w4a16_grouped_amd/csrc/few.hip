@@ -64,7 +64,8 @@ struct FewW8 {
   __device__ static __forceinline__ bf16x8 part(const u32x4& w, int i) { return i8x8_to_bf16(w[2 * i], w[2 * i + 1]); }
 };
 
-// 16 bytes at an offset of a buffer; past its end zeros.
+// 16 bytes at an offset of a buffer; past its end (kFewPast in all of them) zeros, for which no bytes move.
+constexpr uint32_t kFewPast = 0xFFFFFFF0u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t few_buffer(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00027000);
 }
@@ -283,6 +284,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
   const int chunks = (share + C - 1) / C, blocks = I / 8;
   const int first = ALONE ? 0 : wave * share * STEP;             // of the contraction
   const int whole = max(0, min(share, (H - first) / STEP)) / C;  // chunks that lie within the share and the row
+  const int some = min(share, (H - first + STEP - 1) / STEP);    // steps of which any lane's part does; others are not loaded (4
+                                                                 // tokens, 68 experts top-9, int8 2112 x 2416: 74 us with them, 64)
   const uint32_t row_bytes = (uint32_t)H * W::BYTES;
   const uint32_t lane_offset = (uint32_t)(l16 < 8 ? l16 : I + l16 - 8) * row_bytes + (first + q * W::LANE) * W::BYTES;
   const char* xrow = xs + min(l16, T - 1) * xstride + (first + q * W::LANE) * 2;
@@ -308,7 +311,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
     const auto buffer = few_buffer(static_cast<const char*>(p.w13) + (size_t)e * expert_bytes, expert_bytes);
     const uint32_t offset = lane_offset + (uint32_t)c.block * 8 * row_bytes + c.chunk * (C * STEP * W::BYTES);
 #pragma unroll
-    for (int i = 0; i < C; ++i) ring[b][i] = few_load(buffer, offset + i * (STEP * W::BYTES));
+    for (int i = 0; i < C; ++i) ring[b][i] = few_load(buffer, c.chunk * C + i < some ? offset + i * (STEP * W::BYTES) : kFewPast);
     if constexpr (W::SCALED && ALONE) if (c.chunk == chunks - 1) {
       const auto scales = few_buffer(p.w13_s + (size_t)e * (2 * I), (uint32_t)I * 8);
       sg[b] = __builtin_bit_cast(Scales, few_load(scales, (c.block * 8 + 4 * (q & 1)) * 4));
@@ -430,7 +433,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   FewEntry* table = reinterpret_cast<FewEntry*>(reinterpret_cast<char*>(few_lds) + NW * TOK * kHRow);
   float* weight = reinterpret_cast<float*>(table + R);
   f32x4* out = reinterpret_cast<f32x4*>(weight + (R + 3) / 4 * 4);  // [pieces][R][COLS / 4]
-  const int groups = p.groups, group = blockIdx.y, col0 = blockIdx.x * COLS;
+  const int groups = p.groups, group = blockIdx.y, col0 = blockIdx.x * p.cols, cols = min(p.cols, H - col0);
   const int n = __builtin_amdgcn_readfirstlane(p.table[0]);
   if (tid < 2 * R) reinterpret_cast<u32x4*>(table)[tid] = reinterpret_cast<const u32x4*>(p.table)[2 + tid];
   if (tid < R) weight[tid] = p.weight[tid];
@@ -444,7 +447,11 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   const bool ragged = I % SUPER != 0;
   const int m = l16 & (MR - 1), in_line = q * SPLIT + l16 / MR;
   const uint32_t row_bytes = (uint32_t)I * W::BYTES;
-  const uint32_t lane_offset = (uint32_t)m * row_bytes + in_line * 16;
+  const uint32_t expert_bytes = (uint32_t)H * row_bytes;
+  uint32_t lane_offset[CT];  // rows that are another workgroup's are past the end: no bytes move for them
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct)
+    lane_offset[ct] = ct * MR + m < cols ? (uint32_t)(col0 + ct * MR + m) * row_bytes + in_line * 16 : expert_bytes;
   const char* hfrag = stage + min(m, TOK - 1) * kHRow + in_line * (W::PARTS * 32);
   struct Cursor {
     int i, unit, super, left;
@@ -464,7 +471,6 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
   };
   u32x4 ring[RING][CT][C], hv[RING][TOK][HB];
   f32x4 sc[RING][CT];
-  const uint32_t expert_bytes = (uint32_t)H * row_bytes;
   // lane i holds what the wave's i-th unit needs (there are at most 64), so that no unit waits for LDS
   const FewEntry& own = table[min((worker + workers * lane) >> shift, n - 1)];
   const int own_expert = own.expert, own_rows = own.rows;
@@ -476,11 +482,11 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
     if (c.unit >= units) return;
     const int e = __builtin_amdgcn_readlane(own_expert, c.i), rows = __builtin_amdgcn_readlane(own_rows, c.i);
     const auto buffer = few_buffer(static_cast<const char*>(p.w2) + (size_t)e * expert_bytes, expert_bytes);
-    const uint32_t offset = lane_offset + (uint32_t)col0 * row_bytes + c.super * (SUPER * W::BYTES);
+    const uint32_t offset = c.super * (SUPER * W::BYTES);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < C; ++i) ring[b][ct][i] = few_load(buffer, offset + ct * MR * row_bytes + i * (LINE * 16));
+      for (int i = 0; i < C; ++i) ring[b][ct][i] = few_load(buffer, lane_offset[ct] + offset + i * (LINE * 16));
 #pragma unroll
     for (int j = 0; j < TOK; ++j)
       if (j < rows) {
@@ -567,7 +573,7 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewArgs p) {
 summed:
   __syncthreads();
   const int t = tid / COLS, c = tid % COLS;
-  const bool mine = tid < COLS * T;
+  const bool mine = tid < COLS * T && c < cols;
   float y = 0.f;
   if (mine) {
     const float* o8 = reinterpret_cast<const float*>(out) + c;
@@ -610,6 +616,15 @@ __global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__
   *reinterpret_cast<u32x2*>(y + i) = u32x2{o[0] | o[1] << 16, o[2] | o[3] << 16};
 }
 
+// Columns of a workgroup of the second launch, at most `most`: H dealt evenly to 256 CUs, or to as many workgroups a CU as it
+// takes.  The CUs share the memory's rate evenly, so that one with a workgroup more than the others ends far later (4 tokens, 68
+// experts top-9, bf16, I 1024: 2048 columns, 256 workgroups of 8, 24.6 us; 2064, 258 of 8, 37.7, and 230 of 9 26.3; 1040, 130 of
+// 8 or 260 of 4, 24.3, and 208 of 5 16.7).  Rows of the instruction that are left over move no bytes.
+static int few_columns(int H, int most) {
+  const int rounds = (H + 256 * most - 1) / (256 * most);
+  return std::max(most / 2 + 1, (H + 256 * rounds - 1) / (256 * rounds));
+}
+
 // Entries that the second launch has to expect: of one token exactly its k, of more the distinct experts of even routing, or
 // what the entries' rows make of all slots.
 static double few_entries(const FewArgs& p) {
@@ -649,7 +664,9 @@ static hipError_t launch_few_of(const FewArgs& p, hipStream_t s) {
 
 template <class W, int COLS, int SUPER, int TOK, int RING, int NW>
 static hipError_t launch_few_second(FewArgs p, hipStream_t s) {
-  const int R = p.T * p.k, supers = (p.I + SUPER - 1) / SUPER, columns = p.H / COLS;
+  const int R = p.T * p.k, supers = (p.I + SUPER - 1) / SUPER;
+  p.cols = COLS == 4 ? 4 : few_columns(p.H, COLS);
+  const int columns = (p.H + p.cols - 1) / p.cols;
   const double entries = few_entries(p);
   // Groups of workgroups that share the units of the same columns where there are few columns and many units: a wave's super-chunk
   // takes about 0.9 us, the third launch that adds the groups' parts 4.5 (11 tokens, 118 experts top-8, int8 224 x 13712: 201 us
@@ -686,25 +703,28 @@ static hipError_t launch_few_w(FewArgs p, hipStream_t s) {
   else if (p.E <= 512) e = launch_few_of<W, 8>(p, s);
   else e = launch_few_of<W, 16>(p, s);
   if (e != hipSuccess) return e;
-  // 4 columns a workgroup where 8 would leave half the CUs idle and the contraction fills super-chunks of 512 (8 tokens, 64
-  // experts top-6, 1024 x 512, bf16: 10.4 us against 13.5; 12 tokens, 1536 x 1536: 47 against 37; int8 1040 x 336: 11.7 against 10.1)
-  const bool narrow = p.H <= 1280 && p.I >= 512;
+  // 4 columns a workgroup where more would leave half the CUs idle and the contraction fills super-chunks of 512 (8 tokens, 64
+  // experts top-6, 1024 x 512, bf16: 10.4 us against 13.5); 16 at most where 8 would be more than a workgroup a CU (16 tokens, 8
+  // experts of 4096 x 14336: 163 us against 190; int8, 4 tokens, 256 experts, 7168 x 2048: 85 against 91)
+  const bool narrow = p.H <= 1024 && p.I >= 512, wide = p.H > 2048;
   if (p.T == 1) {
     if (narrow) return launch_few_second<W, 4, 512, 1, 2, 8>(p, s);
+    if (wide) return launch_few_second<W, 16, 256, 1, 2, 8>(p, s);
     return launch_few_second<W, 8, 256, 1, 3, 8>(p, s);
   }
   if (crowded) {
-    // 16 columns a workgroup halve the traffic of h, but want enough workgroups (16 tokens, 8 experts of 4096 x 14336: 167 us
-    // against 190; 2048 columns: 44 us against 30)
-    if (p.H >= 4096) return launch_few_second<W, 16, 256, 8, 2, 8>(p, s);
+    if (wide) return launch_few_second<W, 16, 256, 8, 2, 8>(p, s);
     return launch_few_second<W, 8, 256, 8, 2, 8>(p, s);
   }
   if (narrow) return launch_few_second<W, 4, 512, 4, 2, 8>(p, s);
-  // int8 units are half as long in bytes and convert their weights: twice the waves (16 tokens, 256 experts top-8, 2048 x 512:
-  // 24 us against 26; bf16, 8 tokens, 128 experts, 2048 x 768: 32 us against 31, so not there)
-  // and from 4096 columns on 16 columns (4 tokens, 256 experts top-8, 7168 x 2048: 85 us against 91; bf16 5120 x 1040: 82 against 68)
-  if (W::SCALED && p.H >= 4096) return launch_few_second<W, 16, 256, 4, 2, 8>(p, s);
-  if (W::SCALED) return launch_few_second<W, 8, 256, 4, 2, 16>(p, s);
+  // int8 units are half as long in bytes and convert their weights: twice the waves where a CU has one workgroup (16 tokens, 256
+  // experts top-8, 2048 x 512: 24 us against 26; 4 tokens, 68 experts top-9, 2304 x 2048 31.7 against 39.4, but 5120 x 2048 64
+  // against 61; bf16, 8 tokens, 128 experts, 2048 x 768: 32 us against 31, so not there)
+  if constexpr (W::SCALED) {
+    if (p.H <= 2048) return launch_few_second<W, 8, 256, 4, 2, 16>(p, s);
+    if (p.H <= 4096) return launch_few_second<W, 16, 256, 4, 2, 16>(p, s);
+  }
+  if (wide) return launch_few_second<W, 16, 256, 4, 2, 8>(p, s);
   return launch_few_second<W, 8, 256, 4, 3, 8>(p, s);
 }
 

@@ -221,8 +221,8 @@ struct FewArgs {
   float* weight;         // [T, k]
   uint16_t* y;           // bf16 [T, H]
   float* parts;          // [groups, T, H], where the second launch's workgroups share their columns in groups
-  // set by the launch: an entry's rows at most, log2 of the pieces of an entry, groups of the second launch
-  int entry_rows = 0, pieces_shift = 0, groups = 1;
+  // set by the launch: an entry's rows at most, log2 of the pieces of an entry, columns of a workgroup and groups of the second launch
+  int entry_rows = 0, pieces_shift = 0, cols = 0, groups = 1;
 };
 hipError_t launch_ffn_few(const FewArgs& a, bool i8, hipStream_t stream);
 

@@ -204,7 +204,8 @@ def test_stream_and_graph(int8):
 
 @pytest.mark.parametrize("int8", [False, True], ids=["w16", "w8a16"])
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 16, 4, 512, 1024), (1, 300, 16, 528, 1040), (1, 9, 2, 32, 4112), (2, 40, 7, 1280, 544), (16, 5, 3, 4112, 48),
-                                       (15, 31, 1, 768, 528), (4, 1024, 3, 144, 16)])
+                                       (15, 31, 1, 768, 528), (4, 1024, 3, 144, 16), (3, 9, 2, 1040, 272), (5, 40, 3, 2064, 288), (6, 40, 3, 3344, 96),
+                                       (1, 9, 3, 2080, 272), (1, 9, 3, 4112, 96), (9, 6, 4, 2576, 272), (3, 30, 3, 7168, 64), (1, 9, 3, 1296, 48)])
 def test_mixes_of_the_rules(T, E, k, H, I, int8):
     """Short rows and narrow outputs, single tokens, crowded experts, in the mixes that SHAPES leaves out."""
     L = Layer(T, E, k, H, I, int8, seed=T * E)
