@@ -13,10 +13,10 @@
 //   gate_up: 8 gate rows and the up rows of the same 8 columns of h, against all tokens.  The waves of a workgroup take a
 //            share of the contraction each and meet in LDS; where rows are short a wave takes such a task alone.
 //   down:    8 rows (columns of y), each as two halves of the contraction, against at most 8 tokens of the expert, as
-//            two halves too (or 4 rows as four quarters); what belongs together is added at the end.  So 4, 8 or 16 columns
-//            of y make a workgroup (256 of them at H 2048 with 8) and still whole instructions.  A workgroup sees every
-//            chosen expert, so the weighted sum over a token's experts is its own, in the order of the slots.  Only where
-//            H is small, and the contraction long, do workgroups share columns: a third launch then adds their parts.
+//            two halves too (or 4 rows as four quarters); what belongs together is added at the end.  So up to 4, 8 or 16
+//            columns of y make a workgroup, as many as deal H evenly to the CUs.  A workgroup sees every chosen expert, so
+//            the weighted sum over a token's experts is its own, in the order of the slots.  Only where H is small, and the
+//            contraction long, do workgroups share columns: a third launch then adds their parts.
 // h stays in two bf16 parts (value, and what its rounding left), for about 16 significant bits: the traffic of h is small
 // beside the weights', and y is then rounded once.  Sums are fp32.
 //
@@ -411,7 +411,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
   }
 }
 
-// The second launch: COLS (4, 8 or 16) columns of y a workgroup, whose group (blockIdx.y) takes every groups-th NW units.  A
+// The second launch: up to COLS (4, 8 or 16) columns of y a workgroup, whose group (blockIdx.y) takes every groups-th NW units.  A
 // unit is an entry and every pieces-th super-chunk of SUPER elements of the contraction; a wave takes it from a place of
 // its own on (workgroups in step would ask the same few memory channels).
 // The instruction's 16 rows are 8 columns as two halves of the contraction, or 4 as four quarters (more workgroups where H
@@ -619,7 +619,7 @@ __global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__
 // Columns of a workgroup of the second launch, at most `most`: H dealt evenly to 256 CUs, or to as many workgroups a CU as it
 // takes.  The CUs share the memory's rate evenly, so that one with a workgroup more than the others ends far later (4 tokens, 68
 // experts top-9, bf16, I 1024: 2048 columns, 256 workgroups of 8, 24.6 us; 2064, 258 of 8, 37.7, and 230 of 9 26.3; 1040, 130 of
-// 8 or 260 of 4, 24.3, and 208 of 5 16.7).  Rows of the instruction that are left over move no bytes.
+// 8 or 260 of 4, 24.3, and 208 of 5 16.7; 8 tokens, 64 experts top-6, bf16 768 x 768 14.7 with 4 and 12.7 with 3).  Rows of the instruction that are left over move no bytes.
 static int few_columns(int H, int most) {
   const int rounds = (H + 256 * most - 1) / (256 * most);
   return std::max(most / 2 + 1, (H + 256 * rounds - 1) / (256 * rounds));
@@ -665,13 +665,13 @@ static hipError_t launch_few_of(const FewArgs& p, hipStream_t s) {
 template <class W, int COLS, int SUPER, int TOK, int RING, int NW>
 static hipError_t launch_few_second(FewArgs p, hipStream_t s) {
   const int R = p.T * p.k, supers = (p.I + SUPER - 1) / SUPER;
-  p.cols = COLS == 4 ? 4 : few_columns(p.H, COLS);
-  const int columns = (p.H + p.cols - 1) / p.cols;
   const double entries = few_entries(p);
   // Groups of workgroups that share the units of the same columns where there are few columns and many units: a wave's super-chunk
   // takes about 0.9 us, the third launch that adds the groups' parts 4.5 (11 tokens, 118 experts top-8, int8 224 x 13712: 201 us
   // down in one group, 62 in eight; 10 tokens, 46 experts top-9, bf16 592 x 5280: 89 and 73).
-  if (p.H <= kFewGroupsH && entries * supers > 16.0 * NW) p.groups = std::max(1, std::min(kFewGroups, 640 / columns));
+  if (p.H <= kFewGroupsH && entries * supers > 16.0 * NW) p.groups = std::max(1, std::min(kFewGroups, 512 * COLS / p.H));
+  p.cols = p.groups > 1 ? COLS : few_columns(p.H, COLS);
+  const int columns = (p.H + p.cols - 1) / p.cols;
   // Pieces (a power of two) of the contraction that units are cut into, no more than there are super-chunks: one token's entries,
   // all alike, until every wave has a unit; of more tokens until there are about 32, so that the waves end together (9 tokens, 10
   // experts top-8, int8 1760 x 4672: 50 us uncut, 42 in quarters).  At most 64 units a wave.
