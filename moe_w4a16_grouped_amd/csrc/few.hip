@@ -21,7 +21,7 @@
 // beside the weights', and y is then rounded once.  Sums are fp32.
 //
 // Measured, both launches and the weights' rate (a large copy reads and writes at 5.2 TB/s here, a sum reads at 4.0):
-//   16 tokens, 8 experts of 4096 x 14336, bf16      474 us, 5.9 TB/s         (324 gate_up, 164 down)
+//   16 tokens, 8 experts of 4096 x 14336, bf16      474-493 us, 5.7 TB/s     (324 gate_up, 164 down)
 //   8 tokens, 128 experts top-8, 2048 x 768, bf16    89 us, 5.4 TB/s         (58, 29)
 //   16 tokens, 256 experts top-8, 2048 x 512, int8   73 us, 4.4 TB/s         (47, 23)
 //   one token, 128 experts top-8, 2048 x 768         20 us bf16, 15 us int8  (12, 7.4 and 9.3, 6.6)
