@@ -154,7 +154,7 @@ struct FewLds {
   uint32_t keys[kFewSlots];
   int32_t list[kFewSlots];                    // the chosen experts, ascending
   int16_t slot[kFewSlots][kFewTokens];        // a chosen expert's slot of each token, or -1
-  int32_t more;
+  int32_t more[kFewSlots / 64];               // further entries of the experts of 64 ranks
 };
 
 // ONE: a single token.  ALONE: a task is a wave's own, the whole contraction of it, rather than a workgroup's.
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
     }
   };
   fetch(0);
-  if (tid == 0) s.zero[0] = s.zero[1] = u32x4{0u, 0u, 0u, 0u}, s.more = 0;
+  if (tid == 0) s.zero[0] = s.zero[1] = u32x4{0u, 0u, 0u, 0u};
   for (int i = tid; i < R * (kFewTokens / 8); i += 64 * kFewWaves) reinterpret_cast<u32x4*>(s.slot)[i] = u32x4{~0u, ~0u, ~0u, ~0u};
   int id[NT] = {};
   uint32_t key[NT] = {}, chosen = 0u;
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
   }
   const int32_t* list = ONE ? s.ids : s.list;
 
-  if (writer) {  // the routing, and the entries: an expert's first rows at its rank, further ones behind the experts
+  if (writer) {  // the routing, and the entries: an expert's first rows at its rank, further ones behind all experts, in their order
     for (int t = wave; t < T; t += kFewWaves) {
       const int f = t * k + min(lane, k - 1);
       const float w = few_weight(from_ordered_bits(s.keys[f]), k);
@@ -257,6 +257,28 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
       }
     }
     FewEntry* table = reinterpret_cast<FewEntry*>(p.table) + 1;
+    int behind = n, entries = n;  // where this expert's further entries start, and the end of all
+    if constexpr (!ONE) {
+      int further = 0;  // at most 3: 16 rows by fours
+      if (tid < n) {
+        int rows = 0;
+        const u32x4* slots = reinterpret_cast<const u32x4*>(s.slot[tid]);
+#pragma unroll
+        for (int i = 0; i < kFewTokens / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) rows += __popc(~slots[i][j] & 0x80008000u);
+        further = (rows - 1) / p.entry_rows;
+      }
+      const uint64_t ones = __ballot(further & 1), twos = __ballot(further & 2), below = (1ull << lane) - 1ull;
+      behind += __popcll(ones & below) + 2 * __popcll(twos & below);
+      if (lane == 0 && wave < kFewSlots / 64) s.more[wave] = __popcll(ones) + 2 * __popcll(twos);
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kFewSlots / 64; ++w) {
+        behind += w < wave ? s.more[w] : 0;
+        entries += s.more[w];
+      }
+    }
     if (tid < n) {
       FewEntry* at = table + tid;
       int have = 0;
@@ -266,7 +288,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
         if (have == p.entry_rows) {
           at->expert = list[tid];
           at->rows = have;
-          at = table + n + atomicAdd(&s.more, 1);
+          at = table + behind++;
           have = 0;
         }
         at->row[have++] = (int16_t)f;
@@ -274,8 +296,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs p) 
       at->expert = list[tid];
       at->rows = have;
     }
-    __syncthreads();
-    if (tid == 0) p.table[0] = n + s.more;
+    if (tid == 0) p.table[0] = entries;
   }
 
   // this wave's share of the contraction, in chunks of C steps

@@ -324,3 +324,38 @@ def test_refusals_of_the_binding():
         moe.moe_ffn_few_w16(L.x, L.logits, L.w13, L.w2, 9)
     with pytest.raises(moe.MoEError):
         moe.moe_ffn_few_w16(L.x.repeat(5, 1), L.logits.repeat(5, 1), L.w13, L.w2, 2)
+
+
+def _table(ws, T, k, I):
+    """The entries that the first launch leaves in the workspace, behind h: (expert, rows) in the order in which the second takes them."""
+    at = (T * k * I * 4 + 255) // 256 * 256
+    ints = ws[at:at + 32 * (1 + T * k)].view(torch.int32).view(-1, 8).cpu()
+    rows = ints[1:, 2:6].contiguous().view(torch.int16)
+    return [(int(e[0]), rows[i, :int(e[1])].tolist()) for i, e in enumerate(ints[1:1 + int(ints[0, 0])])]
+
+
+@pytest.mark.parametrize("int8", [False, True], ids=["w16", "w8a16"])
+@pytest.mark.parametrize("T,E,k,H,I", [(16, 128, 16, 1024, 1024), (16, 300, 16, 528, 2064), (15, 100, 16, 1024, 2064), (16, 80, 16, 272, 4112),
+                                       (3, 8, 2, 48, 32), (1, 20, 10, 240, 1040)])
+def test_entries_stand_in_a_fixed_order(T, E, k, H, I, int8):
+    """Experts ascending (of one token: by slot) with their first rows, then in the same order what is left of those with more rows than an entry takes.
+    Where workgroups share columns a place in this table decides with which others an entry is summed, so arrival order must
+    not enter it.  The larger cases have such experts on both sides of the 64th: their entries come from two waves."""
+    logits = _rand((T, E), F32, 1)
+    if E >= 80:
+        logits[:, [3, 40, E - 2]] += 20.0  # all tokens on these
+    L = Layer(T, E, k, H, I, int8, seed=T + E, logits=logits)
+    ws = torch.full((moe.moe_ffn_few_workspace_bytes(T, H, I, E, k),), 0xFF, dtype=torch.uint8, device="cuda")
+    ids = L.routing()[0].cpu()
+    most = 1 if T == 1 else (8 if T * k > 2 * E else 4)
+    held = {e: torch.nonzero(ids.view(-1) == e).view(-1).tolist() for e in (ids[0] if T == 1 else torch.unique(ids)).tolist()}
+    if E >= 80:
+        over = [i for i, rows in enumerate(held.values()) if len(rows) > most]
+        assert over[0] < 64 <= over[-1]
+    want = [(e, rows[:most]) for e, rows in held.items()]
+    want += [(e, rows[at:at + most]) for e, rows in held.items() for at in range(most, len(rows), most)]
+    y = L.run(workspace=ws)
+    assert _table(ws, T, k, I) == want
+    L.check(y)
+    for _ in range(8):
+        assert torch.equal(L.run(workspace=ws), y) and _table(ws, T, k, I) == want
