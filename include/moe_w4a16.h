@@ -747,7 +747,7 @@ moe_status_t moe_ffn_forward_w16(const uint16_t* x, const float* router_logits, 
  * ---- Root-mean-square norm in front of the experts -----------------------------------------------------
  * [ATOM, 8.2: dynamic activation quantization is part of a format's contract.]  For each row of x [T, H]:
  *   s = x + residual (fp32, rounded to the type; s = x where residual is NULL)
- *   r = 1 / sqrt(mean(s^2) + eps),  y = s * r * weight (fp32, rounded once)
+ *   r = 1 / sqrt(mean(s^2) + eps),  y = (s * r) * weight (fp32, rounded once; the same bits whatever quant is)
  * and, formed in the same pass, 8-bit codes and scales of y for the products that take them:
  *   MOE_QUANT_I8  one scale a row (moe_gemm_i8, moe_grouped_gemm_i8): scale = max |y| / 127, code = the integer
  *                 nearest to the real quotient 127 z / max |z|, z = s * weight (which y / scale is), ties to even.

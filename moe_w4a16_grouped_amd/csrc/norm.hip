@@ -288,20 +288,22 @@ __device__ __forceinline__ u32x2 norm_codes8(const float (&s)[8], const float (&
 // 32.2 us against 35.5, 4096 x 2048 15.2 against 16.8, 8191 x 4096 55.9 against 57.6, 801 x 2048 4.5 both ways).
 template <bool F16, bool WF32, int QUANT>
 __device__ __forceinline__ void norm_store(const NormArgs& p, const u32x4& sv, const u32x4 (&wv)[WF32 ? 2 : 1], float r,
-                                           double zmax, bool some, bool fast, bool quick, size_t at) {
+                                           double zmax, bool some, bool quick, size_t at) {
   float s[8], w[8];
   unpack8<F16>(sv, s);
   weight8<F16, WF32>(wv, w);
-  float z[8], y[8];
+  if (p.y) {  // (s r) w: s w may leave the range of fp32 where y does not; the same whatever codes stand beside it
+    float y[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) z[j] = s[j] * w[j];
-  if (p.y) {  // z r, or, where z may pass fp32, s r w
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = QUANT != kQuantNone && fast ? z[j] * r : s[j] * r * w[j];
+    for (int j = 0; j < 8; ++j) y[j] = s[j] * r * w[j];
     store16<1>(pack8<F16>(y), static_cast<u32x4*>(p.y) + at);
   }
-  if constexpr (QUANT != kQuantNone)
+  if constexpr (QUANT != kQuantNone) {
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = s[j] * w[j];
     __builtin_nontemporal_store(norm_codes8<QUANT>(s, w, z, zmax, some, quick), static_cast<u32x2*>(p.q) + at);
+  }
 }
 
 // TH threads a row (64: a wave, four rows a workgroup), NC chunks of 8 columns a thread, held between the sums and the
@@ -363,11 +365,13 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
   meet(0, ss, zmax, bits);
   // rows whose squares fp32 cannot add, or whose products or their quotients it cannot hold: once more in 64 bits (rows of
   // zeros too: they may be products that fp32 let vanish)
-  bool fast = ss < 1e36 && (ss > 1e-25 || p.eps > 1e-15f);
+  const bool sums = ss < 1e36 && (ss > 1e-25 || p.eps > 1e-15f);
+  bool fast = sums;
   if (QUANT != kQuantNone) fast = fast && bits >= 0x21800000u && bits < 0x7B800000u;  // 2^-60 and 2^120
   if (QUANT == kQuantI8 && !WF32) zmax = (double)__uint_as_float(bits);
   bool bad = false;
   if (!fast) {
+    const double first = ss;
     ss = zmax = 0.0;
     bits = 0u;
 #pragma unroll
@@ -378,6 +382,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
     }
     meet(1, ss, zmax, bits);
     bad = bits >= 0x7F800000u || !(ss < __builtin_inf());
+    if (sums) ss = first;  // what the row has without codes, for the same y
   }
   const double rd = rsqrt_f64(fma(ss, p.inv_h, (double)p.eps));
   const float r = (float)rd;
@@ -409,7 +414,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_kernel(NormArgs p
         if ((lane & 15) == 0) p.q_scale[(size_t)row * (nc / 16) + c / 16] = scale;
         quick = fast && zmax >= 0x1p-60;
       }
-      norm_store<F16, WF32, QUANT>(p, sv[j], wv[j], r, zmax, scale > 0.f, fast, quick, base + c);
+      norm_store<F16, WF32, QUANT>(p, sv[j], wv[j], r, zmax, scale > 0.f, quick, base + c);
     }
   }
 }

@@ -395,3 +395,29 @@ def test_refusals_of_the_binding():
         moe.moe_rmsnorm_add(x, w, 1e-6, want_y=False)
     with pytest.raises(moe.MoEError):
         moe.moe_rmsnorm_add_grad(x, x, w, 1e-6, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("x_dtype,w_dtype", [(BF16, BF16), (BF16, F32), (F16, F32)])
+@pytest.mark.parametrize("T,H", [(7, 512), (2050, 1024), (33, 2048), (6, 16384)])
+def test_y_does_not_depend_on_the_codes(T, H, x_dtype, w_dtype):
+    """The same bits of y whatever codes are formed beside it, in rows of ordinary and of far magnitudes, of products past fp32
+    and (every 16th column, where y itself is ordinary) below its normal range."""
+    x, w = _rand((T, H), F32, T), _weight(H, F32, H)
+    eps = 1e-6
+    if x_dtype == BF16:
+        eps = 2.0 ** -100
+        x[1] *= 1e30
+        x[2] *= 1e-36
+        x[3] *= 2.0 ** -38
+        x[3, 5::16] *= 2.0 ** -52
+        x[4] *= 2.0 ** 100
+        x[5] *= 2.0 ** 50
+        w[5::16] *= 2.0 ** -57
+        w[9] *= 2.0 ** 75
+    x, w = x.to(x_dtype), w.to(w_dtype)
+    plain = moe.moe_rmsnorm_add(x, w, eps)
+    _check(x, None, w, eps, NONE, True, plain)
+    for quant in (I8, F8):
+        got = moe.moe_rmsnorm_add(x, w, eps, quant=quant)
+        assert torch.equal(got[1], plain[1])
+        _check(x, None, w, eps, quant, True, got)
