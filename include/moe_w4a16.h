@@ -780,7 +780,7 @@ size_t moe_rmsnorm_add_grad_workspace_bytes(int32_t T, int32_t H);
  *   dx = r * (dy * weight - s * r^2 * mean(dy * weight * s)) + ds     [T, H], of x and of the residual alike
  *   dweight = sum over the rows of dy * s * r                         [H], of dweight_dtype MOE_OUT_BF16, _F16 or _F32
  * Sums over a row in 64 bits, everything else in fp32 (dy * weight within its range), one rounding.  dweight is summed
- * in parts of the rows, which are added in order (zeros where T is 0).  workspace: at least
+ * in parts of at most 256 rows one after the other, which are added in order in 64 bits (zeros where T is 0).  workspace: at least
  * moe_rmsnorm_add_grad_workspace_bytes(T, H) bytes.
  * dx may be dy, s or ds.  Types, shapes and alignment as for moe_rmsnorm_add.
  */

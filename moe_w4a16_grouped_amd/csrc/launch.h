@@ -252,6 +252,7 @@ struct NormGradArgs {
   float* parts;    // [rmsnorm_grad_parts, H]
   int dw_out;      // MOE_OUT_BF16, MOE_OUT_F16 or MOE_OUT_F32
   void* dw;
+  int rounds = 1;  // set by the launch: parts that a workgroup writes
 };
 int rmsnorm_grad_parts(int T, int H);
 hipError_t launch_rmsnorm_grad(const NormGradArgs& a, bool f16, bool w_f32, hipStream_t stream);

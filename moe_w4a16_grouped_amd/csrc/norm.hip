@@ -455,6 +455,9 @@ hipError_t launch_rmsnorm(const NormArgs& p, bool f16, bool w_f32, int quant, hi
 // each, so that the weight's gradient stays in its registers; the next row is asked for before the current one's sums
 // meet.  The workgroups' sums of rows go to the workspace and are added in the order of the workgroups.
 // TH threads a row (64: a wave, four rows a workgroup, whose sums meet in LDS before they are written).
+// A sum in fp32 takes at most kGradRows rows; then it is a part of its own, and the parts are added in 64 bits (100000 x 8192 1211 us,
+// 1196 with one part a workgroup; twice the workgroups instead, of half the rows each, do not walk the rows side by side: 1253).
+constexpr int kGradRows = 256;
 template <bool F16, bool WF32, int TH, int NC>
 __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormGradArgs p) {
   constexpr int kWaves = TH / 64, kRows = TH < 256 ? 256 / TH : 1;
@@ -468,8 +471,6 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormG
   for (int j = 0; j < NC; ++j) {
     const int c = t + j * TH;
     if (c < nc) load_weight8<WF32>(p.w, c, wv[j]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
   auto load = [&](long long row) {
     const size_t base = (size_t)row * nc;
@@ -484,96 +485,104 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormG
     }
   };
   int turn = 0;
-  const long long first = (long long)blockIdx.x * kRows + sub;
-  if (kAhead && first < p.T) load(first);
-  for (long long row = first; row < p.T; row += step, turn ^= 1) {
-    double ss = 0.0, gs = 0.0;
-    u32x4 s8[NC], g8[NC], a8[NC];
-    if (!kAhead) load(row);
+  long long row = (long long)blockIdx.x * kRows + sub;
+  if (kAhead && row < p.T) load(row);
+  for (int round = 0; round < p.rounds; ++round) {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      s8[j] = sv[j];
-      g8[j] = gv[j];
-      a8[j] = av[j];
-    }
-    if (kAhead && row + step < p.T) load(row + step);
+    for (int j = 0; j < NC; ++j)
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      if (t + j * TH < nc) {
-        float s[8], d[8], w[8];
-        unpack8<F16>(s8[j], s);
-        unpack8<F16>(g8[j], d);
-        weight8<F16, WF32>(wv[j], w);
+      for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+    for (int left = kGradRows; left > 0 && row < p.T; --left, row += step, turn ^= 1) {
+      double ss = 0.0, gs = 0.0;
+      u32x4 s8[NC], g8[NC], a8[NC];
+      if (!kAhead) load(row);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fma((double)s[i], (double)s[i], ss);
-          gs = fma((double)(d[i] * w[i]), (double)s[i], gs);
+      for (int j = 0; j < NC; ++j) {
+        s8[j] = sv[j];
+        g8[j] = gv[j];
+        a8[j] = av[j];
+      }
+      if (kAhead && row + step < p.T) load(row + step);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        if (t + j * TH < nc) {
+          float s[8], d[8], w[8];
+          unpack8<F16>(s8[j], s);
+          unpack8<F16>(g8[j], d);
+          weight8<F16, WF32>(wv[j], w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            ss = fma((double)s[i], (double)s[i], ss);
+            gs = fma((double)(d[i] * w[i]), (double)s[i], gs);
+          }
+        }
+      }
+      ss = wave_f64(ss, AddF64{});
+      gs = wave_f64(gs, AddF64{});
+      if constexpr (kWaves > 1) {
+        if (lane == 0) {
+          part[turn][wave][0] = ss;
+          part[turn][wave][1] = gs;
+        }
+        __syncthreads();  // one a row: a wave writes this half of part again only past the next row's barrier
+        ss = gs = 0.0;
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) {
+          ss += part[turn][k][0];
+          gs += part[turn][k][1];
+        }
+      }
+      const double rd = rsqrt_f64(fma(ss, p.inv_h, (double)p.eps));
+      const float r = (float)rd, k = (float)(rd * rd * (gs * p.inv_h));
+      const size_t base = (size_t)row * nc;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = t + j * TH;
+        if (c < nc) {
+          float s[8], d[8], w[8], a[8], o[8];
+          unpack8<F16>(s8[j], s);
+          unpack8<F16>(g8[j], d);
+          weight8<F16, WF32>(wv[j], w);
+          if (p.ds) unpack8<F16>(a8[j], a);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float xhat = s[i] * r;
+            o[i] = fmaf(-xhat, k, r * (d[i] * w[i]));
+            if (p.ds) o[i] += a[i];
+            dw[j][i] = fmaf(d[i], xhat, dw[j][i]);
+          }
+          // past the L2 (8191 x 4096 48.5 us against 51.3, 8192 x 2048 28.6 both ways)
+          store16<1>(pack8<F16>(o), static_cast<u32x4*>(p.dx) + base + c);
         }
       }
     }
-    ss = wave_f64(ss, AddF64{});
-    gs = wave_f64(gs, AddF64{});
-    if constexpr (kWaves > 1) {
-      if (lane == 0) {
-        part[turn][wave][0] = ss;
-        part[turn][wave][1] = gs;
+    if constexpr (kRows > 1) {
+      __shared__ float more[kRows - 1][TH * NC * 8];
+      static_assert(NC == 1, "a thread's sums stand 16 bytes apart from its neighbour's");
+      f32x4* mine = reinterpret_cast<f32x4*>(more[sub > 0 ? sub - 1 : 0]);
+      if (round > 0) __syncthreads();  // the last round's have been read
+      if (sub > 0) {
+        mine[t] = f32x4{dw[0][0], dw[0][1], dw[0][2], dw[0][3]};
+        mine[TH + t] = f32x4{dw[0][4], dw[0][5], dw[0][6], dw[0][7]};
       }
-      __syncthreads();  // one a row: a wave writes this half of part again only past the next row's barrier
-      ss = gs = 0.0;
+      __syncthreads();
+      if (sub == 0) {
 #pragma unroll
-      for (int k = 0; k < kWaves; ++k) {
-        ss += part[turn][k][0];
-        gs += part[turn][k][1];
+        for (int r = 0; r < kRows - 1; ++r) {
+          const f32x4* other = reinterpret_cast<const f32x4*>(more[r]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dw[0][i] += other[(i >> 2) * TH + t][i & 3];
+        }
       }
     }
-    const double rd = rsqrt_f64(fma(ss, p.inv_h, (double)p.eps));
-    const float r = (float)rd, k = (float)(rd * rd * (gs * p.inv_h));
-    const size_t base = (size_t)row * nc;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = t + j * TH;
-      if (c < nc) {
-        float s[8], d[8], w[8], a[8], o[8];
-        unpack8<F16>(s8[j], s);
-        unpack8<F16>(g8[j], d);
-        weight8<F16, WF32>(wv[j], w);
-        if (p.ds) unpack8<F16>(a8[j], a);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xhat = s[i] * r;
-          o[i] = fmaf(-xhat, k, r * (d[i] * w[i]));
-          if (p.ds) o[i] += a[i];
-          dw[j][i] = fmaf(d[i], xhat, dw[j][i]);
-        }
-        // past the L2 (8191 x 4096 48.5 us against 51.3, 8192 x 2048 28.6 both ways)
-        store16<1>(pack8<F16>(o), static_cast<u32x4*>(p.dx) + base + c);
+      if (sub == 0 && c < nc) {
+        f32x4* dst = reinterpret_cast<f32x4*>(p.parts + ((size_t)round * gridDim.x + blockIdx.x) * p.H) + 2 * (size_t)c;
+        dst[0] = f32x4{dw[j][0], dw[j][1], dw[j][2], dw[j][3]};
+        dst[1] = f32x4{dw[j][4], dw[j][5], dw[j][6], dw[j][7]};
       }
-    }
-  }
-  if constexpr (kRows > 1) {
-    __shared__ float more[kRows - 1][TH * NC * 8];
-    static_assert(NC == 1, "a thread's sums stand 16 bytes apart from its neighbour's");
-    f32x4* mine = reinterpret_cast<f32x4*>(more[sub > 0 ? sub - 1 : 0]);
-    if (sub > 0) {
-      mine[t] = f32x4{dw[0][0], dw[0][1], dw[0][2], dw[0][3]};
-      mine[TH + t] = f32x4{dw[0][4], dw[0][5], dw[0][6], dw[0][7]};
-    }
-    __syncthreads();
-    if (sub > 0) return;
-#pragma unroll
-    for (int r = 0; r < kRows - 1; ++r) {
-      const f32x4* other = reinterpret_cast<const f32x4*>(more[r]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dw[0][i] += other[(i >> 2) * TH + t][i & 3];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = t + j * TH;
-    if (c < nc) {
-      f32x4* dst = reinterpret_cast<f32x4*>(p.parts + (size_t)blockIdx.x * p.H) + 2 * (size_t)c;
-      dst[0] = f32x4{dw[j][0], dw[j][1], dw[j][2], dw[j][3]};
-      dst[1] = f32x4{dw[j][4], dw[j][5], dw[j][6], dw[j][7]};
     }
   }
 }
@@ -614,14 +623,23 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restric
 // threads 51.1, 512 of two chunks 54.2).  Workgroups: as many as the card holds at once, so that few parts are left to add.
 static int grad_threads(int H) { return H <= 512 ? 64 : (H <= 2048 ? 256 : (H <= 4096 ? 512 : 1024)); }
 
-int rmsnorm_grad_parts(int T, int H) {
+struct GradGrid {
+  int workgroups, rounds;  // rounds: of kGradRows rows a workgroup's row
+};
+static GradGrid grad_grid(int T, int H) {
   const int th = grad_threads(H), rows = th < 256 ? 256 / th : 1, most = 1024 / std::max(1, th / 256);
-  return std::min((T + rows - 1) / rows, most);
+  return {std::min((T + rows - 1) / rows, most), std::max(1, (T + kGradRows * rows * most - 1) / (kGradRows * rows * most))};
+}
+int rmsnorm_grad_parts(int T, int H) {
+  const GradGrid g = grad_grid(T, H);
+  return g.workgroups * g.rounds;
 }
 
 template <bool F16, bool WF32>
-static hipError_t launch_norm_grad_of(const NormGradArgs& p, hipStream_t s) {
-  const int n = rmsnorm_grad_parts(p.T, p.H);
+static hipError_t launch_norm_grad_of(NormGradArgs p, hipStream_t s) {
+  const GradGrid g = grad_grid(p.T, p.H);
+  const int n = g.workgroups;
+  p.rounds = g.rounds;
   if (p.T == 0) {
   } else if (p.H <= 512) rmsnorm_grad_kernel<F16, WF32, 64, 1><<<n, 256, 0, s>>>(p);
   else if (p.H <= 2048) rmsnorm_grad_kernel<F16, WF32, 256, 1><<<n, 256, 0, s>>>(p);
@@ -629,7 +647,7 @@ static hipError_t launch_norm_grad_of(const NormGradArgs& p, hipStream_t s) {
   else if (p.H <= 8192) rmsnorm_grad_kernel<F16, WF32, 1024, 1><<<n, 1024, 0, s>>>(p);
   else rmsnorm_grad_kernel<F16, WF32, 1024, 2><<<n, 1024, 0, s>>>(p);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  rmsnorm_dw_kernel<<<(p.H + 31) / 32, 1024, 0, s>>>(p.parts, n, p.H, p.dw_out, p.dw);
+  rmsnorm_dw_kernel<<<(p.H + 31) / 32, 1024, 0, s>>>(p.parts, n * g.rounds, p.H, p.dw_out, p.dw);
   return hipGetLastError();
 }
 

@@ -421,3 +421,15 @@ def test_y_does_not_depend_on_the_codes(T, H, x_dtype, w_dtype):
         got = moe.moe_rmsnorm_add(x, w, eps, quant=quant)
         assert torch.equal(got[1], plain[1])
         _check(x, None, w, eps, quant, True, got)
+
+
+def test_weight_gradient_of_many_rows():
+    """However many rows there are, at most 256 of them are added one after the other in fp32 (and then 3 waves' sums); the rest is
+    added in 64 bits.  Every addend is 1/2 + 2^-14 - 2^-21, which a sum of 2048 such rows on rounds down by almost half a step each time."""
+    T, H = 1 << 24, 8
+    r = 1 + 2.0 ** -13 - 2.0 ** -20
+    eps = float(torch.tensor(1 / r ** 2 - 0.25, dtype=F32))
+    s, dy = torch.full((T, H), 0.5, dtype=BF16, device="cuda"), torch.ones((T, H), dtype=BF16, device="cuda")
+    _, dw = moe.moe_rmsnorm_add_grad(dy, s, torch.ones(H, device="cuda"), eps)
+    want = torch.full((H,), T * 0.5 / (0.25 + eps) ** 0.5, dtype=torch.float64, device="cuda")
+    ru.assert_close(dw, want, (256 + 6) * U * want, "dw")
