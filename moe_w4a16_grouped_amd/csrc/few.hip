@@ -695,9 +695,11 @@ static hipError_t launch_few_second(FewArgs p, hipStream_t s) {
   const int columns = (p.H + p.cols - 1) / p.cols;
   // Pieces (a power of two) of the contraction that units are cut into, no more than there are super-chunks: one token's entries,
   // all alike, until every wave has a unit; of more tokens until there are about 32, so that the waves end together (9 tokens, 10
-  // experts top-8, int8 1760 x 4672: 50 us uncut, 42 in quarters).  At most 64 units a wave.
+  // experts top-8, int8 1760 x 4672: 50 us uncut, 42 in quarters).  At most 64 units a wave, each a lane's, whatever
+  // the routing: R bounds the entries.
   const double want = p.T == 1 ? NW * p.groups : 30;
-  while (entries * (1 << p.pieces_shift) < want && (2 << p.pieces_shift) <= supers && (R << p.pieces_shift) < 64 * NW) ++p.pieces_shift;
+  while (entries * (1 << p.pieces_shift) < want && (2 << p.pieces_shift) <= supers && (R << (p.pieces_shift + 1)) <= 64 * NW)
+    ++p.pieces_shift;
   const int lds = NW * TOK * (SUPER * 4 + 16) + R * 32 + (R + 3) / 4 * 16 + (R << p.pieces_shift) * 4 * COLS;
   const auto kernel = few_down_kernel<W, COLS, SUPER, TOK, RING, NW>;
   if (lds > (64 << 10)) {
