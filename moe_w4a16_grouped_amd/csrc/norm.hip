@@ -557,9 +557,9 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormG
       }
     }
     if constexpr (kRows > 1) {
-      __shared__ float more[kRows - 1][TH * NC * 8];
+      __shared__ f32x4 more[kRows - 1][TH * NC * 2];
       static_assert(NC == 1, "a thread's sums stand 16 bytes apart from its neighbour's");
-      f32x4* mine = reinterpret_cast<f32x4*>(more[sub > 0 ? sub - 1 : 0]);
+      f32x4* mine = more[sub > 0 ? sub - 1 : 0];
       if (round > 0) __syncthreads();  // the last round's have been read
       if (sub > 0) {
         mine[t] = f32x4{dw[0][0], dw[0][1], dw[0][2], dw[0][3]};
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(TH < 256 ? 256 : TH) void rmsnorm_grad_kernel(NormG
       if (sub == 0) {
 #pragma unroll
         for (int r = 0; r < kRows - 1; ++r) {
-          const f32x4* other = reinterpret_cast<const f32x4*>(more[r]);
+          const f32x4* other = more[r];
 #pragma unroll
           for (int i = 0; i < 8; ++i) dw[0][i] += other[(i >> 2) * TH + t][i & 3];
         }
