@@ -711,13 +711,20 @@ _I8, _F32, _INT32, _U8, _BF16 = (torch.int8,), (torch.float32,), (torch.int32,),
 _ACT = tuple(_IN)
 
 
+_C_INT = 2 ** 31 - 1  # ctypes would pass larger sizes on without their upper bits
+
+
 def _need(t, dtypes, shape, name, dev=None):
-    """A contiguous GPU tensor of one of the dtypes and of this shape (None = any size), on dev."""
+    """A contiguous GPU tensor of one of the dtypes and of this shape (None = any size that a C int holds, ... = any that the
+    call is not told or takes in 64 bits), on dev."""
     s = t.shape
     if t.dtype in dtypes and t.is_cuda and t.is_contiguous() and (dev is None or t.device == dev):
         if len(s) == len(shape):
             for got, want in zip(s, shape):
-                if want is not None and got != want:
+                if want is None:
+                    if got > _C_INT:
+                        raise ValueError(f"{name} has a dimension of {got} (at most {_C_INT})")
+                elif got != want and want is not ...:
                     break
             else:
                 return s
@@ -778,7 +785,7 @@ def _groups(A, R, a_row_of, a_row_div, expert_offsets, E, dev):
     else:
         if a_row_of.dim() != 1 or a_row_of.shape[0] < R:
             raise ValueError(f"a_row_of must hold {R} indexes (got {tuple(a_row_of.shape)})")
-        _need(a_row_of, _INT32, (None,), "a_row_of", dev)
+        _need(a_row_of, _INT32, (...,), "a_row_of", dev)
 
 
 def moe_i8_quantize(x, q=None, s=None, stream=None):
@@ -825,7 +832,7 @@ def moe_linear_i8(x, Wq, Ws, epilogue: int = MOE_EPI_NONE, out_dtype: int = MOE_
     y = _out(y, (T, _cols(N, epilogue)), out_dtype, dev, "y", stream)
     lib, size = load(), 0
     if workspace is not None:
-        size, = _need(workspace, _U8, (None,), "workspace", dev)
+        size, = _need(workspace, _U8, (...,), "workspace", dev)
     else:
         size = lib.moe_linear_i8_workspace_bytes(T, K)
         if size:
@@ -839,7 +846,7 @@ def moe_grouped_gemm_i8(Aq, As, a_row_of, a_row_div: int, Wq, Ws, expert_offsets
                         epilogue: int = MOE_EPI_NONE, out_dtype: int = MOE_OUT_BF16, C=None, stream=None):
     """Grouped int8 product over expert_offsets int32 [E + 1]: Aq int8 [*, K], As fp32 [*], Wq int8 [E, N, K],
     Ws fp32 [E, N] -> C [out_rows, N] ([out_rows, N/2] for SILU_MUL)."""
-    rows, K = _need(Aq, _I8, (None, None), "Aq")
+    rows, K = _need(Aq, _I8, (..., None), "Aq")
     dev = Aq.device
     _need(As, _F32, (rows,), "As", dev)
     E, N, _ = _need(Wq, _I8, (None, None, K), "Wq", dev)
@@ -873,7 +880,7 @@ def _layer_io(x, router_logits, H, E, k, y, topk_ids_out, topk_w_out, workspace,
     if workspace is None:
         workspace = _empty(max(need_bytes, 256), torch.uint8, dev, stream, keep=False)
     else:
-        _need(workspace, _U8, (None,), "workspace", dev)
+        _need(workspace, _U8, (...,), "workspace", dev)
     return y, workspace
 
 
@@ -900,7 +907,7 @@ def moe_grouped_gemm_w16(A, a_row_of, a_row_div: int, W, expert_offsets, out_row
                          out_dtype: int = None, C=None, stream=None):
     """Grouped product over expert_offsets int32 [E + 1]: A [*, K] and W [E, N, K], both bf16 or both fp16 -> C
     [out_rows, N] ([out_rows, N/2] for SILU_MUL) of out_dtype (default: the operands' type)."""
-    _, K = _need(A, _W16, (None, None), "A")
+    _, K = _need(A, _W16, (..., None), "A")
     dev, dt = A.device, A.dtype
     E, N, _ = _need(W, (dt,), (None, None, K), "W", dev)
     _groups(A, out_rows, a_row_of, a_row_div, expert_offsets, E, dev)
@@ -935,7 +942,7 @@ def moe_grouped_gemm_w16_dw(dC, A, a_row_of, a_row_div: int, expert_offsets, out
     (default: the operands' type); zeros for experts without rows."""
     R, N = _need(dC, _W16, (None, None), "dC")
     dev, dt = dC.device, dC.dtype
-    _, K = _need(A, (dt,), (None, None), "A", dev)
+    _, K = _need(A, (dt,), (..., None), "A", dev)
     if expert_offsets.dim() != 1 or expert_offsets.shape[0] < 2:
         raise ValueError(f"expert_offsets must have the shape (E + 1,) (got {tuple(expert_offsets.shape)})")
     E = expert_offsets.shape[0] - 1
@@ -944,7 +951,7 @@ def moe_grouped_gemm_w16_dw(dC, A, a_row_of, a_row_div: int, expert_offsets, out
     dW = _out(dW, (E, N, K), out_dtype, dev, "dW", stream)
     lib, size = load(), 0
     if workspace is not None:
-        size, = _need(workspace, _U8, (None,), "workspace", dev)
+        size, = _need(workspace, _U8, (...,), "workspace", dev)
     else:
         size = lib.moe_grouped_gemm_w16_dw_workspace_bytes(R, E, N, K)
         if size:
@@ -1057,7 +1064,7 @@ def moe_rmsnorm_add_grad(dy, s, weight, eps: float, ds=None, out_dtype: int = No
     dweight = _out(dweight, (H,), out_dtype, dev, "dweight", stream)
     lib, size = load(), 0
     if workspace is not None:
-        size, = _need(workspace, _U8, (None,), "workspace", dev)
+        size, = _need(workspace, _U8, (...,), "workspace", dev)
     else:
         size = lib.moe_rmsnorm_add_grad_workspace_bytes(T, H)
         if size:

@@ -85,3 +85,33 @@ def test_python_refuses_before_the_library():
                  lambda: moe.moe_ffn_few_w16(x, x, x, x, 1), lambda: moe.moe_ffn_few_w8a16(x, x, x, x, x, x, 1)):
         with pytest.raises(ValueError):
             call()
+
+
+class _Sized:
+    """What the binding looks at of a GPU tensor: sizes that a C int does not hold need more memory than a test should take."""
+    is_cuda, device = True, torch.device("cuda", 0)
+
+    def __init__(self, *shape, dtype=torch.bfloat16):
+        self.shape, self.dtype = shape, dtype
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        raise AssertionError("the call went on")
+
+
+def test_sizes_past_a_c_int_are_refused():
+    """2^32 + 8 rows would reach the library as 8, whose results would pass for all."""
+    n, w = (1 << 32) + 8, _Sized(64)
+    tall, wide, half = _Sized(n, 64), _Sized(1, (1 << 32) + 64), _Sized(1 << 31, 64)
+    many = _Sized(1, n, 64), _Sized(1, 64, n // 2)
+    q, s = _Sized(n, 64, dtype=torch.int8), _Sized(n, dtype=torch.float32)
+    logits = _Sized(1, 1, dtype=torch.float32)
+    for call in (lambda: moe.moe_rmsnorm_add(tall, w, 1e-6), lambda: moe.moe_rmsnorm_add(wide, _Sized(wide.shape[1]), 1e-6),
+                 lambda: moe.moe_rmsnorm_add(half, w, 1e-6), lambda: moe.moe_rmsnorm_add_grad(tall, tall, w, 1e-6),
+                 lambda: moe.moe_ffn_few_w16(_Sized(1, 64), logits, *many, 1), lambda: moe.moe_ffn_few_w16(wide, logits, *many, 1),
+                 lambda: moe.moe_ffn_few_w8a16(_Sized(1, 64), logits, _Sized(n, 128, 64, dtype=torch.int8), s, q, s, 1),
+                 lambda: moe.moe_i8_quantize(tall), lambda: moe.moe_silu_mul(tall), lambda: moe.moe_gemm_i8(q, s, q, s)):
+        with pytest.raises(ValueError, match="at most 2147483647"):
+            call()
