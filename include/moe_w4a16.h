@@ -802,7 +802,7 @@ moe_status_t moe_rmsnorm_add_grad(const void* dy, const void* s, int32_t dtype, 
  * routing (NULL = skip).  workspace: at least moe_ffn_few_workspace_bytes(T, H, I, E, k) bytes, of one call at a time.
  * (Where H <= 1024 and the experts' contraction is long, a third, small launch adds what workgroups share.)
  * Where T * H passes 65536 the tokens are taken in groups that do not, each with its own launches (and its own reading
- * of the weights).
+ * of the weights: the layers of any size are faster there).
  * Shapes: 0 <= T <= MOE_FEW_MAX_TOKENS, 1 <= k <= min(E, MOE_FEW_MAX_K), E <= MOE_MAX_EXPERTS, H and I multiples of
  * 16, 16 <= H <= 65536, 16 <= I <= MOE_I8_MAX_K, one expert's gate_up weights below 4 GiB.  Alignment: x, weights, y and
  * workspace 16 bytes, the others 4.

@@ -17,15 +17,17 @@
 //            columns of y make a workgroup, as many as deal H evenly to the CUs.  A workgroup sees every chosen expert, so
 //            the weighted sum over a token's experts is its own, in the order of the slots.  Only where H is small, and the
 //            contraction long, do workgroups share columns: a third launch then adds their parts.
-// h stays in two bf16 parts (value, and what its rounding left), for about 16 significant bits: the traffic of h is small
-// beside the weights', and y is then rounded once.  Sums are fp32.
+// h stays in two bf16 parts (value, and what its rounding left), for about 16 significant bits: what the matrix instruction takes
+// beside bf16 weights, in the bytes of an fp32.  Of 16384 y of 8 tokens 40 come out as the second nearest bf16 (8 in an fp32 form), which
+// adds 4e-7 of itself to y's distance from 64 bits, 1.687e-3; a third part would cost half as many matrix instructions, and half of h's
+// LDS, again.  y is rounded once.  Sums are fp32.
 //
 // Measured, both launches and the weights' rate (a large copy reads and writes at 5.2 TB/s here, a sum reads at 4.0):
 //   16 tokens, 8 experts of 4096 x 14336, bf16      474-493 us, 5.7 TB/s     (324 gate_up, 164 down)
-//   8 tokens, 128 experts top-8, 2048 x 768, bf16    89 us, 5.4 TB/s         (58, 29)
-//   16 tokens, 256 experts top-8, 2048 x 512, int8   73 us, 4.4 TB/s         (47, 23)
+//   8 tokens, 128 experts top-8, 2048 x 768, bf16    89 us, 5.5 TB/s         (58, 30)
+//   16 tokens, 256 experts top-8, 2048 x 512, int8   72 us, 4.4 TB/s         (47, 23)
 //   one token, 128 experts top-8, 2048 x 768         20 us bf16, 15 us int8  (12, 7.4 and 9.3, 6.6)
-//   11 tokens, 60 experts top-6, 1040 x 336, int8    21 us                   (12.6, 8.5)
+//   11 tokens, 60 experts top-6, 1040 x 336, int8    21 us                   (13, 8.7)
 // The last two are latency: 3 us until a workgroup knows the experts (6 for 16 tokens), about 2 us a round trip to memory, and
 // the border between the launches.
 #include <algorithm>

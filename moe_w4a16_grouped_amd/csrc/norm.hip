@@ -10,13 +10,13 @@
 //     scale = max |z| r / top, rounded to fp32 once
 // The codes do not depend on r, nor on the order in which anything is added: z is exact in 64 bits (at most 24 + 11
 // significant bits), and of a quotient next to a border between two codes the exact products top z and border max |z|
-// are compared.  Squares are added by fours in fp32 and the rest in 64 bits; rows that leave
-// the middle of fp32's range go through 64 bits altogether, which no 16-bit value overflows.
+// are compared.  Squares are added by fours in fp32 and the rest in 64 bits; rows whose squares or products leave
+// the middle of fp32's range go through 64 bits once more, which no 16-bit value overflows.
 //
 // Bound by memory: a row is read once, held in registers between its sums and its outputs, and s, y, codes and scales are
-// written from there.  8191 x 4096 with a residual to FP8 55 us (302 MB, 5.5 TB/s; 50 % of the issue slots are the vector
-// unit's, and a large addition of two tensors runs at 6.3 TB/s); 801 x 2048 to int8 4.3 us, one row 2.2 us (from Python 8.9 and
-// 11 us: the call's checks, outputs and launch).  The gradient of 8191 x 4096 with ds 48.5 + 4 us (268 MB, 5.5 TB/s).
+// written from there.  8191 x 4096 with a residual to FP8 54 to 58 us, box by box (302 MB, 5.6 TB/s; 48 % of the issue slots are the vector
+// unit's, and a large addition of two tensors runs at 6.3 TB/s); 801 x 2048 to int8 4.3 us, one row 2.2 us (from Python 9 to 10 and
+// 11 to 13 us: the call's checks, outputs and launch).  The gradient of 8191 x 4096 with ds 48.5 + 4 us (268 MB, 5.5 TB/s).
 #include <algorithm>
 
 #include "launch.h"
@@ -284,8 +284,8 @@ __device__ __forceinline__ u32x2 norm_codes8(const float (&s)[8], const float (&
   return some ? c : u32x2{0u, 0u};
 }
 
-// A chunk's outputs.  All stores of this kernel go past the L2, which they would only clear of rows to be read (5000 x 4096 to FP8
-// 32.2 us against 35.5, 4096 x 2048 15.2 against 16.8, 8191 x 4096 55.9 against 57.6, 801 x 2048 4.5 both ways).
+// A chunk's outputs.  All stores of this kernel go past the L2, which they would only clear of rows to be read (to FP8 with a
+// residual: 5000 x 4096 36.8 us against 39.7, 4096 x 2048 14.5 against 16.1, 8191 x 4096 58.1 against 59.9; 801 x 2048 to int8 4.5 both ways).
 template <bool F16, bool WF32, int QUANT>
 __device__ __forceinline__ void norm_store(const NormArgs& p, const u32x4& sv, const u32x4 (&wv)[WF32 ? 2 : 1], float r,
                                            double zmax, bool some, bool quick, size_t at) {
@@ -453,7 +453,9 @@ hipError_t launch_rmsnorm(const NormArgs& p, bool f16, bool w_f32, int quant, hi
 //   dx = r g - xhat (r^2 mean(g s)) (+ ds),   dw = sum over the rows of dy xhat.
 // r is formed again from s, which has to be read anyway.  A workgroup takes every nwg-th row, a thread the same columns of
 // each, so that the weight's gradient stays in its registers; the next row is asked for before the current one's sums
-// meet.  The workgroups' sums of rows go to the workspace and are added in the order of the workgroups.
+// meet.  The workgroups' sums of rows go to the workspace and are added in the order of the workgroups.  Rows past 4096 columns are
+// farther from their bytes: one workgroup of 1024 threads a CU, with threads that have no columns, and a barrier a row (2023 x 5192
+// 24 us, its bytes 16; 2048 x 16384 90 us, 52; 4096 x 8192 57 us, 52).
 // TH threads a row (64: a wave, four rows a workgroup, whose sums meet in LDS before they are written).
 // A sum in fp32 takes at most kGradRows rows; then it is a part of its own, and the parts are added in 64 bits (100000 x 8192 1211 us,
 // 1196 with one part a workgroup; twice the workgroups instead, of half the rows each, do not walk the rows side by side: 1253).
